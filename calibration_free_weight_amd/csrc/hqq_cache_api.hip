@@ -1,0 +1,302 @@
+// hqq_cache_api.hip -- the C entry points of the quantized key/value cache: argument checks,
+// the workspace plan of attention, and the launch sequences.
+#include <cmath>
+
+#include "hqq.h"
+#include "hqq_cache_internal.h"
+#include "hqq_internal.h"
+
+namespace {
+
+hqq_status refuse(const char *msg, hqq_status st = HQQ_ERR_ARG)
+{
+    hqq::report_error(st, msg);
+    return st;
+}
+
+hqq_status done(hipError_t e)
+{
+    if (e != hipSuccess) return refuse(hipGetErrorString(e), HQQ_ERR_DEVICE);
+    hqq::report_error(HQQ_OK, "");
+    return HQQ_OK;
+}
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+hqq_status check_cache(const hqq_cache *c)
+{
+    if (!c) return refuse("cache must be non-null");
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return refuse("cache: head_dim must be 64, 128 or 256");
+    if (c->nbits != 4 && c->nbits != 8) return refuse("cache: nbits must be 4 or 8");
+    if ((c->group_size != 32 && c->group_size != 64 && c->group_size != 128) || c->group_size > c->head_dim)
+        return refuse("cache: group_size must be 32, 64 or 128 and at most head_dim");
+    if (c->dtype != HQQ_F16 && c->dtype != HQQ_BF16) return refuse("cache: dtype must be HQQ_F16 or HQQ_BF16");
+    if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+        return refuse("cache: page_size must be a power of two in [16, 4096]");
+    if (c->n_heads < 1 || c->n_heads > 1024) return refuse("cache: n_heads must be in [1, 1024]");
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX) return refuse("cache: n_pages must be in [1, 2^31 - 1]");
+    if (!c->k_codes || !c->v_codes || !c->k_meta || !c->v_meta)
+        return refuse("cache: k_codes, v_codes, k_meta and v_meta must be non-null");
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_meta, 16) || !aligned(c->v_meta, 16))
+        return refuse("cache: k_codes, v_codes, k_meta and v_meta must be 16-byte aligned");
+    return HQQ_OK;
+}
+
+hqq_status check_seqs(const hqq_cache *c, const hqq_seqs *s)
+{
+    if (!s) return refuse("seqs must be non-null");
+    if (s->n_seqs < 0 || s->n_seqs > hqq::kMaxSeqs) return refuse("seqs: n_seqs must be in [0, 4096]");
+    if (s->n_tokens < 0 || s->n_tokens > (1 << 24)) return refuse("seqs: n_tokens must be in [0, 2^24]");
+    if (s->n_tokens * c->n_heads > INT32_MAX) return refuse("seqs: n_tokens * n_heads must be below 2^31");
+    if (s->max_pages < 0 || (int64_t)s->max_pages * c->page_size > INT32_MAX)
+        return refuse("seqs: max_pages * page_size must be in [0, 2^31)");
+    if (s->n_seqs == 0 || s->n_tokens == 0) return HQQ_OK;
+    if ((!s->table && s->max_pages > 0) || !s->lens) return refuse("seqs: table and lens must be non-null");
+    if (!aligned(s->table, 4) || !aligned(s->lens, 4) || !aligned(s->cu_tokens, 4))
+        return refuse("seqs: table, lens and cu_tokens must be 4-byte aligned");
+    if (!s->cu_tokens && s->n_tokens % s->n_seqs != 0)
+        return refuse("seqs: n_tokens must be a multiple of n_seqs without cu_tokens");
+    return HQQ_OK;
+}
+
+// A tensor of rows: non-null, 16-byte rows.
+hqq_status check_rows(const void *p, int64_t ts, int64_t hs, const char *null, const char *shape)
+{
+    if (!p) return refuse(null);
+    if (!aligned(p, 16) || ts < 0 || hs < 0 || ts % 8 || hs % 8 || ts > (int64_t(1) << 36) ||
+        hs > (int64_t(1) << 36))
+        return refuse(shape);
+    return HQQ_OK;
+}
+
+int log2_of(int x)
+{
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+hqq::CacheView view_of(const hqq_cache *c)
+{
+    return hqq::CacheView{static_cast<uint8_t *>(c->k_codes), static_cast<uint8_t *>(c->v_codes),
+                          static_cast<uint32_t *>(c->k_meta), static_cast<uint32_t *>(c->v_meta), c->n_heads};
+}
+
+hqq::SeqView view_of(const hqq_cache *c, const hqq_seqs *s)
+{
+    return hqq::SeqView{s->table,     s->lens, s->cu_tokens,         s->n_seqs,      s->max_pages, (int32_t)s->n_tokens, -1,
+                        log2_of(c->page_size), (int32_t)c->n_pages};
+}
+
+hqq_status cache_rows(bool write, const hqq_cache *cache, const hqq_seqs *seqs, const void *k, int64_t k_ts,
+                      int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs, void *stream)
+{
+    hqq_status st = check_cache(cache);
+    if (st == HQQ_OK) st = check_seqs(cache, seqs);
+    if (st != HQQ_OK) return st;
+    if (seqs->n_seqs == 0 || seqs->n_tokens == 0) return done(hipSuccess);
+    const char *null = "k and v must be non-null";
+    const char *shape = "k and v must be 16-byte aligned, with strides that are multiples of 8 in [0, 2^36]";
+    st = check_rows(k, k_ts, k_hs, null, shape);
+    if (st == HQQ_OK) st = check_rows(v, v_ts, v_hs, null, shape);
+    if (st != HQQ_OK) return st;
+    auto rows = [](const void *p) { return static_cast<uint16_t *>(const_cast<void *>(p)); };
+    const hqq::RowPtrs p{rows(k), rows(v), k_ts, k_hs, v_ts, v_hs};
+    return done(hqq::launch_cache_rows(write, view_of(cache), view_of(cache, seqs), p, cache->head_dim,
+                                       cache->nbits, cache->group_size, cache->dtype == HQQ_BF16,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+// ---- attention --------------------------------------------------------------------------------
+// How one side's work is cut, and where its partial results lie in the workspace.
+struct SidePlan {
+    int tiles16, workers;
+    size_t starts, slot_o, slot_ml, row_o, row_ml;      // offsets; row_* only with a prefix
+};
+
+struct Plan {
+    SidePlan own, prefix;
+    size_t bytes;
+};
+
+// Query rows to a tile: 16 where a sequence has no more, for its work is to read the cache;
+// up to 64 (32 for 256-wide heads, whose sums fill the registers) so that each code read and
+// widened meets more rows.
+int tiles_for(int64_t rows, int dim)
+{
+    const int t = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+    return dim == 256 && t > 2 ? 2 : t;
+}
+
+// Blocks of a launch: what the 256 CUs hold at once.
+int workers_for(int tiles16, int heads)
+{
+    const int blocks = tiles16 == 1 ? 1024 : 512;
+    return (blocks + heads - 1) / heads;
+}
+
+Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefix_len)
+{
+    const int per = n_q_heads / c->n_heads;
+    const int64_t rows = s->n_tokens * per;
+    Plan p{};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t was = at;
+        at += (n + 255) / 256 * 256;
+        return was;
+    };
+    auto side = [&](int64_t tile_rows, int n_seqs, bool keep_rows) {
+        SidePlan x{};
+        x.tiles16 = tiles_for(tile_rows, c->head_dim);
+        x.workers = workers_for(x.tiles16, c->n_heads);
+        const size_t slots = (size_t)c->n_heads * 2 * x.workers * 16 * x.tiles16;
+        x.starts = take(4 * ((size_t)n_seqs + 1));
+        x.slot_o = take(slots * c->head_dim * 4);
+        x.slot_ml = take(slots * 8);
+        if (keep_rows) {
+            x.row_o = take((size_t)c->n_heads * rows * c->head_dim * 4);
+            x.row_ml = take((size_t)c->n_heads * rows * 8);
+        }
+        return x;
+    };
+    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, prefix_len > 0);
+    if (prefix_len > 0) p.prefix = side(rows, 1, true);
+    p.bytes = at;
+    return p;
+}
+
+// Checks that the sizes allow a plan; HQQ_OK with *empty set when there is nothing to do.
+hqq_status check_plan(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefix_len, bool *empty)
+{
+    hqq_status st = check_cache(c);
+    if (st == HQQ_OK) st = check_seqs(c, s);
+    if (st != HQQ_OK) return st;
+    if (n_q_heads < 1 || n_q_heads % c->n_heads != 0)
+        return refuse("n_q_heads must be a positive multiple of the cache's n_heads");
+    if (s->n_tokens * n_q_heads > INT32_MAX || n_q_heads > (1 << 20))
+        return refuse("n_tokens * n_q_heads must be below 2^31");
+    if (prefix_len < 0 || prefix_len > INT32_MAX) return refuse("prefix_len must be in [0, 2^31)");
+    *empty = s->n_seqs == 0 || s->n_tokens == 0;
+    if (*empty) return HQQ_OK;
+    // units of work are counted in 32 bits
+    const int64_t tiles = s->n_tokens * (n_q_heads / c->n_heads) / 16 + s->n_seqs;
+    const int64_t longest = (int64_t)s->max_pages * c->page_size;
+    const int64_t far = longest > prefix_len ? longest : prefix_len;
+    if (tiles > INT32_MAX / (far / hqq::kUnit + 1))
+        return refuse("too many rows over too long sequences for one call", HQQ_ERR_UNSUPPORTED);
+    return HQQ_OK;
+}
+
+hqq::AttnSide side_at(const SidePlan &p, char *ws, bool keep_rows)
+{
+    auto f = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+    return hqq::AttnSide{reinterpret_cast<int32_t *>(ws + p.starts), f(p.slot_o), f(p.slot_ml),
+                         keep_rows ? f(p.row_o) : nullptr, keep_rows ? f(p.row_ml) : nullptr,
+                         p.workers, p.tiles16};
+}
+
+}  // namespace
+
+extern "C" {
+
+hqq_status hqq_cache_write(const hqq_cache *cache, const hqq_seqs *seqs, const void *k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                           void *stream)
+{
+    return cache_rows(true, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
+}
+
+hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k, int64_t k_token_stride,
+                          int64_t k_head_stride, void *v, int64_t v_token_stride, int64_t v_head_stride,
+                          void *stream)
+{
+    return cache_rows(false, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
+}
+
+size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs, int n_q_heads, int64_t prefix_len)
+{
+    bool empty;
+    if (check_plan(cache, seqs, n_q_heads, prefix_len, &empty) != HQQ_OK) return 0;
+    hqq::report_error(HQQ_OK, "");
+    return empty ? 0 : plan_of(cache, seqs, n_q_heads, prefix_len).bytes;
+}
+
+hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *seqs, const int32_t *prefix_pages,
+                                      int n_prefix_pages, int64_t prefix_len, const void *q, int64_t q_token_stride,
+                                      int64_t q_head_stride, int n_q_heads, float scale, void *out,
+                                      int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream)
+{
+    bool empty;
+    hqq_status st = check_plan(cache, seqs, n_q_heads, prefix_len, &empty);
+    if (st != HQQ_OK) return st;
+    if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * cache->page_size > INT32_MAX ||
+        prefix_len > (int64_t)n_prefix_pages * cache->page_size)
+        return refuse("prefix_len must be at most n_prefix_pages * page_size, and that below 2^31");
+    if (prefix_len > 0 && (!prefix_pages || !aligned(prefix_pages, 4)))
+        return refuse("prefix_pages must be non-null and 4-byte aligned");
+    if (!std::isfinite(scale)) return refuse("scale must be finite");
+    if (empty) return done(hipSuccess);
+    st = check_rows(q, q_token_stride, q_head_stride, "q must be non-null",
+                    "q must be 16-byte aligned, with strides that are multiples of 8 in [0, 2^36]");
+    if (st == HQQ_OK)
+        st = check_rows(out, out_token_stride, out_head_stride, "out must be non-null",
+                        "out must be 16-byte aligned, with strides that are multiples of 8 in [0, 2^36]");
+    if (st != HQQ_OK) return st;
+    if (lse && !aligned(lse, 4)) return refuse("lse must be 4-byte aligned");
+    const Plan p = plan_of(cache, seqs, n_q_heads, prefix_len);
+    if (!workspace || workspace_bytes < p.bytes)
+        return refuse("workspace missing or smaller than hqq_cache_attention_workspace()", HQQ_ERR_WORKSPACE);
+    if (!aligned(workspace, 256)) return refuse("workspace must be 256-byte aligned");
+    char *ws = static_cast<char *>(workspace);
+    const bool shared = prefix_len > 0;
+    const hipStream_t str = static_cast<hipStream_t>(stream);
+    const hqq::AttnShape shape{cache->head_dim, cache->nbits, cache->group_size, cache->dtype == HQQ_BF16};
+    hqq::AttnArgs a{};
+    a.c = view_of(cache);
+    a.s = view_of(cache, seqs);
+    a.side = side_at(p.own, ws, shared);
+    a.q = static_cast<const uint16_t *>(q);
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.q_ts = q_token_stride;
+    a.q_hs = q_head_stride;
+    a.o_ts = out_token_stride;
+    a.o_hs = out_head_stride;
+    a.per = n_q_heads / cache->n_heads;
+    a.causal = 1;
+    a.scale = scale * 1.44269504088896341f;
+    hqq::JoinArgs j{a.s, a.side, {}, a.out, lse, a.o_ts, a.o_hs, a.per, cache->n_heads, cache->head_dim, 0};
+    if (shared) {
+        // the prefix is one sequence whose rows are all rows of the call
+        hqq::AttnArgs b = a;
+        b.s.table = prefix_pages;
+        b.s.lens = nullptr;
+        b.s.cu = nullptr;
+        b.s.n_seqs = 1;
+        b.s.max_pages = n_prefix_pages;
+        b.s.fixed_len = (int32_t)prefix_len;
+        b.side = side_at(p.prefix, ws, true);
+        b.causal = 0;
+        j.prefix = b.side;
+        j.prefix_len = b.s.fixed_len;
+        const hipError_t e = hqq::launch_attn(b, shape, str);
+        if (e != hipSuccess) return done(e);
+    }
+    hipError_t e = hqq::launch_attn(a, shape, str);
+    if (e == hipSuccess) e = hqq::launch_join(j, shape.bf16, str);
+    return done(e);
+}
+
+hqq_status hqq_cache_attention(const hqq_cache *cache, const hqq_seqs *seqs, const void *q, int64_t q_token_stride,
+                               int64_t q_head_stride, int n_q_heads, float scale, void *out,
+                               int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    return hqq_cache_attention_prefix(cache, seqs, nullptr, 0, 0, q, q_token_stride, q_head_stride, n_q_heads, scale,
+                                      out, out_token_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

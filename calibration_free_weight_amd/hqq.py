@@ -14,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libhqq.so")
 
 HQQ_OK, HQQ_ERR_ARG, HQQ_ERR_UNSUPPORTED, HQQ_ERR_WORKSPACE, HQQ_ERR_DEVICE = range(5)
+HQQ_F16, HQQ_BF16 = range(2)
 
 # Functions declared in include/hqq.h (checked by the tests against the header).
 EXPORTS = ("hqq_packed_bytes", "hqq_workspace_bytes", "hqq_quantize", "hqq_quantize_batch",
@@ -22,7 +23,8 @@ EXPORTS = ("hqq_packed_bytes", "hqq_workspace_bytes", "hqq_quantize", "hqq_quant
            "hqq_gemm_workspace_bytes", "hqq_gemm_f16", "hqq_requant_scales",
            "hqq_dequantize_scales", "hqq_pack", "hqq_unpack", "hqq_status_string",
            "hqq_last_error", "hqq_batch_check", "hqq_debug_solver", "hqq_quantize_noalloc",
-           "hqq_gemm_multi")
+           "hqq_gemm_multi", "hqq_cache_write", "hqq_cache_read", "hqq_cache_attention",
+           "hqq_cache_attention_prefix", "hqq_cache_attention_workspace")
 
 
 class HQQError(RuntimeError):
@@ -44,6 +46,18 @@ class hqq_gemm_weight(C.Structure):
     _fields_ = [("packed", C.c_void_p), ("scale", C.c_void_p), ("zero", C.c_void_p),
                 ("zero_meta", C.c_void_p), ("N", C.c_int64), ("nbits", C.c_int),
                 ("group_size", C.c_int), ("zero_bits", C.c_int), ("Y", C.c_void_p)]
+
+
+class hqq_cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_meta", C.c_void_p),
+                ("v_meta", C.c_void_p), ("n_pages", C.c_int64), ("page_size", C.c_int),
+                ("n_heads", C.c_int), ("head_dim", C.c_int), ("nbits", C.c_int),
+                ("group_size", C.c_int), ("dtype", C.c_int)]
+
+
+class hqq_seqs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("lens", C.c_void_p), ("cu_tokens", C.c_void_p),
+                ("n_seqs", C.c_int), ("max_pages", C.c_int), ("n_tokens", C.c_int64)]
 
 
 _L = None
@@ -98,6 +112,17 @@ def lib():
         L.hqq_pack.argtypes = [vp, i64, i32, vp, vp]
         L.hqq_unpack.restype = i32
         L.hqq_unpack.argtypes = [vp, i64, i32, vp, vp]
+        cp, sp, st = C.POINTER(hqq_cache), C.POINTER(hqq_seqs), C.c_size_t
+        for name in ("hqq_cache_write", "hqq_cache_read"):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = [cp, sp, vp, i64, i64, vp, i64, i64, vp]
+        L.hqq_cache_attention.restype = i32
+        L.hqq_cache_attention.argtypes = [cp, sp, vp, i64, i64, i32, f32, vp, i64, i64, vp, vp, st, vp]
+        L.hqq_cache_attention_prefix.restype = i32
+        L.hqq_cache_attention_prefix.argtypes = [cp, sp, vp, i32, i64, vp, i64, i64, i32, f32, vp,
+                                                 i64, i64, vp, vp, st, vp]
+        L.hqq_cache_attention_workspace.restype = st
+        L.hqq_cache_attention_workspace.argtypes = [cp, sp, i32, i64]
         L.hqq_status_string.restype = C.c_char_p
         L.hqq_status_string.argtypes = [i32]
         L.hqq_last_error.restype = C.c_char_p
@@ -291,6 +316,202 @@ def hqq_pack(codes, n_codes, nbits, packed, stream=None) -> None:
 
 def hqq_unpack(packed, n_codes, nbits, codes, stream=None) -> None:
     _check(lib().hqq_unpack(_p(packed), n_codes, nbits, _p(codes), _stream(stream)))
+
+
+# ---- the quantized key/value cache ------------------------------------------------------------
+# A cache is a dict of its four tensors and sizes (alloc_cache makes one): k_codes and v_codes,
+# uint8 [n_pages, n_heads, page_size*head_dim*nbits/8], k_meta and v_meta, [n_pages, n_heads,
+# page_size, head_dim/group_size, 2] of the type of the rows, page_size, n_heads, head_dim,
+# nbits, group_size. table: int32 [n_seqs, max_pages]; lens: int32 [n_seqs]; cu_tokens: int32
+# [n_seqs + 1] or None. Rows are [n_tokens, heads, head_dim] with contiguous dimensions. The
+# calls run on the current stream of the cache's device unless `stream` is given.
+def _require(ok, msg):
+    if not ok:
+        raise HQQError(HQQ_ERR_ARG, msg)
+
+
+def _cache_struct(cache):
+    import torch
+    kc, vc, km, vm = (cache[x] for x in ("k_codes", "v_codes", "k_meta", "v_meta"))
+    page, heads, dim = cache["page_size"], cache["n_heads"], cache["head_dim"]
+    nbits, group = cache["nbits"], cache["group_size"]
+    n, dev, dtype = kc.shape[0], kc.device, km.dtype
+    codes, meta = (n, heads, page * dim * nbits // 8), (n, heads, page, dim // max(group, 1), 2)
+    _require(kc.shape == codes and vc.shape == codes and kc.dtype == vc.dtype == torch.uint8,
+             "k_codes and v_codes must be uint8 [n_pages, n_heads, page_size*head_dim*nbits/8]")
+    _require(km.shape == meta and vm.shape == meta and vm.dtype == dtype and
+             dtype in (torch.float16, torch.bfloat16),
+             "k_meta and v_meta must be [n_pages, n_heads, page_size, head_dim/group_size, 2] "
+             "of float16 or bfloat16")
+    _require(kc.is_contiguous() and vc.is_contiguous() and km.is_contiguous() and vm.is_contiguous(),
+             "the cache's tensors must be contiguous")
+    _require(kc.is_cuda and dev == vc.device == km.device == vm.device,
+             "the cache's tensors must be on one GPU")
+    return hqq_cache(kc.data_ptr(), vc.data_ptr(), km.data_ptr(), vm.data_ptr(), n, page, heads,
+                     dim, nbits, group, HQQ_BF16 if dtype == torch.bfloat16 else HQQ_F16), dev, dtype
+
+
+def _seqs_struct(table, lens, cu_tokens, n_tokens, dev):
+    import torch
+    _require(table.dim() == 2 and table.is_contiguous() and table.dtype == torch.int32 and table.device == dev,
+             "table must be a contiguous int32 [n_seqs, max_pages] on the cache's device")
+    n = table.shape[0]
+    _require(lens.shape == (n,) and lens.dtype == torch.int32 and lens.is_contiguous() and lens.device == dev,
+             "lens must be a contiguous int32 [n_seqs] on the cache's device")
+    if cu_tokens is not None:
+        _require(cu_tokens.shape == (n + 1,) and cu_tokens.dtype == torch.int32 and
+                 cu_tokens.is_contiguous() and cu_tokens.device == dev,
+                 "cu_tokens must be a contiguous int32 [n_seqs + 1] on the cache's device")
+    return hqq_seqs(table.data_ptr(), lens.data_ptr(), None if cu_tokens is None else cu_tokens.data_ptr(),
+                    n, table.shape[1], n_tokens)
+
+
+def _rows(x, n_tokens, heads, dim, dev, dtype, name):
+    shape = x.shape
+    _require(len(shape) == 3 and shape[0] == n_tokens and (heads is None or shape[1] == heads) and
+             shape[2] == dim and x.stride(2) == 1 and x.dtype == dtype and x.device == dev,
+             f"{name} must be [n_tokens, heads, head_dim] with contiguous dimensions, of the "
+             "cache's type and device")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+class _on:
+    """Makes a device current for a call, where it is not; gives the call's stream."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self.guard = None
+        if torch.cuda.current_device() != dev.index:
+            self.guard = torch.cuda.device(dev)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return C.c_void_p(int(self.stream))
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _cache_rows(fn, cache, table, lens, k, v, cu_tokens, stream):
+    c, dev, dtype = _cache_struct(cache)
+    n = k.shape[0]
+    s = _seqs_struct(table, lens, cu_tokens, n, dev)
+    kr = _rows(k, n, c.n_heads, c.head_dim, dev, dtype, "k")
+    vr = _rows(v, n, c.n_heads, c.head_dim, dev, dtype, "v")
+    with _on(dev, stream) as st:
+        _check(fn(C.byref(c), C.byref(s), *kr, *vr, st))
+
+
+def hqq_cache_write(cache, table, lens, k, v, cu_tokens=None, stream=None) -> None:
+    """Quantize k and v [n_tokens, n_heads, head_dim] into the cache as the last tokens of
+    their sequences (lens counts them)."""
+    _cache_rows(lib().hqq_cache_write, cache, table, lens, k, v, cu_tokens, stream)
+
+
+def hqq_cache_read(cache, table, lens, k, v, cu_tokens=None, stream=None) -> None:
+    """Fill k and v with what the cache holds of the last tokens of the sequences."""
+    _cache_rows(lib().hqq_cache_read, cache, table, lens, k, v, cu_tokens, stream)
+
+
+def _attention_args(cache, table, lens, q, cu_tokens):
+    c, dev, dtype = _cache_struct(cache)
+    s = _seqs_struct(table, lens, cu_tokens, q.shape[0], dev)
+    return c, s, _rows(q, q.shape[0], None, c.head_dim, dev, dtype, "q"), dev, dtype
+
+
+def hqq_cache_attention_workspace(cache, table, lens, n_tokens, n_q_heads, prefix_len=0, cu_tokens=None) -> int:
+    """Workspace bytes of an attention call of these sizes."""
+    c, dev, _ = _cache_struct(cache)
+    s = _seqs_struct(table, lens, cu_tokens, n_tokens, dev)
+    n = int(lib().hqq_cache_attention_workspace(C.byref(c), C.byref(s), n_q_heads, prefix_len))
+    if n == 0 and hqq_last_error():
+        raise HQQError(HQQ_ERR_ARG, hqq_last_error())
+    return n
+
+
+def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream):
+    import torch
+    c, s, qr, dev, dtype = _attention_args(cache, table, lens, q, cu_tokens)
+    n, heads, dim = q.shape
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=dtype, device=dev)
+    orow = _rows(out, n, heads, dim, dev, dtype, "out")
+    if lse is not None:
+        _require(lse.shape == (n, heads) and lse.dtype == torch.float32 and lse.is_contiguous() and
+                 lse.device == dev, "lse must be a contiguous float32 [n_tokens, n_q_heads]")
+    pages, n_pages = None, 0
+    if prefix_pages is not None:
+        _require(prefix_pages.dim() == 1 and prefix_pages.dtype == torch.int32 and
+                 prefix_pages.is_contiguous() and prefix_pages.device == dev,
+                 "prefix_pages must be a contiguous int32 vector on the cache's device")
+        pages, n_pages = prefix_pages.data_ptr(), prefix_pages.shape[0]
+    L = lib()
+    with _on(dev, stream) as st:
+        if workspace is None:
+            # from the allocator's pool of the stream that the call runs on
+            need = int(L.hqq_cache_attention_workspace(C.byref(c), C.byref(s), heads, prefix_len))
+            own = stream is None or int(stream) == torch.cuda.current_stream(dev).cuda_stream
+            with torch.cuda.stream(None if own else torch.cuda.ExternalStream(int(stream), device=dev)):
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _check(L.hqq_cache_attention_prefix(
+            C.byref(c), C.byref(s), pages, n_pages, prefix_len, *qr, heads,
+            dim ** -0.5 if scale is None else scale, *orow, _p(lse), _p(workspace),
+            workspace.numel() * workspace.element_size(), st))
+    return out
+
+
+def hqq_cache_attention(cache, table, lens, q, out, lse=None, scale=None, cu_tokens=None,
+                        workspace=None, stream=None) -> None:
+    """out = attention of q [n_tokens, n_q_heads, head_dim] over the cache: the row at position
+    x of its sequence sees positions 0..x. scale: head_dim ** -0.5 unless given. workspace: a
+    tensor of hqq_cache_attention_workspace() bytes, allocated when None."""
+    _attention(cache, table, lens, None, 0, q, out, lse, scale, cu_tokens, workspace, stream)
+
+
+def hqq_cache_attention_prefix(cache, table, lens, prefix_pages, prefix_len, q, out, lse=None, scale=None,
+                               cu_tokens=None, workspace=None, stream=None) -> None:
+    """hqq_cache_attention for sequences that share a prefix of prefix_len tokens, held once in
+    prefix_pages (int32 [n]); table and lens are those of what follows it."""
+    _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream)
+
+
+def alloc_cache(n_pages, page_size, n_heads, head_dim, nbits=4, group_size=64, dtype=None, device="cuda"):
+    """An empty cache (a dict, see above); its tensors' contents are of no meaning until written."""
+    import torch
+    dtype = torch.float16 if dtype is None else dtype
+    codes = (n_pages, n_heads, page_size * head_dim * nbits // 8)
+    meta = (n_pages, n_heads, page_size, head_dim // group_size, 2)
+    return dict(k_codes=torch.empty(codes, dtype=torch.uint8, device=device),
+                v_codes=torch.empty(codes, dtype=torch.uint8, device=device),
+                k_meta=torch.empty(meta, dtype=dtype, device=device),
+                v_meta=torch.empty(meta, dtype=dtype, device=device),
+                page_size=page_size, n_heads=n_heads, head_dim=head_dim, nbits=nbits,
+                group_size=group_size)
+
+
+def cache_read(cache, table, lens, n_tokens, cu_tokens=None, stream=None):
+    """Allocate and fill (k, v) for the last tokens of the sequences, n_tokens in all."""
+    import torch
+    km = cache["k_meta"]
+    shape = (n_tokens, cache["n_heads"], cache["head_dim"])
+    k = torch.empty(shape, dtype=km.dtype, device=km.device)
+    v = torch.empty(shape, dtype=km.dtype, device=km.device)
+    hqq_cache_read(cache, table, lens, k, v, cu_tokens, stream)
+    return k, v
+
+
+def cache_attention(cache, table, lens, q, cu_tokens=None, scale=None, lse=None, stream=None):
+    """Allocate the output and call hqq_cache_attention."""
+    return _attention(cache, table, lens, None, 0, q, None, lse, scale, cu_tokens, None, stream)
+
+
+def cache_attention_prefix(cache, table, lens, prefix_pages, prefix_len, q, cu_tokens=None, scale=None,
+                           lse=None, stream=None):
+    """Allocate the output and call hqq_cache_attention_prefix."""
+    return _attention(cache, table, lens, prefix_pages, prefix_len, q, None, lse, scale, cu_tokens, None, stream)
 
 
 # ---- allocation helpers (PyTorch device memory for the outputs) -----------------------------

@@ -279,6 +279,122 @@ hqq_status hqq_gemm_multi(const void *X, int64_t M, int64_t K, const hqq_gemm_we
 hqq_status hqq_gemm_f16(const void *X, int64_t M, const void *Wr, int64_t N, int64_t K, void *Y,
                         void *stream);
 
+/* ---- The quantized key/value cache of one attention layer ------------------------------------
+ * The pages quantize a model's weights [SK "HQQLinear layer"]; while the model answers, the
+ * other large tensors it reads per token are the keys and values of what came before. These
+ * calls keep them as codes on min-max grids, the rule of the 8-bit scales and zeros below
+ * per group of a token's head, with no optimisation: a cache is written token by token.
+ *
+ * Grid. A head's vector of one token (head_dim values of type `dtype`) is cut into groups of
+ * group_size consecutive dimensions. With top = 2^nbits - 1, a group's values v become
+ *   base = min(v)
+ *   step = the smallest number of the type >= (max(v) - min(v)) / top; 0 if the range is 0;
+ *          with bfloat16 at least 2^-100 otherwise
+ *   q    = min(rne((v - base) / step), top), decided on the exact quotient,
+ * and read back as base + q * step, off by at most step / 2. (With binary16, where base +
+ * top * step would round to infinity, q stops at top - 1 and the error at step.) Values must
+ * be finite, and below 2^120 with bfloat16; a group that holds others reads back as
+ * unspecified values, other groups are not affected.
+ *
+ * Pages. Tokens lie in pages of page_size; a sequence's pages are listed in a table, so that
+ * sequences grow page by page and may share pages. Per page and head:
+ *   k_codes: per token, code e of unit (a, m) is dimension 32m + 8a + e; units in order
+ *            (a, m), a < 4, m < head_dim/32. A 4-bit unit is 4 bytes, byte i = code i |
+ *            code (i+4) << 4; an 8-bit unit is 8 bytes, byte e = code e.
+ *   v_codes: per block of four tokens, 16 rows r; a row holds its four tokens in turn, each
+ *            with codes i = 0 .. head_dim/16 - 1, code i = G*(g/16) + j for dimension
+ *            g*G + r*(g/16) + j (g = group_size, group G, j < g/16); byte k = code 2k |
+ *            code (2k+1) << 4 with 4 bits, byte i = code i with 8.
+ *   k_meta, v_meta: per token, head_dim/group_size pairs {step, base} of type `dtype`.
+ * This order is what the matrix instructions of hqq_cache_attention read with wide loads and
+ * no exchange between lanes. */
+typedef enum hqq_dtype {
+    HQQ_F16 = 0,             /* IEEE binary16                                             */
+    HQQ_BF16 = 1             /* bfloat16                                                  */
+} hqq_dtype;
+
+typedef struct hqq_cache {
+    void *k_codes, *v_codes; /* [n_pages][n_heads][page_size*head_dim*nbits/8] bytes, each */
+    void *k_meta, *v_meta;   /* [n_pages][n_heads][page_size][head_dim/group_size][2]      */
+                             /* all four 16-byte aligned                                   */
+    int64_t n_pages;         /* 1 .. 2^31 - 1                                              */
+    int page_size;           /* tokens per page: a power of two, 16..4096                  */
+    int n_heads;             /* key/value heads, 1..1024                                   */
+    int head_dim;            /* 64, 128 or 256                                             */
+    int nbits;               /* 4 or 8                                                     */
+    int group_size;          /* 32, 64 or 128, at most head_dim                            */
+    int dtype;               /* hqq_dtype of keys, values, queries, outputs and meta       */
+} hqq_cache;
+
+/* The tokens of a call and the sequences they belong to. The call's tokens are rows
+ * 0..n_tokens-1 of its tensors, one sequence after another: sequence b has rows
+ * cu_tokens[b] .. cu_tokens[b+1]-1, or n_tokens/n_seqs rows each when cu_tokens is NULL.
+ * They are the last tokens of their sequences: with n_b rows, row cu_tokens[b] + j is at
+ * position lens[b] - n_b + j of sequence b. All arrays are device memory, read by the
+ * kernels only; what they hold is not checked by the call, but no value in them makes a
+ * kernel leave its buffers: lengths count as 0..max_pages*page_size, rows outside the tensors
+ * do not exist, and a position whose table entry is not in [0, n_pages), or that is
+ * negative, is not in the cache (writes drop it, reads give zeros, attention does not see
+ * it). Rows behind cu_tokens[n_seqs] are not touched. cu_tokens must not decrease, and one
+ * position of the cache must not be written twice by a call, or its contents are
+ * unspecified. */
+typedef struct hqq_seqs {
+    const int32_t *table;    /* [n_seqs][max_pages]: pages of each sequence in order       */
+    const int32_t *lens;     /* [n_seqs]: tokens of each sequence, the call's included     */
+    const int32_t *cu_tokens;/* [n_seqs + 1], or NULL                                      */
+    int n_seqs;              /* 0..4096                                                    */
+    int max_pages;           /* max_pages * page_size < 2^31                               */
+    int64_t n_tokens;        /* rows of the call's tensors, 0..2^24                        */
+} hqq_seqs;
+
+/* Write the call's tokens into the cache: k and v are [n_tokens, n_heads, head_dim] with
+ * strides in elements between tokens and between heads (multiples of 8; dimensions are
+ * contiguous; pointers 16-byte aligned), e.g. slices of one fused projection's output. */
+hqq_status hqq_cache_write(const hqq_cache *cache, const hqq_seqs *seqs, const void *k,
+                           int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                           int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/* Read tokens back, the mirror of hqq_cache_write: k and v get base + q * step rounded once
+ * to the type, zeros for tokens that are not in the cache. With n_b = lens[b] the whole
+ * sequence is read. The heads of a token must not overlap, nor the tokens. */
+hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
+                          int64_t k_token_stride, int64_t k_head_stride, void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/* Attention of the call's tokens over the cache. q and out are [n_tokens, n_q_heads,
+ * head_dim] with strides as above; n_q_heads is a multiple of n_heads, and query head h
+ * reads key/value head h / (n_q_heads / n_heads). The row at position x of its sequence
+ * sees positions 0..x (which must be in the cache already: write, then attend):
+ *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * <q, k_t>),
+ * with k_t, v_t = base + q * step unrounded, scores, weights and sums in binary32 and out
+ * rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
+ * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. workspace: device,
+ * 256-byte aligned, at least hqq_cache_attention_workspace() bytes; calls that may run at the
+ * same time need one each. Results do not depend on what it held. */
+hqq_status hqq_cache_attention(const hqq_cache *cache, const hqq_seqs *seqs, const void *q,
+                               int64_t q_token_stride, int64_t q_head_stride, int n_q_heads,
+                               float scale, void *out, int64_t out_token_stride,
+                               int64_t out_head_stride, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* hqq_cache_attention for a batch whose sequences begin with the same prefix_len tokens: the
+ * pages prefix_pages (device, int32 [n_prefix_pages], in order, of the same cache) hold them
+ * once, and every row sees all of them before what it sees of its own sequence, whose
+ * positions and lens count behind the prefix. The prefix is read once for all rows.
+ * 0 <= prefix_len <= n_prefix_pages * page_size < 2^31; 0 is hqq_cache_attention. */
+hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *seqs,
+                                      const int32_t *prefix_pages, int n_prefix_pages,
+                                      int64_t prefix_len, const void *q, int64_t q_token_stride,
+                                      int64_t q_head_stride, int n_q_heads, float scale,
+                                      void *out, int64_t out_token_stride,
+                                      int64_t out_head_stride, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two attention calls for these sizes (prefix_len 0 for the first);
+ * a function of the sizes alone. 0 if the arguments are invalid: the call then says why. */
+size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs,
+                                     int n_q_heads, int64_t prefix_len);
+
 /* The bit-packing of the quantized weight W_q [SK "HQQLinear layer": W_q holds the packed
  * codes; bit widths 8/4/3/2/1 from its introduction], standalone: pack n_codes uint8 codes
  * (device, each < 2^nbits) into the layout under "Packed codes" above. `packed` (device,
