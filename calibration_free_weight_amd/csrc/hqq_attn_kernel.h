@@ -11,10 +11,13 @@
 //                      tiles of four tokens), the order of the contraction being free;
 // so weights never cross lanes, and the running maximum and sums are per lane (the maximum
 // agreed on by the four lanes of a column, and only when some column's grows by more than a
-// factor of 2^6). Codes go into the products as whole numbers, exact in either type, and the
-// grids are applied to the sums: S = step . (q, Q) + base . sum(Q) per group, and
-// V's step to the weights, whose product with base is summed beside. Whatever the lengths, a
-// token outside its sequence has grid {0, 0} and weight 0.
+// factor of 2^6). Codes go into the products as whole numbers, and the grids are applied to
+// the sums: S = step . (q, Q) + base . sum(Q) per group; V's step goes to the weights, and the
+// middle of V's grid, times the weights, is summed beside. The 16 lanes of a row of lanes hold
+// the grids of its four tokens, one group each, and a broadcast within the row is part of the
+// multiplication that takes one (DPP), so a grid costs no register of its own and no
+// conversion per use. Whatever the lengths, a token outside its sequence has grid {0, 0} and
+// weight 0.
 #pragma once
 
 #include "hqq_cache_internal.h"
@@ -27,7 +30,6 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
 constexpr int kAttnThreads = 256;
@@ -44,6 +46,13 @@ __device__ __forceinline__ f32x4 mfma32(const u32x4 a, const u32x4 b, const f32x
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Lane N of each row of 16 lanes, for all of the row.
+template <int N>
+__device__ __forceinline__ float row_lane(float x)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xf, 0xf, true));
 }
 
 // Two whole numbers 0..15 in neighbouring bytes (pair HI: bytes 2, 3) as two values of the
@@ -96,29 +105,35 @@ __device__ __forceinline__ u32x4 key_frag(const uint32_t *w)
     return f;
 }
 
-// Code i of a value's row for two tokens (words x, y hold it) as bfloat16 numbers.
+// Code i of a value's row for two tokens (words x, y hold it), less the middle of the codes
+// (8 or 128), as binary16 numbers: exact, and half as large as the codes, so that the
+// rounding of the weights they meet weighs no more than it would on the values themselves.
 template <int NB>
 __device__ __forceinline__ uint32_t value_pair(const uint32_t *x, const uint32_t *y, int i)
 {
+    uint32_t w;
+    float off;
     if constexpr (NB == 4) {
-        // bytes 2c and 2c + 1 of both tokens, side by side: codes 4c..4c+3
+        // Codes 4c..4c+3 of both tokens in the halves of a word. With exponent bits over it,
+        // a code in the lowest bits stands for 1024 + q, one in bits 4 to 7 for 64 + q.
         const int c = i >> 2, k = c & 1;
-        const uint32_t p = __builtin_amdgcn_perm(y[c >> 1], x[c >> 1], k ? 0x07030602u : 0x05010400u);
-        const uint32_t n = (i & 1 ? p >> 4 : p) & 0x0f0f0f0fu;
-        return i & 2 ? small2<true, true>(n) : small2<true, false>(n);
+        uint32_t p = __builtin_amdgcn_perm(y[c >> 1], x[c >> 1], k ? 0x07060302u : 0x05040100u);
+        if (i & 2) p >>= 8;
+        w = i & 1 ? (p & 0x00f000f0u) | 0x54005400u : (p & 0x000f000fu) | 0x64006400u;
+        off = i & 1 ? 72.f : 1032.f;
     } else {
-        return whole_bf16x2(ubyte(x[i >> 2], i & 3), ubyte(y[i >> 2], i & 3));
+        const uint32_t p = __builtin_amdgcn_perm(y[i >> 2], x[i >> 2], i & 2 ? 0x07030602u : 0x05010400u);
+        w = __builtin_amdgcn_perm(0x64646464u, p, i & 1 ? 0x04030402u : 0x04010400u);
+        off = 1152.f;
     }
+    const f16x2 mid = {(_Float16)off, (_Float16)off};
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, w) - mid);
 }
 
-// Two binary32 numbers as bfloat16 (nearest even), and what that leaves of them.
-__device__ __forceinline__ uint32_t round_pair(float &a, float &b)
+__device__ __forceinline__ uint32_t round_pair(float a, float b)
 {
     const f32x2 x = {a, b};
-    const uint32_t r = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-    a -= __uint_as_float(r << 16);
-    b -= __uint_as_float(r & 0xffff0000u);
-    return r;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2));
 }
 
 template <int BYTES>
@@ -138,6 +153,19 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[BYTES
         const uint2 x = *reinterpret_cast<const uint2 *>(p);
         w[0] = x.x;
         w[1] = x.y;
+    }
+}
+
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F &&f)
+{
+    if constexpr (I < N) {
+        f(Index<I>{});
+        static_for<N, I + 1>(f);
     }
 }
 
@@ -183,38 +211,54 @@ __device__ void lay_out(const AttnArgs &a, int32_t *starts, int32_t *scan)
     __syncthreads();
 }
 
+// How far a score may lie above the maximum that weights are taken from: weights reach 2^6.
+constexpr float kSlack = 6.f;
+// V's steps are scaled to below 2^9 (by a power of two that follows the largest seen), so that
+// weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
+constexpr int kStepBits = 8;
+
 template <typename T, int NB, int D, int G, int RT>
-__global__ __launch_bounds__(kAttnThreads) void attn_kernel(AttnArgs a)
+__global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
 {
     constexpr bool kBf16 = Types<T>::kBf16;
     constexpr int kGroups = D / G, kRows = 16 * RT;
-    constexpr int kKeyBytes = D * NB / 32;      // a lane's quarter of a token's key
-    constexpr int kValBytes = D * NB / 128;     // a row of a token's value
+    constexpr int kRow = D * NB / 8;            // bytes of a token's codes
+    constexpr int kKeyBytes = kRow / 4;         // a lane's quarter of a token's key
+    constexpr int kValBytes = kRow / 16;        // a row of a token's value
     constexpr int kUnitWords = NB / 4;
+    constexpr int kGrids = 4 * kGroups;         // of four tokens
+    constexpr int kGridRegs = (kGrids + 15) / 16;
+    constexpr int kPart = D < 128 ? D : 128;    // dimensions joined over the waves at a time
+    constexpr int kStride = kPart + 4;
     extern __shared__ int32_t shared[];
     int32_t *starts = shared;                                       // [n_seqs + 1]
     int32_t *scan = shared + (((unsigned)a.s.n_seqs + 4) & ~3u);    // [kWaves]
     float *ml = reinterpret_cast<float *>(scan + 4);                // [kWaves][kRows][2]
-    float *sum = ml + kWaves * kRows * 2;                           // [kRows][D]
+    float *part = ml + kWaves * kRows * 2;                          // [kWaves][16][kStride]
 
     lay_out<kRows>(a, starts, scan);
     const int h = (int)(blockIdx.x % (unsigned)a.c.heads), w = (int)(blockIdx.x / (unsigned)a.c.heads);
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b <= a.s.n_seqs; b += kAttnThreads) a.side.starts[b] = starts[b];
-    const int W = a.side.workers, U = starts[a.s.n_seqs];
+    const int W = a.side.workers, U = __builtin_amdgcn_readfirstlane(starts[a.s.n_seqs]);
     const int u_end = first_unit(w + 1, W, U);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // where a lane's parts lie from the first byte (word) of 16 tokens'
+    const unsigned key_at = col * kRow + quad * kKeyBytes, val_at = lane * 4 * kValBytes;
+    const unsigned grid_at = quad * kGrids + (col & (kGrids - 1));
 
     for (int u = first_unit(w, W, U); u < u_end;) {
         // the item that unit u is of
         int b = 0;
         for (int hi = a.s.n_seqs; hi - b > 1;) {
             const int mid = (b + hi) >> 1;
-            if (starts[mid] <= u) b = mid; else hi = mid;
+            if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) b = mid; else hi = mid;
         }
         const Rows rows = rows_of(a.s, b);
         const int len = len_of(a.s, b), n_rows = (rows.end - rows.begin) * a.per;
-        const int along = units_along(len), tile = (u - starts[b]) / along, u_in = (u - starts[b]) % along;
+        const int along = units_along(len), u_item = u - __builtin_amdgcn_readfirstlane(starts[b]);
+        const int tile = u_item / along, u_in = u_item % along;
         const int count = min(u_end - u, along - u_in);
         const int row0 = tile * kRows;
         u += count;
@@ -247,7 +291,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_kernel(AttnArgs a)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x += v[e];
                 }
-                qsum[t][g] = column_sum(x);
+                qsum[t][g] = column_sum(x) * a.scale;
             }
         }
 #pragma unroll
@@ -259,233 +303,305 @@ __global__ __launch_bounds__(kAttnThreads) void attn_kernel(AttnArgs a)
         lim_high = __builtin_amdgcn_readfirstlane(lim_high);
 
         f32x4 o[RT][D / 16];
-        float m[RT], l[RT], bsum[RT][kGroups];
+        // m: scores are taken from it; above: how far one may lie above before m moves (none
+        // while m has not been set)
+        float m[RT], above[RT], l[RT], bsum[RT][kGroups];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            m[t] = -INFINITY;
+            m[t] = 0.f;
+            above[t] = -INFINITY;
             l[t] = 0.f;
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) bsum[t][g] = 0.f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[t][j] = f32x4{0, 0, 0, 0};
         }
+        // V's steps are below step_lim and multiplied by step_by
+        float step_lim = 0.f, step_by = 0.f;
 
-        for (int step = 0; step < count; ++step) {
-            const int t0 = (u_in + step) * kUnit + wave * kTile;
-            if (t0 >= lim_high) break;
-            float s[RT][8];
-            uint32_t vw[8][(kValBytes + 3) / 4];
-            uint32_t vmeta[8][kGroups];
-            int good[2];                        // tokens of each half that are in the cache
+        const int t_end = min((u_in + count) * kUnit, lim_high);
+        uint32_t kw[2][kKeyBytes / 4], vw[2][kValBytes], kgrid[2][kGridRegs], vgrid[2][kGridRegs];
+        int page[2];
+        // Tokens of a half that are in the cache; their first byte of codes over kRow.
+        auto find = [&](int t0) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                page[half] = __builtin_amdgcn_readfirstlane(t0 + 16 * half < len ? page_of(a.s, b, t0 + 16 * half) : -1);
+        };
+        auto first = [&](int t0, int half) {
+            const int at = (t0 + 16 * half) & ((1 << a.s.page_shift) - 1);
+            return (((int64_t)max(page[half], 0) * a.c.heads + h) << a.s.page_shift) + at;
+        };
+        auto load_keys = [&](int t0) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int th = t0 + 16 * half;
-                int page = th < len ? page_of(a.s, b, th) : -1;
-                page = __builtin_amdgcn_readfirstlane(page);
-                good[half] = page < 0 ? 0 : min(16, len - th);
-                const int at = th & ((1 << a.s.page_shift) - 1);
-                const int64_t slice = ((int64_t)max(page, 0) * a.c.heads + h) << a.s.page_shift;
-                const uint8_t *kc = a.c.k_codes + slice * (D * NB / 8) +
-                                    k_unit_at(at + col, quad, 0, D, NB);
-                const uint8_t *vc = a.c.v_codes + slice * (D * NB / 8) +
-                                    v_row_at(at + 4 * quad, col, D, NB);
-                const uint32_t *km = a.c.k_meta + (slice + at + 4 * quad) * kGroups;
-                const uint32_t *vm = a.c.v_meta + (slice + at + 4 * quad) * kGroups;
-                uint32_t kw[kKeyBytes / 4], vq[kValBytes], kmeta[4][kGroups];
-                load_words<kKeyBytes>(kc, kw);
-                load_words<4 * kValBytes>(vc, vq);
+                const int64_t at = first(t0, half);
+                load_words<kKeyBytes>(a.c.k_codes + at * kRow + key_at, kw[half]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int k = 0; k < kGridRegs; ++k) kgrid[half][k] = (a.c.k_meta + at * kGroups)[grid_at + 16 * k];
+            }
+        };
+        auto load_values = [&](int t0) {
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const bool in = 4 * quad + i < good[half];
-                        kmeta[i][g] = in ? km[i * kGroups + g] : 0u;
-                        vmeta[4 * half + i][g] = in ? vm[i * kGroups + g] : 0u;
+            for (int half = 0; half < 2; ++half) {
+                const int64_t at = first(t0, half);
+                load_words<4 * kValBytes>(a.c.v_codes + at * kRow + val_at, vw[half]);
+#pragma unroll
+                for (int k = 0; k < kGridRegs; ++k) vgrid[half][k] = (a.c.v_meta + at * kGroups)[grid_at + 16 * k];
+            }
+        };
+
+        int t0 = u_in * kUnit + wave * kTile;
+        if (t0 < t_end) {
+            find(t0);
+            load_keys(t0);
+            load_values(t0);
+        }
+        for (; t0 < t_end; t0 += kUnit) {
+            // The next step's keys are asked for as soon as this one's are in the products,
+            // its values once this one's are: both are under way during half a step, with no
+            // registers but their own.
+            const int next = t0 + kUnit < t_end ? t0 + kUnit : t0;
+            int good[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                good[half] = page[half] < 0 ? 0 : min(16, len - t0 - 16 * half);
+            const bool open = t0 + kTile <= lim_low && good[0] == 16 && good[1] == 16;
+            if (!open) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int k = 0; k < kGridRegs; ++k) {
+                        const int token = 4 * quad + ((col & (kGrids - 1)) + 16 * k) / kGroups;
+                        if (token >= good[half]) kgrid[half][k] = vgrid[half][k] = 0;
                     }
+            }
+            f32x4 acc[2][RT][kGroups];
+            float kstep[2][kGridRegs], kbase[2][kGridRegs];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (kValBytes >= 4) {
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                        for (int k = 0; k < kValBytes / 4; ++k)
-                            vw[4 * half + i][k] = vq[i * (kValBytes / 4) + k];
-                    } else {
-                        vw[4 * half + i][0] = vq[i / 2] >> (16 * (i & 1));
-                    }
+                for (int k = 0; k < kGridRegs; ++k) {
+                    kstep[half][k] = to_f32<T>(kgrid[half][k] & 0xffffu) * a.scale;
+                    kbase[half][k] = to_f32<T>(kgrid[half][k] >> 16);
                 }
-                // scores, one group of dimensions after another
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][4 * half + i] = 0.f;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    f32x4 acc[RT];
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+                    for (int t = 0; t < RT; ++t) acc[half][t][g] = f32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int mm = g * G / 32; mm < (g + 1) * G / 32; ++mm) {
-                        const u32x4 kf = key_frag<kBf16, NB>(kw + mm * kUnitWords);
+                        const u32x4 kf = key_frag<kBf16, NB>(kw[half] + mm * kUnitWords);
 #pragma unroll
-                        for (int t = 0; t < RT; ++t) acc[t] = mfma32<kBf16>(kf, qf[t][mm], acc[t]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float st = to_f32<T>(kmeta[i][g] & 0xffffu), ba = to_f32<T>(kmeta[i][g] >> 16);
-#pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            s[t][4 * half + i] += fmaf(st, acc[t][i], ba * qsum[t][g]);
+                        for (int t = 0; t < RT; ++t) acc[half][t][g] = mfma32<kBf16>(kf, qf[t][mm], acc[half][t][g]);
                     }
                 }
             }
-            const bool open = t0 + kTile <= lim_low && good[0] == 16 && good[1] == 16;
+            find(next);
+            load_keys(next);
+            __builtin_amdgcn_sched_barrier(0);
+
+            float s[RT][8];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                float top = -INFINITY;
+                static_for<8>([&](auto i) {
+                    constexpr int half = i.value / 4, r = i.value % 4;
+                    float x = -m[t];
+                    static_for<kGroups>([&](auto g) {
+                        constexpr int at = r * kGroups + g.value;
+                        x = fmaf(row_lane<at % 16>(kbase[half][at / 16]), qsum[t][g.value], x);
+                        x = fmaf(row_lane<at % 16>(kstep[half][at / 16]), acc[half][t][g.value][r], x);
+                    });
+                    s[t][i.value] = x;
+                });
+                if (!open) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[t][i] *= a.scale;
-                    if (!open) {
+                    for (int i = 0; i < 8; ++i) {
                         const int at = 4 * quad + (i & 3);
                         if (t0 + 16 * (i >> 2) + at >= lim[t] || at >= good[i >> 2]) s[t][i] = -INFINITY;
                     }
-                    top = fmaxf(top, s[t][i]);
                 }
-                // Weights are 2^(s - m) with m the largest score up to some time ago: at most
-                // 2^6, which costs the sums nothing.
-                if (__any(top > m[t] + 6.f)) {
+                float top = fmaxf(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])),
+                                  fmaxf(fmaxf(s[t][4], s[t][5]), fmaxf(s[t][6], s[t][7])));
+                if (__any(top > above[t])) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
-                    const float next = fmaxf(m[t], top);
-                    const float f = next == m[t] ? 1.f : __builtin_amdgcn_exp2f(m[t] - next);
-                    m[t] = next;
+                    // m moves up to the largest score, or at first to it wherever it is
+                    const float d = top > fminf(above[t], 0.f) ? top : 0.f;
+                    const float f = above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-d);
+                    if (top > -INFINITY) above[t] = kSlack;
+                    m[t] += d;
                     l[t] *= f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[t][i] -= d;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) bsum[t][g] *= f;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) o[t][j] *= f;
                 }
-                const float mu = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    s[t][i] = __builtin_amdgcn_exp2f(s[t][i] - mu);
+                    s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
                     l[t] += s[t][i];
                 }
             }
-            // Weights times V's step, as a bfloat16 number and what it leaves, again as one:
-            // 16 bits in all, over the whole range of binary32.
+
+            float vstep[2][kGridRegs], vmid[2][kGridRegs];
+            float most = 0.f;
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                u32x4 ph[RT], pl[RT];
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int k = 0; k < kGridRegs; ++k) {
+                    vstep[half][k] = to_f32<T>(vgrid[half][k] & 0xffffu);
+                    vmid[half][k] = fmaf(vstep[half][k], NB == 4 ? 8.f : 128.f, to_f32<T>(vgrid[half][k] >> 16));
+                    most = fmaxf(most, vstep[half][k]);
+                }
+            if (__any(most >= step_lim && most > 0.f)) {
+#pragma unroll
+                for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
+                // the power of two at or below it
+                const float p2 = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
+                const float by = ldexpf(1.f / p2, kStepBits), f = step_by > 0.f ? by / step_by : 1.f;
+                step_lim = 2.f * p2;
+                step_by = by;
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) o[t][j] *= f;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int k = 0; k < kGridRegs; ++k) vstep[half][k] *= step_by;
+
+            // weights times V's step, in binary16
+            static_for<kGroups>([&](auto g) {
+                u32x4 pf[RT];
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        float x = s[t][i] * to_f32<T>(vmeta[i][g] & 0xffffu);
-                        float y = s[t][i + 1] * to_f32<T>(vmeta[i + 1][g] & 0xffffu);
-                        bsum[t][g] = fmaf(s[t][i], to_f32<T>(vmeta[i][g] >> 16), bsum[t][g]);
-                        bsum[t][g] = fmaf(s[t][i + 1], to_f32<T>(vmeta[i + 1][g] >> 16), bsum[t][g]);
-                        ph[t][i / 2] = round_pair(x, y);
-                        pl[t][i / 2] = round_pair(x, y);
-                    }
+                    static_for<4>([&](auto i) {
+                        constexpr int half = i.value / 2, r = i.value % 2 * 2;
+                        constexpr int at = r * kGroups + g.value, at1 = at + kGroups;
+                        const float x = s[t][2 * i.value], y = s[t][2 * i.value + 1];
+                        bsum[t][g.value] = fmaf(row_lane<at % 16>(vmid[half][at / 16]), x, bsum[t][g.value]);
+                        bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vmid[half][at1 / 16]), y, bsum[t][g.value]);
+                        pf[t][i.value] = round_pair(row_lane<at % 16>(vstep[half][at / 16]) * x,
+                                                    row_lane<at1 % 16>(vstep[half][at1 / 16]) * y);
+                    });
                 }
 #pragma unroll
-                for (int j = g * G / 16; j < (g + 1) * G / 16; ++j) {
+                for (int jj = 0; jj < G / 16; ++jj) {
+                    const int j = g.value * (G / 16) + jj;
                     u32x4 vf;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) vf[i] = value_pair<NB>(vw[2 * i], vw[2 * i + 1], j);
+                    for (int i = 0; i < 4; ++i) {
+                        // tokens 2i and 2i + 1 of the lane's eight
+                        uint32_t x[kValBytes > 4 ? kValBytes / 4 : 1], y[kValBytes > 4 ? kValBytes / 4 : 1];
+                        const uint32_t *v = vw[i / 2];
+                        if constexpr (kValBytes >= 4) {
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        o[t][j] = mfma32<true>(vf, ph[t], o[t][j]);
-                        o[t][j] = mfma32<true>(vf, pl[t], o[t][j]);
+                            for (int k = 0; k < kValBytes / 4; ++k) {
+                                x[k] = v[(i % 2 * 2) * (kValBytes / 4) + k];
+                                y[k] = v[(i % 2 * 2 + 1) * (kValBytes / 4) + k];
+                            }
+                        } else {
+                            x[0] = v[i % 2];
+                            y[0] = v[i % 2] >> 16;
+                        }
+                        vf[i] = value_pair<NB>(x, y, j);
                     }
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) o[t][j] = mfma32<false>(vf, pf[t], o[t][j]);
                 }
-            }
+            });
+            load_values(next);
+            __builtin_amdgcn_sched_barrier(0);
         }
 
         // The four waves' parts, on the largest of their maxima.
-        __syncthreads();                        // the last piece's sums have been read
+        const float unstep = step_by > 0.f ? 1.f / step_by : 0.f;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             l[t] = column_sum(l[t]);
             if (quad == 0) {
-                ml[(wave * kRows + 16 * t + col) * 2] = m[t];
+                ml[(wave * kRows + 16 * t + col) * 2] = above[t] < 0.f ? -INFINITY : m[t];
                 ml[(wave * kRows + 16 * t + col) * 2 + 1] = l[t];
             }
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) bsum[t][g] = column_sum(bsum[t][g]);
         }
-        __syncthreads();
-        float f[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            float top = -INFINITY;
-            for (int k = 0; k < kWaves; ++k) top = fmaxf(top, ml[(k * kRows + 16 * t + col) * 2]);
-            f[t] = m[t] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[t] - top);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const float base = column_sum(bsum[t][g]);
-#pragma unroll
-                for (int j = g * G / 16; j < (g + 1) * G / 16; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[t][j][i] = (o[t][j][i] + base) * f[t];
-            }
-        }
-        for (int k = 0; k < kWaves; ++k) {
-            if (k == wave) {
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int d = j / (G / 16) * G + (4 * quad + i) * (G / 16) + j % (G / 16);
-                            float *x = sum + (16 * t + col) * D + d;
-                            *x = k == 0 ? o[t][j][i] : *x + o[t][j][i];
-                        }
-            }
-            __syncthreads();
-        }
-        const int rows_here = min(kRows, n_rows - row0);
         const bool whole = count == along;
         const int slot = 2 * w + (u_in > 0 ? 0 : 1);
-        for (int x = threadIdx.x; x < rows_here * D; x += kAttnThreads) {
-            const int r = x / D, d = x % D;
-            float top = -INFINITY, all = 0.f;
-            for (int k = 0; k < kWaves; ++k) top = fmaxf(top, ml[(k * kRows + r) * 2]);
-            for (int k = 0; k < kWaves; ++k) {
-                const float mk = ml[(k * kRows + r) * 2];
-                all += mk == -INFINITY ? 0.f : ml[(k * kRows + r) * 2 + 1] * __builtin_amdgcn_exp2f(mk - top);
-            }
-            const int tok = rows.begin + (row0 + r) / a.per, hq = h * a.per + (row0 + r) % a.per;
-            if (!whole) {
-                const int64_t at = ((int64_t)h * 2 * W + slot) * kRows + r;
-                a.side.slot_o[at * D + d] = sum[x];
-                if (d == 0) {
-                    a.side.slot_ml[at * 2] = top;
-                    a.side.slot_ml[at * 2 + 1] = all;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int d0 = 0; d0 < D; d0 += kPart) {
+                // a lane has runs of G/16 neighbouring dimensions of its column
+#pragma unroll
+                for (int g = d0 / G; g < (d0 + kPart) / G; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int jj = 0; jj < G / 16; ++jj)
+                            part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
+                                fmaf(o[t][g * (G / 16) + jj][i], unstep, bsum[t][g]);
+                __syncthreads();
+                for (int x = threadIdx.x; x < 16 * kPart / 4; x += kAttnThreads) {
+                    const int r = x / (kPart / 4), d = x % (kPart / 4) * 4, row = row0 + 16 * t + r;
+                    if (row >= n_rows) break;
+                    float mk[kWaves], top = -INFINITY, all = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kWaves; ++k) {
+                        mk[k] = ml[(k * kRows + 16 * t + r) * 2];
+                        top = fmaxf(top, mk[k]);
+                    }
+                    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < kWaves; ++k) {
+                        if (mk[k] == -INFINITY) continue;
+                        const float f = __builtin_amdgcn_exp2f(mk[k] - top);
+                        all = fmaf(f, ml[(k * kRows + 16 * t + r) * 2 + 1], all);
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (k * 16 + r) * kStride + d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum[e] = fmaf(f, v[e], sum[e]);
+                    }
+                    float *to_o, *to_ml;
+                    int64_t at;
+                    if (!whole) {
+                        at = ((int64_t)h * 2 * W + slot) * kRows + 16 * t + r;
+                        to_o = a.side.slot_o;
+                        to_ml = a.side.slot_ml;
+                    } else {
+                        at = (int64_t)h * a.s.n_tokens * a.per + (int64_t)rows.begin * a.per + row;
+                        to_o = a.side.row_o;
+                        to_ml = a.side.row_ml;
+                    }
+                    if (to_o) {
+                        *reinterpret_cast<f32x4 *>(to_o + at * D + d0 + d) = sum;
+                        if (d0 + d == 0) *reinterpret_cast<f32x2 *>(to_ml + at * 2) = f32x2{top, all};
+                        continue;
+                    }
+                    const float inv = all > 0.f ? 1.f / all : 0.f;
+                    const int tok = rows.begin + row / a.per, hq = h * a.per + row % a.per;
+                    const uint2 packed = {from_f32<T>(sum[0] * inv) | from_f32<T>(sum[1] * inv) << 16,
+                                          from_f32<T>(sum[2] * inv) | from_f32<T>(sum[3] * inv) << 16};
+                    *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + d0 + d) = packed;
+                    if (a.lse && d0 + d == 0)
+                        a.lse[(int64_t)tok * a.c.heads * a.per + hq] =
+                            all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
                 }
-            } else if (a.side.row_o) {
-                const int64_t at = (int64_t)h * a.s.n_tokens * a.per + (int64_t)rows.begin * a.per + row0 + r;
-                a.side.row_o[at * D + d] = sum[x];
-                if (d == 0) {
-                    a.side.row_ml[at * 2] = top;
-                    a.side.row_ml[at * 2 + 1] = all;
-                }
-            } else {
-                a.out[tok * a.o_ts + hq * a.o_hs + d] = (uint16_t)from_f32<T>(all > 0.f ? sum[x] / all : 0.f);
-                if (a.lse && d == 0)
-                    a.lse[(int64_t)tok * a.c.heads * a.per + hq] =
-                        all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
+                __syncthreads();
             }
-        }
-        __syncthreads();
     }
 }
 
 template <typename T, int NB, int D, int G, int RT>
 hipError_t launch_one(const AttnArgs &a, hipStream_t stream)
 {
-    // at most 16 KB of starts, 2 KB and 32 KB: within what any launch may ask for
+    // at most 16 KB of starts, 1 KB and 33 KB: within what any launch may ask for
+    const int part = D < 128 ? D : 128;
     const size_t lds = 4 * (((size_t)a.s.n_seqs + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
-                       4 * (size_t)16 * RT * D;
+                       4 * (size_t)kWaves * 16 * (part + 4);
     attn_kernel<T, NB, D, G, RT><<<dim3((unsigned)a.side.workers * a.c.heads), kAttnThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
@@ -494,9 +610,8 @@ template <typename T, int NB, int D, int G>
 hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
     if (a.side.tiles16 == 1) return launch_one<T, NB, D, G, 1>(a, stream);
-    if (a.side.tiles16 == 2) return launch_one<T, NB, D, G, 2>(a, stream);
     if constexpr (D <= 128)
-        if (a.side.tiles16 == 4) return launch_one<T, NB, D, G, 4>(a, stream);
+        if (a.side.tiles16 == 2) return launch_one<T, NB, D, G, 2>(a, stream);
     return hipErrorInvalidValue;
 }
 

@@ -121,18 +121,17 @@ struct Plan {
 };
 
 // Query rows to a tile: 16 where a sequence has no more, for its work is to read the cache;
-// up to 64 (32 for 256-wide heads, whose sums fill the registers) so that each code read and
-// widened meets more rows.
+// else 32, so that each code read and widened meets more rows (256-wide heads fill the
+// registers with 16).
 int tiles_for(int64_t rows, int dim)
 {
-    const int t = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    return dim == 256 && t > 2 ? 2 : t;
+    return rows <= 16 || dim == 256 ? 1 : 2;
 }
 
 // Blocks of a launch: what the 256 CUs hold at once.
 int workers_for(int tiles16, int heads)
 {
-    const int blocks = tiles16 == 1 ? 1024 : 512;
+    const int blocks = tiles16 == 1 ? 768 : 512;
     return (blocks + heads - 1) / heads;
 }
 

@@ -75,7 +75,7 @@ struct AttnSide {
     float *slot_ml;             // [heads][2 * workers][rows_per][2]: maximum (base 2), sum
     float *row_o, *row_ml;      // [heads][n_tokens * per][dim], [..][2], or null
     int32_t workers;            // runs of a head's units
-    int32_t tiles16;            // rows_per / 16: 1, 2 or 4
+    int32_t tiles16;            // rows_per / 16: 1 or 2
 };
 
 struct AttnArgs {

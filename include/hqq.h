@@ -366,8 +366,8 @@ hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
  * reads key/value head h / (n_q_heads / n_heads). The row at position x of its sequence
  * sees positions 0..x (which must be in the cache already: write, then attend):
  *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * <q, k_t>),
- * with k_t, v_t = base + q * step unrounded, scores, weights and sums in binary32 and out
- * rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
+ * with k_t, v_t = base + q * step unrounded, scores and sums in binary32, weights rounded to
+ * 11 bits where they meet the codes of v, and out rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
  * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. workspace: device,
  * 256-byte aligned, at least hqq_cache_attention_workspace() bytes; calls that may run at the
  * same time need one each. Results do not depend on what it held. */

@@ -109,6 +109,18 @@ class Held:
             base = m[..., 1].repeat_interleave(g, -1)
             self.part[w] = (base + q * step, base.abs() + q * step)
 
+    def steps(self, pages, n):
+        """V's steps by dimension of the first n tokens of `pages`, [heads, n, dim]; 0 where not
+        in the cache."""
+        c, size = self.c, self.c["page_size"]
+        pages = list(pages)[:-(-n // size)]
+        n_pages = c["k_codes"].shape[0]
+        ok = torch.tensor([0 <= p < n_pages for p in pages], dtype=torch.bool).repeat_interleave(size)[:n]
+        idx = torch.tensor([p if 0 <= p < n_pages else 0 for p in pages], dtype=torch.long)
+        step = c["v_meta"].cpu().double()[..., 0].repeat_interleave(c["group_size"], -1)
+        y = step[idx].transpose(0, 1).reshape(c["n_heads"], -1, c["head_dim"])[:, :n]
+        return torch.where(ok[None, :, None], y, torch.zeros_like(y))
+
     def tokens(self, which, pages, n):
         """Values and their parts' magnitudes of the first n tokens of `pages`: [heads, n, dim],
         and which of them are in the cache."""
@@ -126,15 +138,18 @@ class Held:
 
 def attention(held, table, lens, cu, q, scale, prefix_pages=(), prefix_len=0):
     """(out, lse, bound) in float64 for q [n, heads, dim]; rows of no sequence are NaN. `bound`
-    is how far a binary32 evaluation with weights kept to 16 bits may be off, before the
+    is how far a binary32 evaluation with V's weights rounded to binary16 may be off, before the
     output's own rounding:
 
     A score is a sum of dim exact products of a 16-bit number and a code, scaled: its error is
     at most (dim + 8) 2^-24 of the sum of magnitudes S, so a weight's relative error is twice
     scale*S*(dim + 8)*2^-24, once more for the sum that divides, plus 2^-18 for exp2 (its
-    argument below 2^6 in magnitude where it matters, and a unit in the last place), plus 2^-16
-    for the two 8-bit parts of weight times step. Sums over n tokens add n 2^-24 at most. All
-    of it weighs on A = sum of p (|base| + q step)."""
+    argument below 2^6 in magnitude where it matters, and a unit in the last place). Sums over
+    n tokens add n 2^-24 at most. All of it weighs on A = sum of p (|base| + q step).
+    Weight times step is rounded to binary16's 11 bits, by at most half a step of them, and
+    meets a code less the middle one: 2^-11 of sum p step 2^(nbits - 1), and where it is below
+    binary16's normal numbers n 2^-26 of the largest step (steps are scaled to 2^8, the
+    largest weight is at least 1, and a subnormal number is off by 2^-25 at most)."""
     c = held.c
     heads, dim = c["n_heads"], c["head_dim"]
     n, hq, _ = q.shape
@@ -164,11 +179,15 @@ def attention(held, table, lens, cu, q, scale, prefix_pages=(), prefix_len=0):
         p = w / tot.clamp(min=1e-300)
         o = torch.einsum("hpts,hsd->hptd", p, v)
         a = torch.einsum("hpts,hsd->hptd", p, va)
+        vs = torch.cat((held.steps(prefix_pages, prefix_len), held.steps(table[b], ln)), 1) * 2.0 ** (c["nbits"] - 1)
+        a2 = torch.einsum("hpts,hsd->hptd", p, vs) * 2.0 ** -11
+        if vs.shape[1]:
+            a2 = a2 + s.shape[-1] * 2.0 ** -26 * vs.amax((0, 1, 2)) * 2
         ds = torch.where(p > 1e-12, mag, torch.zeros_like(mag)).amax(-1, keepdim=True) * (dim + 8) * 2.0 ** -24 \
             if s.shape[-1] else torch.zeros_like(m)
-        rel = 4 * ds + 2.0 ** -17 + 2.0 ** -16 + s.shape[-1] * 2.0 ** -24
+        rel = 4 * ds + 2.0 ** -17 + s.shape[-1] * 2.0 ** -24
         out[lo:hi] = o.permute(2, 0, 1, 3).reshape(hi - lo, hq, dim)
-        bound[lo:hi] = (a * rel).permute(2, 0, 1, 3).reshape(hi - lo, hq, dim)
+        bound[lo:hi] = (a * rel + a2).permute(2, 0, 1, 3).reshape(hi - lo, hq, dim)
         lse[lo:hi] = (m + torch.log(tot)).squeeze(-1).permute(2, 0, 1).reshape(hi - lo, hq)
         blse[lo:hi] = (2 * ds + 2.0 ** -18 + s.shape[-1] * 2.0 ** -24 + m.abs().nan_to_num(0, 0, 0) * 2.0 ** -22) \
             .squeeze(-1).permute(2, 0, 1).reshape(hi - lo, hq)
