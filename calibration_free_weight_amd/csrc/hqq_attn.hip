@@ -6,18 +6,26 @@ namespace hqq {
 namespace {
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWaves = kJoinThreads / 64;
+constexpr int kAhead = 8;       // pieces asked for at a time
 
-template <typename T, int E>
-struct Acc {                    // a row's result so far; lane holds E dimensions
-    float m = -INFINITY, l = 0.f, o[E] = {};
+template <int E>
+struct Acc {                    // a row's result so far; a lane holds E dimensions
+    float m = -INFINITY, l = 0.f;
+    float o[E] = {};
 };
 
-// Adds 64 pieces at a time: lane k has the maximum m and sum l of piece k, whose output is
-// at o + off(k) * D.
-template <typename T, int E, typename Off>
-__device__ __forceinline__ void add_pieces(Acc<T, E> &acc, int n, float m, float l, const float *o, Off off)
+template <int E>
+struct Floats {
+    float x[E];
+} __attribute__((aligned(4 * E)));
+
+// Adds up to 64 pieces: lane k has the maximum m and sum l of piece k, whose output is at
+// o + off(k) * D. Of the row's WPR waves each adds every WPR-th piece's output.
+template <int E, int WPR, typename Off>
+__device__ __forceinline__ void add_pieces(Acc<E> &acc, int n, float m, float l, const float *o, Off off)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, mine = (threadIdx.x >> 6) % WPR;
     float top = m;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
@@ -32,62 +40,81 @@ __device__ __forceinline__ void add_pieces(Acc<T, E> &acc, int n, float m, float
     acc.m = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc.o[e] *= g;
-    for (int k = 0; k < n; ++k) {
-        const float fk = __shfl(f, k);
-        if (fk == 0.f) continue;            // nothing was seen there, or nothing written
-        const float *x = o + off(k) * (64 * E) + lane * E;
+    for (int k0 = mine; k0 < n; k0 += kAhead * WPR) {
+        Floats<E> x[kAhead];
+        float fk[kAhead];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc.o[e] = fmaf(fk, x[e], acc.o[e]);
+        for (int j = 0; j < kAhead; ++j) {
+            const int k = min(k0 + j * WPR, n - 1);
+            x[j] = *reinterpret_cast<const Floats<E> *>(o + off(k) * (64 * E) + lane * E);
+            fk[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), k));
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (k0 + j * WPR < n)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc.o[e] = fmaf(fk[j], x[j].x[e], acc.o[e]);
     }
 }
 
 // Adds what one side found for a row; false if the item is whole and its result elsewhere.
-template <typename T, int E>
-__device__ __forceinline__ bool add_side(Acc<T, E> &acc, const AttnSide &d, int n_seqs, int b, int row_in_item,
-                                         int along, int h, int64_t row, int64_t rows)
+template <int E, int WPR>
+__device__ __forceinline__ bool add_side(Acc<E> &acc, const AttnSide &d, int b, int row_in_item, int along,
+                                         int h, int64_t row, int64_t rows)
 {
     const int lane = threadIdx.x & 63, per = 16 * d.tiles16;
-    if (along == 0) return true;
-    const int U = d.starts[n_seqs], W = d.workers;
+    const int U = d.starts[d.s.n_seqs], W = runs_of(d.workers, U);
     const int u0 = d.starts[b] + row_in_item / per * along;
-    const int w0 = worker_of(u0, W, U), w1 = worker_of(u0 + along - 1, W, U);
+    const int w0 = run_of(u0, W, U), w1 = run_of(u0 + along - 1, W, U);
     if (w0 == w1) {
         if (!d.row_o) return false;
         const int64_t at = h * rows + row;
         const float m = lane == 0 ? d.row_ml[at * 2] : -INFINITY, l = lane == 0 ? d.row_ml[at * 2 + 1] : 0.f;
-        add_pieces<T, E>(acc, 1, m, l, d.row_o, [&](int) { return at; });
+        add_pieces<E, WPR>(acc, 1, m, l, d.row_o, [&](int) { return at; });
         return true;
     }
+    // the item's first run goes on behind it, the others began before theirs
+    const auto at = [&](int w) { return ((int64_t)h * 2 * d.workers + 2 * w + (w == w0)) * per + row_in_item % per; };
     for (int wb = w0; wb <= w1; wb += 64) {
         const int w = wb + lane;
-        const auto at = [&](int v) { return ((int64_t)h * 2 * W + 2 * v + (v == w0)) * per + row_in_item % per; };
-        const bool have = w <= w1 && first_unit(w, W, U) < first_unit(w + 1, W, U);
-        const float m = have ? d.slot_ml[at(w) * 2] : -INFINITY, l = have ? d.slot_ml[at(w) * 2 + 1] : 0.f;
-        add_pieces<T, E>(acc, min(64, w1 - wb + 1), m, l, d.slot_o, [&](int k) { return at(wb + k); });
+        const float m = w <= w1 ? d.slot_ml[at(w) * 2] : -INFINITY, l = w <= w1 ? d.slot_ml[at(w) * 2 + 1] : 0.f;
+        add_pieces<E, WPR>(acc, min(64, w1 - wb + 1), m, l, d.slot_o, [&](int k) { return at(wb + k); });
     }
     return true;
 }
 
-// A wave per query row: finds the pieces of its item on each side by the rule that dealt them
-// out, and adds them on the largest of their maxima, in order.
-template <typename T, int D>
+// WPR waves per query row: they find the pieces of its item on each side by the rule that
+// dealt them out, and add them on the largest of their maxima, in order.
+template <typename T, int D, int WPR>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
 {
     constexpr int E = D / 64;
-    const int64_t x = (int64_t)blockIdx.x * (kJoinThreads / 64) + (threadIdx.x >> 6);
-    const int heads = a.heads * a.per, lane = threadIdx.x & 63;
-    const int i = (int)(x / heads), hq = (int)(x % heads), h = hq / a.per;
-    if (i >= a.s.n_tokens) return;
-    const int b = seq_at(a.s, i);
-    const Rows r = rows_of(a.s, b);
+    __shared__ float part[WPR > 1 ? kJoinWaves : 1][D];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int x = (int)(blockIdx.x * (unsigned)(kJoinWaves / WPR)) + wave / WPR;
+    const int heads = a.heads * a.per, n_tokens = a.side[0].s.n_tokens;
+    const int i = x / heads, hq = x % heads, h = hq / a.per;
+    if (i >= n_tokens) return;                      // all waves of a row together
+    const int b = __builtin_amdgcn_readfirstlane(find_seq(a.side[0].s, i));
+    const Rows r = rows_of(a.side[0].s, b);
     if (i < r.begin || i >= r.end) return;          // a row of no sequence stays as it was
-    Acc<T, E> acc;
-    const int64_t row = (int64_t)i * a.per + hq % a.per, rows = (int64_t)a.s.n_tokens * a.per;
-    if (a.prefix.starts)
-        add_side<T, E>(acc, a.prefix, 1, 0, (int)row, units_along(a.prefix_len), h, row, rows);
-    if (!add_side<T, E>(acc, a.side, a.s.n_seqs, b, (i - r.begin) * a.per + hq % a.per,
-                        units_along(len_of(a.s, b)), h, row, rows))
+    Acc<E> acc;
+    const int64_t row = (int64_t)i * a.per + hq % a.per, rows = (int64_t)n_tokens * a.per;
+    if (a.sides == 2)
+        add_side<E, WPR>(acc, a.side[1], 0, (int)row, units_along(a.side[1].s.fixed_len, a.side[1].unit), h, row, rows);
+    if (!add_side<E, WPR>(acc, a.side[0], b, (i - r.begin) * a.per + hq % a.per,
+                          units_along(len_of(a.side[0].s, b), a.side[0].unit), h, row, rows))
         return;
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[wave][lane * E + e] = acc.o[e];
+        __syncthreads();
+        if (wave % WPR) return;
+#pragma unroll
+        for (int k = 1; k < WPR; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc.o[e] += part[wave + k][lane * E + e];
+    }
     const float inv = acc.l > 0.f ? 1.f / acc.l : 0.f;
     uint16_t *o = a.out + i * a.o_ts + hq * a.o_hs + lane * E;
 #pragma unroll
@@ -96,14 +123,23 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
         a.lse[x] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * 0.6931471805599453f : -INFINITY;
 }
 
+template <typename T, int D>
+void join_rows(const JoinArgs &a, hipStream_t stream)
+{
+    // few rows have many pieces each: a block for each row
+    const int64_t rows = (int64_t)a.side[0].s.n_tokens * a.heads * a.per;
+    if (rows <= 1024)
+        join_kernel<T, D, kJoinWaves><<<dim3((unsigned)rows), kJoinThreads, 0, stream>>>(a);
+    else
+        join_kernel<T, D, 1><<<dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), kJoinThreads, 0, stream>>>(a);
+}
+
 template <typename T>
 hipError_t join_typed(const JoinArgs &a, hipStream_t stream)
 {
-    const int64_t rows = (int64_t)a.s.n_tokens * a.heads * a.per;
-    const dim3 grid((unsigned)((rows + kJoinThreads / 64 - 1) / (kJoinThreads / 64)));
-    if (a.dim == 64) join_kernel<T, 64><<<grid, kJoinThreads, 0, stream>>>(a);
-    else if (a.dim == 128) join_kernel<T, 128><<<grid, kJoinThreads, 0, stream>>>(a);
-    else join_kernel<T, 256><<<grid, kJoinThreads, 0, stream>>>(a);
+    if (a.dim == 64) join_rows<T, 64>(a, stream);
+    else if (a.dim == 128) join_rows<T, 128>(a, stream);
+    else join_rows<T, 256>(a, stream);
     return hipGetLastError();
 }
 

@@ -35,7 +35,7 @@ typedef __attribute__((ext_vector_type(2))) float f32x2;
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = kAttnThreads / 64;
 constexpr int kTile = 32;                   // tokens of a wave's step
-static_assert(kTile * kWaves == kUnit, "a unit is one step of the block");
+static_assert(kTile * kWaves == kStep, "a step is a tile for each wave");
 
 template <bool BF16>
 __device__ __forceinline__ f32x4 mfma32(const u32x4 a, const u32x4 b, const f32x4 c)
@@ -178,14 +178,14 @@ __device__ __forceinline__ float column_sum(float x)
 
 // The units before each sequence's, in LDS: starts[n_seqs] is their sum.
 template <int ROWS>
-__device__ void lay_out(const AttnArgs &a, int32_t *starts, int32_t *scan)
+__device__ void lay_out(const AttnSide &d, int per, int32_t *starts, int32_t *scan)
 {
-    const int t = threadIdx.x, n = a.s.n_seqs;
+    const int t = threadIdx.x, n = d.s.n_seqs;
     const int each = (n + kAttnThreads - 1) / kAttnThreads, b0 = min(t * each, n), b1 = min(b0 + each, n);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-        const Rows r = rows_of(a.s, b);
-        const int u = tiles_of((r.end - r.begin) * a.per, ROWS) * units_along(len_of(a.s, b));
+        const Rows r = rows_of(d.s, b);
+        const int u = tiles_of((r.end - r.begin) * per, ROWS) * units_along(len_of(d.s, b), d.unit);
         starts[b] = u;
         sum += u;
     }
@@ -230,17 +230,25 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
     constexpr int kGridRegs = (kGrids + 15) / 16;
     constexpr int kPart = D < 128 ? D : 128;    // dimensions joined over the waves at a time
     constexpr int kStride = kPart + 4;
+    const unsigned blocks0 = (unsigned)a.side[0].workers * a.c.heads;
+    AttnSide d = a.side[0];
+    unsigned block = blockIdx.x;
+    if (block >= blocks0) {
+        d = a.side[1];
+        block -= blocks0;
+    }
     extern __shared__ int32_t shared[];
     int32_t *starts = shared;                                       // [n_seqs + 1]
-    int32_t *scan = shared + (((unsigned)a.s.n_seqs + 4) & ~3u);    // [kWaves]
+    int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [kWaves]
     float *ml = reinterpret_cast<float *>(scan + 4);                // [kWaves][kRows][2]
     float *part = ml + kWaves * kRows * 2;                          // [kWaves][16][kStride]
 
-    lay_out<kRows>(a, starts, scan);
-    const int h = (int)(blockIdx.x % (unsigned)a.c.heads), w = (int)(blockIdx.x / (unsigned)a.c.heads);
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= a.s.n_seqs; b += kAttnThreads) a.side.starts[b] = starts[b];
-    const int W = a.side.workers, U = __builtin_amdgcn_readfirstlane(starts[a.s.n_seqs]);
+    lay_out<kRows>(d, a.per, starts, scan);
+    const int h = (int)(block % (unsigned)a.c.heads), w = (int)(block / (unsigned)a.c.heads);
+    if (block == 0)
+        for (int b = threadIdx.x; b <= d.s.n_seqs; b += kAttnThreads) d.starts[b] = starts[b];
+    const int U = __builtin_amdgcn_readfirstlane(starts[d.s.n_seqs]), W = runs_of(d.workers, U);
+    if (w >= W) return;
     const int u_end = first_unit(w + 1, W, U);
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -251,13 +259,13 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
     for (int u = first_unit(w, W, U); u < u_end;) {
         // the item that unit u is of
         int b = 0;
-        for (int hi = a.s.n_seqs; hi - b > 1;) {
+        for (int hi = d.s.n_seqs; hi - b > 1;) {
             const int mid = (b + hi) >> 1;
             if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) b = mid; else hi = mid;
         }
-        const Rows rows = rows_of(a.s, b);
-        const int len = len_of(a.s, b), n_rows = (rows.end - rows.begin) * a.per;
-        const int along = units_along(len), u_item = u - __builtin_amdgcn_readfirstlane(starts[b]);
+        const Rows rows = rows_of(d.s, b);
+        const int len = len_of(d.s, b), n_rows = (rows.end - rows.begin) * a.per;
+        const int along = units_along(len, d.unit), u_item = u - __builtin_amdgcn_readfirstlane(starts[b]);
         const int tile = u_item / along, u_in = u_item % along;
         const int count = min(u_end - u, along - u_in);
         const int row0 = tile * kRows;
@@ -273,7 +281,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             const bool have = row < n_rows;
             const int tok = have ? row / a.per : 0, hq = h * a.per + (have ? row % a.per : 0);
             const uint16_t *q = a.q + (rows.begin + tok) * a.q_ts + hq * a.q_hs;
-            lim[t] = !have ? 0 : a.causal ? len - (rows.end - rows.begin) + tok + 1 : len;
+            lim[t] = !have ? 0 : d.causal ? len - (rows.end - rows.begin) + tok + 1 : len;
             if (have) {
                 lim_low = min(lim_low, lim[t]);
                 lim_high = max(lim_high, lim[t]);
@@ -319,18 +327,18 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
         // V's steps are below step_lim and multiplied by step_by
         float step_lim = 0.f, step_by = 0.f;
 
-        const int t_end = min((u_in + count) * kUnit, lim_high);
+        const int t_end = (int)min((int64_t)(u_in + count) * d.unit, (int64_t)lim_high);
         uint32_t kw[2][kKeyBytes / 4], vw[2][kValBytes], kgrid[2][kGridRegs], vgrid[2][kGridRegs];
         int page[2];
         // Tokens of a half that are in the cache; their first byte of codes over kRow.
         auto find = [&](int t0) {
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                page[half] = __builtin_amdgcn_readfirstlane(t0 + 16 * half < len ? page_of(a.s, b, t0 + 16 * half) : -1);
+                page[half] = __builtin_amdgcn_readfirstlane(t0 + 16 * half < len ? page_of(d.s, b, t0 + 16 * half) : -1);
         };
         auto first = [&](int t0, int half) {
-            const int at = (t0 + 16 * half) & ((1 << a.s.page_shift) - 1);
-            return (((int64_t)max(page[half], 0) * a.c.heads + h) << a.s.page_shift) + at;
+            const int at = (t0 + 16 * half) & ((1 << d.s.page_shift) - 1);
+            return (((int64_t)max(page[half], 0) * a.c.heads + h) << d.s.page_shift) + at;
         };
         auto load_keys = [&](int t0) {
 #pragma unroll
@@ -351,17 +359,17 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             }
         };
 
-        int t0 = u_in * kUnit + wave * kTile;
+        int t0 = (int)min((int64_t)u_in * d.unit + wave * kTile, (int64_t)t_end);
         if (t0 < t_end) {
             find(t0);
             load_keys(t0);
             load_values(t0);
         }
-        for (; t0 < t_end; t0 += kUnit) {
+        for (; t0 < t_end; t0 += kStep) {
             // The next step's keys are asked for as soon as this one's are in the products,
             // its values once this one's are: both are under way during half a step, with no
             // registers but their own.
-            const int next = t0 + kUnit < t_end ? t0 + kUnit : t0;
+            const int next = t0 + kStep < t_end ? t0 + kStep : t0;
             int good[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -427,13 +435,13 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
                     // m moves up to the largest score, or at first to it wherever it is
-                    const float d = top > fminf(above[t], 0.f) ? top : 0.f;
-                    const float f = above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-d);
+                    const float up = top > fminf(above[t], 0.f) ? top : 0.f;
+                    const float f = above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-up);
                     if (top > -INFINITY) above[t] = kSlack;
-                    m[t] += d;
+                    m[t] += up;
                     l[t] *= f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[t][i] -= d;
+                    for (int i = 0; i < 8; ++i) s[t][i] -= up;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) bsum[t][g] *= f;
 #pragma unroll
@@ -547,7 +555,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                                 fmaf(o[t][g * (G / 16) + jj][i], unstep, bsum[t][g]);
                 __syncthreads();
                 for (int x = threadIdx.x; x < 16 * kPart / 4; x += kAttnThreads) {
-                    const int r = x / (kPart / 4), d = x % (kPart / 4) * 4, row = row0 + 16 * t + r;
+                    const int r = x / (kPart / 4), e0 = d0 + x % (kPart / 4) * 4, row = row0 + 16 * t + r;
                     if (row >= n_rows) break;
                     float mk[kWaves], top = -INFINITY, all = 0.f;
 #pragma unroll
@@ -561,32 +569,32 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                         if (mk[k] == -INFINITY) continue;
                         const float f = __builtin_amdgcn_exp2f(mk[k] - top);
                         all = fmaf(f, ml[(k * kRows + 16 * t + r) * 2 + 1], all);
-                        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (k * 16 + r) * kStride + d);
+                        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (k * 16 + r) * kStride + e0 - d0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sum[e] = fmaf(f, v[e], sum[e]);
                     }
                     float *to_o, *to_ml;
                     int64_t at;
                     if (!whole) {
-                        at = ((int64_t)h * 2 * W + slot) * kRows + 16 * t + r;
-                        to_o = a.side.slot_o;
-                        to_ml = a.side.slot_ml;
+                        at = ((int64_t)h * 2 * d.workers + slot) * kRows + 16 * t + r;
+                        to_o = d.slot_o;
+                        to_ml = d.slot_ml;
                     } else {
-                        at = (int64_t)h * a.s.n_tokens * a.per + (int64_t)rows.begin * a.per + row;
-                        to_o = a.side.row_o;
-                        to_ml = a.side.row_ml;
+                        at = (int64_t)h * d.s.n_tokens * a.per + (int64_t)rows.begin * a.per + row;
+                        to_o = d.row_o;
+                        to_ml = d.row_ml;
                     }
                     if (to_o) {
-                        *reinterpret_cast<f32x4 *>(to_o + at * D + d0 + d) = sum;
-                        if (d0 + d == 0) *reinterpret_cast<f32x2 *>(to_ml + at * 2) = f32x2{top, all};
+                        *reinterpret_cast<f32x4 *>(to_o + at * D + e0) = sum;
+                        if (e0 == 0) *reinterpret_cast<f32x2 *>(to_ml + at * 2) = f32x2{top, all};
                         continue;
                     }
                     const float inv = all > 0.f ? 1.f / all : 0.f;
                     const int tok = rows.begin + row / a.per, hq = h * a.per + row % a.per;
                     const uint2 packed = {from_f32<T>(sum[0] * inv) | from_f32<T>(sum[1] * inv) << 16,
                                           from_f32<T>(sum[2] * inv) | from_f32<T>(sum[3] * inv) << 16};
-                    *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + d0 + d) = packed;
-                    if (a.lse && d0 + d == 0)
+                    *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + e0) = packed;
+                    if (a.lse && e0 == 0)
                         a.lse[(int64_t)tok * a.c.heads * a.per + hq] =
                             all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
                 }
@@ -599,19 +607,20 @@ template <typename T, int NB, int D, int G, int RT>
 hipError_t launch_one(const AttnArgs &a, hipStream_t stream)
 {
     // at most 16 KB of starts, 1 KB and 33 KB: within what any launch may ask for
-    const int part = D < 128 ? D : 128;
-    const size_t lds = 4 * (((size_t)a.s.n_seqs + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
+    const int part = D < 128 ? D : 128, n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
+    const size_t lds = 4 * (((size_t)n + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
                        4 * (size_t)kWaves * 16 * (part + 4);
-    attn_kernel<T, NB, D, G, RT><<<dim3((unsigned)a.side.workers * a.c.heads), kAttnThreads, lds, stream>>>(a);
+    const int64_t runs = a.side[0].workers + (a.sides == 2 ? a.side[1].workers : 0);
+    attn_kernel<T, NB, D, G, RT><<<dim3((unsigned)(runs * a.c.heads)), kAttnThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, int NB, int D, int G>
 hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
-    if (a.side.tiles16 == 1) return launch_one<T, NB, D, G, 1>(a, stream);
+    if (a.side[0].tiles16 == 1) return launch_one<T, NB, D, G, 1>(a, stream);
     if constexpr (D <= 128)
-        if (a.side.tiles16 == 2) return launch_one<T, NB, D, G, 2>(a, stream);
+        if (a.side[0].tiles16 == 2) return launch_one<T, NB, D, G, 2>(a, stream);
     return hipErrorInvalidValue;
 }
 

@@ -93,20 +93,29 @@ HQQ_HD int32_t v_row_at(int32_t t, int32_t r, int32_t dim, int32_t nbits)
 }
 
 // ---- attention: units of work and who does them ---------------------------------------------
-// A key/value head's work is a list of items, one per sequence and tile of `rows_per` of its
-// query rows, each of ceil(length / kUnit) units along its sequence. The units of all items,
-// end to end, are dealt to `workers` equal runs, so that one long sequence among short ones
-// is spread as evenly as a uniform batch.
-constexpr int kUnit = 128;      // tokens of a unit
+// A key/value head's work is a list of items, one per sequence and tile of query rows, each of
+// ceil(length / unit) units along its sequence, one at least (an item that sees nothing still
+// writes its rows). The units of all items, end to end, are dealt in equal runs to as many
+// workers as there are, or as there are units: one long sequence among short ones is spread as
+// evenly as a uniform batch.
+constexpr int kStep = 128;      // tokens of a block's step; a unit is a multiple of it
 
-HQQ_HD int32_t units_along(int32_t len) { return (len + kUnit - 1) / kUnit; }
+HQQ_HD int32_t units_along(int32_t len, int32_t unit)
+{
+    return len <= unit ? 1 : (int32_t)(((int64_t)len + unit - 1) / unit);
+}
 
-HQQ_HD int32_t tiles_of(int32_t rows, int32_t rows_per) { return (rows + rows_per - 1) / rows_per; }
+HQQ_HD int32_t tiles_of(int32_t rows, int32_t rows_per)
+{
+    return (int32_t)(((int64_t)rows + rows_per - 1) / rows_per);
+}
 
-// First unit of worker w of W over U units; worker that has unit u.
+HQQ_HD int32_t runs_of(int32_t workers, int32_t units) { return workers < units ? workers : units; }
+
+// First unit of run w of W over U units; run that has unit u. 1 <= W <= U: no run is empty.
 HQQ_HD int32_t first_unit(int32_t w, int32_t W, int32_t U) { return (int32_t)((int64_t)w * U / W); }
 
-HQQ_HD int32_t worker_of(int32_t u, int32_t W, int32_t U)
+HQQ_HD int32_t run_of(int32_t u, int32_t W, int32_t U)
 {
     return (int32_t)((((int64_t)u + 1) * W - 1) / U);
 }

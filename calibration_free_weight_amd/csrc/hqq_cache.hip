@@ -10,27 +10,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The sequence of the call's row `i` (uniform over a wave's first row, then walked): the
-// wave looks for the first of its rows 64 entries at a time, each lane on from there.
-__device__ __forceinline__ int find_seq(const SeqView &s, int i)
-{
-    if (!s.cu) return seq_at(s, i);
-    const int lane = threadIdx.x & 63;
-    const int first = __builtin_amdgcn_readfirstlane(i);
-    // entries (cu[0], cu[n_seqs]) at a stride, narrowed 64-fold per turn; n_seqs <= 4096
-    int lo = 0, n = s.n_seqs;               // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 63) >> 6;
-        const int at = lo + lane * step;
-        const bool le = lane == 0 || (lane * step < n && s.cu[at] <= first);
-        const int k = __popcll(__ballot(le)) - 1;
-        n = min(step, n - k * step);
-        lo += k * step;
-    }
-    while (lo + 1 < s.n_seqs && s.cu[lo + 1] <= i) ++lo;
-    return lo;
-}
-
 // Whether row i belongs to a sequence, and where its token lies: page (or -1), token of it.
 struct Slot {
     bool mine;

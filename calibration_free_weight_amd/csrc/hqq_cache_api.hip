@@ -49,8 +49,8 @@ hqq_status check_seqs(const hqq_cache *c, const hqq_seqs *s)
     if (s->n_seqs < 0 || s->n_seqs > hqq::kMaxSeqs) return refuse("seqs: n_seqs must be in [0, 4096]");
     if (s->n_tokens < 0 || s->n_tokens > (1 << 24)) return refuse("seqs: n_tokens must be in [0, 2^24]");
     if (s->n_tokens * c->n_heads > INT32_MAX) return refuse("seqs: n_tokens * n_heads must be below 2^31");
-    if (s->max_pages < 0 || (int64_t)s->max_pages * c->page_size > INT32_MAX)
-        return refuse("seqs: max_pages * page_size must be in [0, 2^31)");
+    if (s->max_pages < 0 || (int64_t)s->max_pages * c->page_size > (1 << 30))
+        return refuse("seqs: max_pages * page_size must be in [0, 2^30]");
     if (s->n_seqs == 0 || s->n_tokens == 0) return HQQ_OK;
     if ((!s->table && s->max_pages > 0) || !s->lens) return refuse("seqs: table and lens must be non-null");
     if (!aligned(s->table, 4) || !aligned(s->lens, 4) || !aligned(s->cu_tokens, 4))
@@ -111,8 +111,8 @@ hqq_status cache_rows(bool write, const hqq_cache *cache, const hqq_seqs *seqs, 
 // ---- attention --------------------------------------------------------------------------------
 // How one side's work is cut, and where its partial results lie in the workspace.
 struct SidePlan {
-    int tiles16, workers;
-    size_t starts, slot_o, slot_ml, row_o, row_ml;      // offsets; row_* only with a prefix
+    int tiles16, workers, unit;
+    size_t starts, slot_o, slot_ml, row_o, row_ml;      // offsets; row_* with two sides
 };
 
 struct Plan {
@@ -128,12 +128,9 @@ int tiles_for(int64_t rows, int dim)
     return rows <= 16 || dim == 256 ? 1 : 2;
 }
 
-// Blocks of a launch: what the 256 CUs hold at once.
-int workers_for(int tiles16, int heads)
-{
-    const int blocks = tiles16 == 1 ? 768 : 512;
-    return (blocks + heads - 1) / heads;
-}
+// The longest side that one block takes alone: cutting it saves four steps at most, and
+// joining the pieces costs a launch.
+constexpr int64_t kWhole = 512;
 
 Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefix_len)
 {
@@ -146,22 +143,28 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         at += (n + 255) / 256 * 256;
         return was;
     };
-    auto side = [&](int64_t tile_rows, int n_seqs, bool keep_rows) {
+    auto side = [&](int64_t tile_rows, int n_seqs, int64_t longest) {
         SidePlan x{};
         x.tiles16 = tiles_for(tile_rows, c->head_dim);
-        x.workers = workers_for(x.tiles16, c->n_heads);
+        const int64_t step = hqq::kStep;
+        x.unit = (int)(longest <= kWhole ? (longest + step) / step * step : step);
+        // what the 256 CUs hold at once, or the most units that there can be
+        const int64_t blocks = x.tiles16 == 1 ? 768 : 512;
+        const int64_t units = (rows / (16 * x.tiles16) + n_seqs) * hqq::units_along((int32_t)longest, x.unit);
+        const int64_t each = (blocks + c->n_heads - 1) / c->n_heads;
+        x.workers = (int)(each < units ? each : units);
         const size_t slots = (size_t)c->n_heads * 2 * x.workers * 16 * x.tiles16;
         x.starts = take(4 * ((size_t)n_seqs + 1));
         x.slot_o = take(slots * c->head_dim * 4);
         x.slot_ml = take(slots * 8);
-        if (keep_rows) {
+        if (prefix_len > 0) {
             x.row_o = take((size_t)c->n_heads * rows * c->head_dim * 4);
             x.row_ml = take((size_t)c->n_heads * rows * 8);
         }
         return x;
     };
-    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, prefix_len > 0);
-    if (prefix_len > 0) p.prefix = side(rows, 1, true);
+    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, (int64_t)s->max_pages * c->page_size);
+    if (prefix_len > 0) p.prefix = side(rows, 1, prefix_len);
     p.bytes = at;
     return p;
 }
@@ -176,24 +179,24 @@ hqq_status check_plan(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int6
         return refuse("n_q_heads must be a positive multiple of the cache's n_heads");
     if (s->n_tokens * n_q_heads > INT32_MAX || n_q_heads > (1 << 20))
         return refuse("n_tokens * n_q_heads must be below 2^31");
-    if (prefix_len < 0 || prefix_len > INT32_MAX) return refuse("prefix_len must be in [0, 2^31)");
+    if (prefix_len < 0 || prefix_len > (1 << 30)) return refuse("prefix_len must be in [0, 2^30]");
     *empty = s->n_seqs == 0 || s->n_tokens == 0;
     if (*empty) return HQQ_OK;
     // units of work are counted in 32 bits
     const int64_t tiles = s->n_tokens * (n_q_heads / c->n_heads) / 16 + s->n_seqs;
     const int64_t longest = (int64_t)s->max_pages * c->page_size;
     const int64_t far = longest > prefix_len ? longest : prefix_len;
-    if (tiles > INT32_MAX / (far / hqq::kUnit + 1))
+    if (tiles > INT32_MAX / (far / hqq::kStep + 1))
         return refuse("too many rows over too long sequences for one call", HQQ_ERR_UNSUPPORTED);
     return HQQ_OK;
 }
 
-hqq::AttnSide side_at(const SidePlan &p, char *ws, bool keep_rows)
+hqq::AttnSide side_at(const hqq::SeqView &s, const SidePlan &p, char *ws, bool two, bool causal)
 {
     auto f = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
-    return hqq::AttnSide{reinterpret_cast<int32_t *>(ws + p.starts), f(p.slot_o), f(p.slot_ml),
-                         keep_rows ? f(p.row_o) : nullptr, keep_rows ? f(p.row_ml) : nullptr,
-                         p.workers, p.tiles16};
+    return hqq::AttnSide{s, reinterpret_cast<int32_t *>(ws + p.starts), f(p.slot_o), f(p.slot_ml),
+                         two ? f(p.row_o) : nullptr, two ? f(p.row_ml) : nullptr,
+                         p.workers, p.unit, p.tiles16, causal};
 }
 
 }  // namespace
@@ -231,9 +234,9 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     bool empty;
     hqq_status st = check_plan(cache, seqs, n_q_heads, prefix_len, &empty);
     if (st != HQQ_OK) return st;
-    if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * cache->page_size > INT32_MAX ||
+    if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * cache->page_size > (1 << 30) ||
         prefix_len > (int64_t)n_prefix_pages * cache->page_size)
-        return refuse("prefix_len must be at most n_prefix_pages * page_size, and that below 2^31");
+        return refuse("prefix_len must be at most n_prefix_pages * page_size, and that at most 2^30");
     if (prefix_len > 0 && (!prefix_pages || !aligned(prefix_pages, 4)))
         return refuse("prefix_pages must be non-null and 4-byte aligned");
     if (!std::isfinite(scale)) return refuse("scale must be finite");
@@ -255,8 +258,8 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     const hqq::AttnShape shape{cache->head_dim, cache->nbits, cache->group_size, cache->dtype == HQQ_BF16};
     hqq::AttnArgs a{};
     a.c = view_of(cache);
-    a.s = view_of(cache, seqs);
-    a.side = side_at(p.own, ws, shared);
+    a.side[0] = side_at(view_of(cache, seqs), p.own, ws, shared, true);
+    a.sides = 1;
     a.q = static_cast<const uint16_t *>(q);
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
@@ -265,27 +268,28 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     a.o_ts = out_token_stride;
     a.o_hs = out_head_stride;
     a.per = n_q_heads / cache->n_heads;
-    a.causal = 1;
     a.scale = scale * 1.44269504088896341f;
-    hqq::JoinArgs j{a.s, a.side, {}, a.out, lse, a.o_ts, a.o_hs, a.per, cache->n_heads, cache->head_dim, 0};
+    hqq::JoinArgs j{{a.side[0], {}}, 1, a.out, lse, a.o_ts, a.o_hs, a.per, cache->n_heads, cache->head_dim};
+    hipError_t e = hipSuccess;
     if (shared) {
         // the prefix is one sequence whose rows are all rows of the call
-        hqq::AttnArgs b = a;
-        b.s.table = prefix_pages;
-        b.s.lens = nullptr;
-        b.s.cu = nullptr;
-        b.s.n_seqs = 1;
-        b.s.max_pages = n_prefix_pages;
-        b.s.fixed_len = (int32_t)prefix_len;
-        b.side = side_at(p.prefix, ws, true);
-        b.causal = 0;
-        j.prefix = b.side;
-        j.prefix_len = b.s.fixed_len;
-        const hipError_t e = hqq::launch_attn(b, shape, str);
-        if (e != hipSuccess) return done(e);
+        const hqq::SeqView all{prefix_pages, nullptr, nullptr, 1, n_prefix_pages, (int32_t)seqs->n_tokens,
+                               (int32_t)prefix_len, log2_of(cache->page_size), (int32_t)cache->n_pages};
+        j.side[1] = side_at(all, p.prefix, ws, true, false);
+        j.sides = 2;
+        if (p.own.tiles16 == p.prefix.tiles16) {
+            a.side[1] = j.side[1];          // one launch for both
+            a.sides = 2;
+        } else {
+            hqq::AttnArgs first = a;
+            first.side[0] = j.side[1];
+            e = hqq::launch_attn(first, shape, str);
+        }
     }
-    hipError_t e = hqq::launch_attn(a, shape, str);
-    if (e == hipSuccess) e = hqq::launch_join(j, shape.bf16, str);
+    if (e == hipSuccess) e = hqq::launch_attn(a, shape, str);
+    // without a prefix, and with sequences that are never cut, every row has been written
+    const bool cut = (int64_t)seqs->max_pages * cache->page_size > p.own.unit;
+    if (e == hipSuccess && (shared || cut)) e = hqq::launch_join(j, shape.bf16, str);
     return done(e);
 }
 

@@ -60,45 +60,67 @@ __device__ __forceinline__ void unpack8(const uint4 raw, float (&v)[8])
     }
 }
 
+// The sequence of the call's row `i`, which is the wave's first row or close behind it: the
+// wave looks for the first together, 64 entries at a time, and each lane goes on from there.
+// All lanes of the wave must come here.
+__device__ __forceinline__ int find_seq(const SeqView &s, int i)
+{
+    if (!s.cu) return seq_at(s, i);
+    const int lane = threadIdx.x & 63;
+    const int first = __builtin_amdgcn_readfirstlane(i);
+    int lo = 0, n = s.n_seqs;               // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) >> 6;
+        const bool le = lane == 0 || (lane * step < n && s.cu[lo + lane * step] <= first);
+        const int k = __popcll(__ballot(le)) - 1;
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    while (lo + 1 < s.n_seqs && s.cu[lo + 1] <= i) ++lo;
+    return lo;
+}
+
 // write: k and v rows into the cache; else back out of it. dim 64/128/256, nbits 4/8, g
 // 32/64/128 <= dim.
 hipError_t launch_cache_rows(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p,
                              int dim, int nbits, int g, bool bf16, hipStream_t stream);
 
 // ---- attention ---------------------------------------------------------------------------------
-// Partial results of one side (the sequences, or the shared prefix) in the workspace. A worker
-// leaves at most two pieces of split items: slot 2w for one that began before its run, 2w + 1
-// for one that goes on behind it. Whole items go to the output, or with a prefix to `rows`.
+// What the rows of a call attend to comes from one or two sides: the sequences, and a prefix
+// that all share (one sequence with all rows of the call). A run leaves at most two pieces of
+// split items in the workspace: slot 2w for one that began before the run, 2w + 1 for one that
+// goes on behind it. Whole items go to the output, or with two sides to `row_o`.
 struct AttnSide {
+    SeqView s;
     int32_t *starts;            // [n_seqs + 1]: units before each sequence's, of one head
     float *slot_o;              // [heads][2 * workers][rows_per][dim], not divided by the sum
     float *slot_ml;             // [heads][2 * workers][rows_per][2]: maximum (base 2), sum
     float *row_o, *row_ml;      // [heads][n_tokens * per][dim], [..][2], or null
-    int32_t workers;            // runs of a head's units
+    int32_t workers;            // most runs of a head's units
+    int32_t unit;               // tokens
     int32_t tiles16;            // rows_per / 16: 1 or 2
+    int32_t causal;             // rows see their own position and what is before it, else all
 };
 
 struct AttnArgs {
     CacheView c;
-    SeqView s;
-    AttnSide side;
+    AttnSide side[2];           // of the same tiles16
+    int32_t sides;              // in this launch
     const uint16_t *q;
     uint16_t *out;
     float *lse;                 // nullable
     int64_t q_ts, q_hs, o_ts, o_hs;
     int32_t per;                // query heads to a key/value head
-    int32_t causal;             // rows see their own position and what is before it, else all
     float scale;                // times log2(e)
 };
 
 struct JoinArgs {
-    SeqView s;                  // the call's sequences
-    AttnSide side, prefix;      // prefix.starts null: none
+    AttnSide side[2];           // the sequences; the prefix
+    int32_t sides;
     uint16_t *out;
     float *lse;
     int64_t o_ts, o_hs;
     int32_t per, heads, dim;
-    int32_t prefix_len;
 };
 
 struct AttnShape {

@@ -343,7 +343,7 @@ typedef struct hqq_seqs {
     const int32_t *lens;     /* [n_seqs]: tokens of each sequence, the call's included     */
     const int32_t *cu_tokens;/* [n_seqs + 1], or NULL                                      */
     int n_seqs;              /* 0..4096                                                    */
-    int max_pages;           /* max_pages * page_size < 2^31                               */
+    int max_pages;           /* max_pages * page_size <= 2^30                              */
     int64_t n_tokens;        /* rows of the call's tensors, 0..2^24                        */
 } hqq_seqs;
 
@@ -381,7 +381,7 @@ hqq_status hqq_cache_attention(const hqq_cache *cache, const hqq_seqs *seqs, con
  * pages prefix_pages (device, int32 [n_prefix_pages], in order, of the same cache) hold them
  * once, and every row sees all of them before what it sees of its own sequence, whose
  * positions and lens count behind the prefix. The prefix is read once for all rows.
- * 0 <= prefix_len <= n_prefix_pages * page_size < 2^31; 0 is hqq_cache_attention. */
+ * 0 <= prefix_len <= n_prefix_pages * page_size <= 2^30; 0 is hqq_cache_attention. */
 hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *seqs,
                                       const int32_t *prefix_pages, int n_prefix_pages,
                                       int64_t prefix_len, const void *q, int64_t q_token_stride,

@@ -145,11 +145,15 @@ int main()
         }
     }
     for (int round = 0; round < 200000; ++round) {
-        // runs: every unit has one worker, whose run holds it
-        const int U = 1 + r() % (round % 3 ? 300 : 2000000000), W = 1 + r() % 2000;
-        const int u = r() % U, w = worker_of(u, W, U);
-        need(w >= 0 && w < W && first_unit(w, W, U) <= u && u < first_unit(w + 1, W, U), "a unit's worker");
+        // runs: every unit is in one, and none is empty
+        const int U = 1 + r() % (round % 3 ? 300 : 2000000000), W = runs_of(1 + r() % 2000, U);
+        const int u = r() % U, w = run_of(u, W, U), any_run = r() % W;
+        need(w >= 0 && w < W && first_unit(w, W, U) <= u && u < first_unit(w + 1, W, U), "a unit's run");
         need(first_unit(0, W, U) == 0 && first_unit(W, W, U) == U, "all units");
+        need(first_unit(any_run, W, U) < first_unit(any_run + 1, W, U), "no empty run");
+        const int len = r() % 2 ? (int)(r() % 1000) : INT32_MAX - (int)(r() % 1000), unit = 128 << r() % 4;
+        const int n = units_along(len, unit);
+        need(n >= 1 && (int64_t)n * unit >= len && (n == 1 || (int64_t)(n - 1) * unit < len), "units of a length");
     }
     for (int dim : {64, 128, 256}) for (int nbits : {4, 8}) {
         const int page = 64, bytes = page * dim * nbits / 8;
