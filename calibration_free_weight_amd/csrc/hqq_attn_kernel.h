@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
 
     lay_out<kRows>(d, a.per, starts, scan);
     const int h = (int)(block % (unsigned)a.c.heads), w = (int)(block / (unsigned)a.c.heads);
-    if (block == 0)
+    if (block == 0 && d.starts)
         for (int b = threadIdx.x; b <= d.s.n_seqs; b += kAttnThreads) d.starts[b] = starts[b];
     const int U = __builtin_amdgcn_readfirstlane(starts[d.s.n_seqs]), W = runs_of(d.workers, U);
     if (w >= W) return;

@@ -117,6 +117,7 @@ struct SidePlan {
 
 struct Plan {
     SidePlan own, prefix;
+    bool join;                  // pieces or two sides are put together; else no workspace
     size_t bytes;
 };
 
@@ -163,9 +164,11 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         }
         return x;
     };
-    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, (int64_t)s->max_pages * c->page_size);
+    const int64_t longest = (int64_t)s->max_pages * c->page_size;
+    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, longest);
     if (prefix_len > 0) p.prefix = side(rows, 1, prefix_len);
-    p.bytes = at;
+    p.join = prefix_len > 0 || longest > p.own.unit;
+    p.bytes = p.join ? at : 0;
     return p;
 }
 
@@ -249,9 +252,9 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     if (st != HQQ_OK) return st;
     if (lse && !aligned(lse, 4)) return refuse("lse must be 4-byte aligned");
     const Plan p = plan_of(cache, seqs, n_q_heads, prefix_len);
-    if (!workspace || workspace_bytes < p.bytes)
+    if (p.join && (!workspace || workspace_bytes < p.bytes))
         return refuse("workspace missing or smaller than hqq_cache_attention_workspace()", HQQ_ERR_WORKSPACE);
-    if (!aligned(workspace, 256)) return refuse("workspace must be 256-byte aligned");
+    if (p.join && !aligned(workspace, 256)) return refuse("workspace must be 256-byte aligned");
     char *ws = static_cast<char *>(workspace);
     const bool shared = prefix_len > 0;
     const hipStream_t str = static_cast<hipStream_t>(stream);
@@ -259,6 +262,7 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     hqq::AttnArgs a{};
     a.c = view_of(cache);
     a.side[0] = side_at(view_of(cache, seqs), p.own, ws, shared, true);
+    if (!p.join) a.side[0].starts = nullptr;
     a.sides = 1;
     a.q = static_cast<const uint16_t *>(q);
     a.out = static_cast<uint16_t *>(out);
@@ -287,9 +291,7 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
         }
     }
     if (e == hipSuccess) e = hqq::launch_attn(a, shape, str);
-    // without a prefix, and with sequences that are never cut, every row has been written
-    const bool cut = (int64_t)seqs->max_pages * cache->page_size > p.own.unit;
-    if (e == hipSuccess && (shared || cut)) e = hqq::launch_join(j, shape.bf16, str);
+    if (e == hipSuccess && p.join) e = hqq::launch_join(j, shape.bf16, str);
     return done(e);
 }
 

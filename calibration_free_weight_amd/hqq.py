@@ -325,84 +325,92 @@ def hqq_unpack(packed, n_codes, nbits, codes, stream=None) -> None:
 # nbits, group_size. table: int32 [n_seqs, max_pages]; lens: int32 [n_seqs]; cu_tokens: int32
 # [n_seqs + 1] or None. Rows are [n_tokens, heads, head_dim] with contiguous dimensions. The
 # calls run on the current stream of the cache's device unless `stream` is given.
-def _require(ok, msg):
-    if not ok:
-        raise HQQError(HQQ_ERR_ARG, msg)
+_torch = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _bad(msg):
+    return HQQError(HQQ_ERR_ARG, msg)
 
 
 def _cache_struct(cache):
-    import torch
-    kc, vc, km, vm = (cache[x] for x in ("k_codes", "v_codes", "k_meta", "v_meta"))
+    """The C struct of a cache dict, its GPU's index and its type."""
+    T = _torch or _th()
+    kc, vc, km, vm = cache["k_codes"], cache["v_codes"], cache["k_meta"], cache["v_meta"]
     page, heads, dim = cache["page_size"], cache["n_heads"], cache["head_dim"]
     nbits, group = cache["nbits"], cache["group_size"]
-    n, dev, dtype = kc.shape[0], kc.device, km.dtype
-    codes, meta = (n, heads, page * dim * nbits // 8), (n, heads, page, dim // max(group, 1), 2)
-    _require(kc.shape == codes and vc.shape == codes and kc.dtype == vc.dtype == torch.uint8,
-             "k_codes and v_codes must be uint8 [n_pages, n_heads, page_size*head_dim*nbits/8]")
-    _require(km.shape == meta and vm.shape == meta and vm.dtype == dtype and
-             dtype in (torch.float16, torch.bfloat16),
-             "k_meta and v_meta must be [n_pages, n_heads, page_size, head_dim/group_size, 2] "
-             "of float16 or bfloat16")
-    _require(kc.is_contiguous() and vc.is_contiguous() and km.is_contiguous() and vm.is_contiguous(),
-             "the cache's tensors must be contiguous")
-    _require(kc.is_cuda and dev == vc.device == km.device == vm.device,
-             "the cache's tensors must be on one GPU")
+    codes, meta, dtype, dev = kc.shape, km.shape, km.dtype, kc.get_device()
+    n = codes[0]
+    if codes != (n, heads, page * dim * nbits // 8) or vc.shape != codes or \
+            not kc.dtype == vc.dtype == T.uint8:
+        raise _bad("k_codes and v_codes must be uint8 [n_pages, n_heads, page_size*head_dim*nbits/8]")
+    if meta != (n, heads, page, dim // max(group, 1), 2) or vm.shape != meta or vm.dtype != dtype or \
+            (dtype != T.float16 and dtype != T.bfloat16):
+        raise _bad("k_meta and v_meta must be [n_pages, n_heads, page_size, head_dim/group_size, 2] "
+                   "of float16 or bfloat16")
+    if not (kc.is_contiguous() and vc.is_contiguous() and km.is_contiguous() and vm.is_contiguous()):
+        raise _bad("the cache's tensors must be contiguous")
+    if dev < 0 or not dev == vc.get_device() == km.get_device() == vm.get_device():
+        raise _bad("the cache's tensors must be on one GPU")
     return hqq_cache(kc.data_ptr(), vc.data_ptr(), km.data_ptr(), vm.data_ptr(), n, page, heads,
-                     dim, nbits, group, HQQ_BF16 if dtype == torch.bfloat16 else HQQ_F16), dev, dtype
+                     dim, nbits, group, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16), dev, dtype
 
 
 def _seqs_struct(table, lens, cu_tokens, n_tokens, dev):
-    import torch
-    _require(table.dim() == 2 and table.is_contiguous() and table.dtype == torch.int32 and table.device == dev,
-             "table must be a contiguous int32 [n_seqs, max_pages] on the cache's device")
-    n = table.shape[0]
-    _require(lens.shape == (n,) and lens.dtype == torch.int32 and lens.is_contiguous() and lens.device == dev,
-             "lens must be a contiguous int32 [n_seqs] on the cache's device")
+    i32 = _torch.int32
+    shape = table.shape
+    if len(shape) != 2 or table.dtype != i32 or table.get_device() != dev or not table.is_contiguous():
+        raise _bad("table must be a contiguous int32 [n_seqs, max_pages] on the cache's device")
+    n = shape[0]
+    if lens.shape != (n,) or lens.dtype != i32 or lens.get_device() != dev or not lens.is_contiguous():
+        raise _bad("lens must be a contiguous int32 [n_seqs] on the cache's device")
+    cu = None
     if cu_tokens is not None:
-        _require(cu_tokens.shape == (n + 1,) and cu_tokens.dtype == torch.int32 and
-                 cu_tokens.is_contiguous() and cu_tokens.device == dev,
-                 "cu_tokens must be a contiguous int32 [n_seqs + 1] on the cache's device")
-    return hqq_seqs(table.data_ptr(), lens.data_ptr(), None if cu_tokens is None else cu_tokens.data_ptr(),
-                    n, table.shape[1], n_tokens)
+        if cu_tokens.shape != (n + 1,) or cu_tokens.dtype != i32 or cu_tokens.get_device() != dev or \
+                not cu_tokens.is_contiguous():
+            raise _bad("cu_tokens must be a contiguous int32 [n_seqs + 1] on the cache's device")
+        cu = cu_tokens.data_ptr()
+    return hqq_seqs(table.data_ptr(), lens.data_ptr(), cu, n, shape[1], n_tokens)
 
 
-def _rows(x, n_tokens, heads, dim, dev, dtype, name):
-    shape = x.shape
-    _require(len(shape) == 3 and shape[0] == n_tokens and (heads is None or shape[1] == heads) and
-             shape[2] == dim and x.stride(2) == 1 and x.dtype == dtype and x.device == dev,
-             f"{name} must be [n_tokens, heads, head_dim] with contiguous dimensions, of the "
-             "cache's type and device")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+def _rows(x, shape, dev, dtype, name):
+    """Pointer and strides of rows; a strided dimension of one element may have any stride."""
+    if x.shape != shape or x.dtype != dtype or x.get_device() != dev:
+        raise _bad(f"{name} must be [n_tokens, heads, head_dim] of the cache's sizes, type and device")
+    ts, hs, ds = x.stride()
+    if ds != 1:
+        raise _bad(f"{name} must have contiguous dimensions")
+    return x.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0
 
 
-class _on:
-    """Makes a device current for a call, where it is not; gives the call's stream."""
+def _on(dev, fn, *args):
+    """The status of fn(*args) with `dev` as the current GPU."""
+    if _torch.cuda.current_device() == dev:
+        return fn(*args)
+    with _torch.cuda.device(dev):
+        return fn(*args)
 
-    def __init__(self, dev, stream):
-        import torch
-        self.guard = None
-        if torch.cuda.current_device() != dev.index:
-            self.guard = torch.cuda.device(dev)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return C.c_void_p(int(self.stream))
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _stream_of(dev, stream):
+    return int(stream) if stream is not None else _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _cache_rows(fn, cache, table, lens, k, v, cu_tokens, stream):
     c, dev, dtype = _cache_struct(cache)
-    n = k.shape[0]
-    s = _seqs_struct(table, lens, cu_tokens, n, dev)
-    kr = _rows(k, n, c.n_heads, c.head_dim, dev, dtype, "k")
-    vr = _rows(v, n, c.n_heads, c.head_dim, dev, dtype, "v")
-    with _on(dev, stream) as st:
-        _check(fn(C.byref(c), C.byref(s), *kr, *vr, st))
+    shape = (k.shape[0], c.n_heads, c.head_dim)
+    s = _seqs_struct(table, lens, cu_tokens, shape[0], dev)
+    kp, kt, kh = _rows(k, shape, dev, dtype, "k")
+    vp, vt, vh = _rows(v, shape, dev, dtype, "v")
+    st = _on(dev, fn, c, s, kp, kt, kh, vp, vt, vh, _stream_of(dev, stream))
+    if st:
+        _check(st)
 
 
 def hqq_cache_write(cache, table, lens, k, v, cu_tokens=None, stream=None) -> None:
@@ -416,50 +424,57 @@ def hqq_cache_read(cache, table, lens, k, v, cu_tokens=None, stream=None) -> Non
     _cache_rows(lib().hqq_cache_read, cache, table, lens, k, v, cu_tokens, stream)
 
 
-def _attention_args(cache, table, lens, q, cu_tokens):
-    c, dev, dtype = _cache_struct(cache)
-    s = _seqs_struct(table, lens, cu_tokens, q.shape[0], dev)
-    return c, s, _rows(q, q.shape[0], None, c.head_dim, dev, dtype, "q"), dev, dtype
-
-
 def hqq_cache_attention_workspace(cache, table, lens, n_tokens, n_q_heads, prefix_len=0, cu_tokens=None) -> int:
     """Workspace bytes of an attention call of these sizes."""
     c, dev, _ = _cache_struct(cache)
     s = _seqs_struct(table, lens, cu_tokens, n_tokens, dev)
-    n = int(lib().hqq_cache_attention_workspace(C.byref(c), C.byref(s), n_q_heads, prefix_len))
+    n = int(lib().hqq_cache_attention_workspace(c, s, n_q_heads, prefix_len))
     if n == 0 and hqq_last_error():
-        raise HQQError(HQQ_ERR_ARG, hqq_last_error())
+        raise _bad(hqq_last_error())
     return n
 
 
+def _scratch(n, dev, stream):
+    """Scratch memory of a call, from the allocator's pool of the stream that it runs on."""
+    T = _torch
+    if stream is None or int(stream) == T._C._cuda_getCurrentRawStream(dev):
+        return T.empty(n, dtype=T.uint8, device=dev)
+    with T.cuda.stream(T.cuda.ExternalStream(int(stream), device=dev)):
+        return T.empty(n, dtype=T.uint8, device=dev)
+
+
 def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream):
-    import torch
-    c, s, qr, dev, dtype = _attention_args(cache, table, lens, q, cu_tokens)
-    n, heads, dim = q.shape
+    T = _torch or _th()
+    c, dev, dtype = _cache_struct(cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != c.head_dim:
+        raise _bad("q must be [n_tokens, n_q_heads, head_dim]")
+    n, heads, dim = shape
+    s = _seqs_struct(table, lens, cu_tokens, n, dev)
+    qp, qt, qh = _rows(q, shape, dev, dtype, "q")
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=dtype, device=dev)
-    orow = _rows(out, n, heads, dim, dev, dtype, "out")
-    if lse is not None:
-        _require(lse.shape == (n, heads) and lse.dtype == torch.float32 and lse.is_contiguous() and
-                 lse.device == dev, "lse must be a contiguous float32 [n_tokens, n_q_heads]")
+        out = T.empty(shape, dtype=dtype, device=dev)
+    op, ot, oh = _rows(out, shape, dev, dtype, "out")
+    if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
+                            not lse.is_contiguous()):
+        raise _bad("lse must be a contiguous float32 [n_tokens, n_q_heads] on the cache's device")
     pages, n_pages = None, 0
     if prefix_pages is not None:
-        _require(prefix_pages.dim() == 1 and prefix_pages.dtype == torch.int32 and
-                 prefix_pages.is_contiguous() and prefix_pages.device == dev,
-                 "prefix_pages must be a contiguous int32 vector on the cache's device")
+        if prefix_pages.dim() != 1 or prefix_pages.dtype != T.int32 or prefix_pages.get_device() != dev or \
+                not prefix_pages.is_contiguous():
+            raise _bad("prefix_pages must be a contiguous int32 vector on the cache's device")
         pages, n_pages = prefix_pages.data_ptr(), prefix_pages.shape[0]
-    L = lib()
-    with _on(dev, stream) as st:
-        if workspace is None:
-            # from the allocator's pool of the stream that the call runs on
-            need = int(L.hqq_cache_attention_workspace(C.byref(c), C.byref(s), heads, prefix_len))
-            own = stream is None or int(stream) == torch.cuda.current_stream(dev).cuda_stream
-            with torch.cuda.stream(None if own else torch.cuda.ExternalStream(int(stream), device=dev)):
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        _check(L.hqq_cache_attention_prefix(
-            C.byref(c), C.byref(s), pages, n_pages, prefix_len, *qr, heads,
-            dim ** -0.5 if scale is None else scale, *orow, _p(lse), _p(workspace),
-            workspace.numel() * workspace.element_size(), st))
+    L = _L or lib()
+    if workspace is None:
+        need = L.hqq_cache_attention_workspace(c, s, heads, prefix_len)
+        if need:
+            workspace = _scratch(need, dev, stream)
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = _on(dev, L.hqq_cache_attention_prefix, c, s, pages, n_pages, prefix_len, qp, qt, qh, heads,
+             dim ** -0.5 if scale is None else scale, op, ot, oh, None if lse is None else lse.data_ptr(),
+             wp, wb, _stream_of(dev, stream))
+    if st:
+        _check(st)
     return out
 
 
@@ -494,11 +509,10 @@ def alloc_cache(n_pages, page_size, n_heads, head_dim, nbits=4, group_size=64, d
 
 def cache_read(cache, table, lens, n_tokens, cu_tokens=None, stream=None):
     """Allocate and fill (k, v) for the last tokens of the sequences, n_tokens in all."""
-    import torch
+    T = _torch or _th()
     km = cache["k_meta"]
-    shape = (n_tokens, cache["n_heads"], cache["head_dim"])
-    k = torch.empty(shape, dtype=km.dtype, device=km.device)
-    v = torch.empty(shape, dtype=km.dtype, device=km.device)
+    both = T.empty((2, n_tokens, cache["n_heads"], cache["head_dim"]), dtype=km.dtype, device=km.device)
+    k, v = both.unbind(0)
     hqq_cache_read(cache, table, lens, k, v, cu_tokens, stream)
     return k, v
 

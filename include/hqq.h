@@ -391,7 +391,8 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
                                       size_t workspace_bytes, void *stream);
 
 /* Workspace bytes of the two attention calls for these sizes (prefix_len 0 for the first);
- * a function of the sizes alone. 0 if the arguments are invalid: the call then says why. */
+ * a function of the sizes alone. 0 if none is needed (workspace may then be NULL), and if the
+ * arguments are invalid: the call then says why. */
 size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs,
                                      int n_q_heads, int64_t prefix_len);
 

@@ -332,6 +332,40 @@ def test_same_bits_whatever_the_workspace_held(H):
         with pytest.raises(H.HQQError) as e:
             H.hqq_cache_attention_prefix(cache, t, ln, pp, prefix, q, outs[0], workspace=ws[:need - 1])
         assert e.value.status == H.HQQ_ERR_WORKSPACE
+    # sequences that one block takes whole need none
+    short = t[:, :512 // 32].contiguous()
+    assert H.hqq_cache_attention_workspace(cache, short, ln, 4, 8) == 0
+
+
+def test_wrong_tensors_are_refused(H):
+    cache = H.alloc_cache(4, 16, 2, 64, 4, 32, F)
+    t, ln = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), i32([5])
+    q = torch.zeros(1, 4, 64, dtype=F, device="cuda")
+    k = torch.zeros(1, 2, 64, dtype=F, device="cuda")
+
+    def refused(f, *a, **kw):
+        with pytest.raises(H.HQQError) as e:
+            f(*a, **kw)
+        assert e.value.status == H.HQQ_ERR_ARG
+    for bad in (dict(k_codes=cache["k_codes"][:, :1]), dict(v_codes=cache["v_codes"][:3]), dict(k_meta=cache["k_meta"].float()),
+                dict(v_meta=cache["v_meta"].to(B)), dict(page_size=32), dict(n_heads=4), dict(group_size=64), dict(nbits=8),
+                dict(k_meta=cache["k_meta"].cpu()), dict(v_codes=cache["v_codes"].transpose(0, 1))):
+        refused(H.cache_attention, {**cache, **bad}, t, ln, q)
+    for bt, bl in ((t.long(), ln), (t[0], ln), (t.cpu(), ln), (t, ln.long()), (t, i32([5, 5])), (t, ln.cpu()),
+                   (torch.zeros(1, 4, dtype=torch.int32, device="cuda")[:, ::2], i32([5]).expand(2)[:1].float())):
+        refused(H.cache_attention, cache, bt, bl, q)
+        refused(H.hqq_cache_write, cache, bt, bl, k, k)
+    refused(H.cache_attention, cache, t, ln, q, cu_tokens=i32([0]))
+    refused(H.cache_attention, cache, t, ln, q, cu_tokens=torch.tensor([0, 1], device="cuda"))
+    for bq in (q.to(B), q[:, :3], q[..., :32], q.cpu(), q[0], torch.zeros(1, 4, 128, dtype=F, device="cuda")[..., ::2],
+               torch.zeros(2, 4 * 65, dtype=F, device="cuda")[:, 1:].as_strided((2, 4, 64), (260, 64, 1))):
+        refused(H.cache_attention, cache, t, ln, bq)
+    refused(H.hqq_cache_attention, cache, t, ln, q, torch.zeros(1, 2, 64, dtype=F, device="cuda"))
+    refused(H.cache_attention, cache, t, ln, q, lse=torch.zeros(1, 4, dtype=F, device="cuda"))
+    refused(H.cache_attention_prefix, cache, t, ln, t, 5, q)
+    refused(H.cache_attention_prefix, cache, t, ln, t[0], 33, q)
+    refused(H.hqq_cache_write, cache, t, ln, k, k[:, :1])
+    refused(H.hqq_cache_read, cache, t, ln, k.expand(3, 2, 64)[:, :, :32], k)
 
 
 def test_answering_step_by_step(H):
