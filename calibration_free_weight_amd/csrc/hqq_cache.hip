@@ -32,72 +32,117 @@ __device__ __forceinline__ Slot slot_of(const SeqView &s, int i)
 }
 
 // The row of a lane: token i, heads h0 .. h0 + n - 1, dimensions 8u..8u+7. A wave has
-// 512/head_dim tokens and up to HEADS heads.
+// 512/head_dim tokens, and a block the next waves' too, so that the cache lines that its
+// tokens' grids share are filled by one block (blocks go round the eight dies, and lines that
+// two of them fill in part are written twice).
 struct Place {
     int i, h0, n, u;
 };
 template <int D, int HEADS>
 __device__ __forceinline__ Place place_of(int heads)
 {
-    constexpr int kLanes = D / 8, kTokens = 64 / kLanes;
-    const unsigned wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kLanes = D / 8, kTokens = kThreads / kLanes;
     const unsigned parts = (heads + HEADS - 1) / HEADS;
-    const int lane = threadIdx.x & 63, h0 = (int)(wave % parts) * HEADS;
-    return Place{(int)(wave / parts) * kTokens + lane / kLanes, h0, min(HEADS, heads - h0), lane % kLanes};
+    const int h0 = (int)(blockIdx.x % parts) * HEADS;
+    return Place{(int)(blockIdx.x / parts) * kTokens + (int)threadIdx.x / kLanes, h0, min(HEADS, heads - h0),
+                 (int)threadIdx.x % kLanes};
 }
 
-// The smallest and largest of a group: of the lane's values, then over its G/8 lanes, by
-// exchanges within a row of 16 lanes (pairs, quads, halves mirrored, the row mirrored).
+// Smaller and larger of two (fminf would first quiet signalling numbers: an instruction each).
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t smaller_halves(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("v_pk_min_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// f over the G/8 lanes of a group, by exchanges within a row of 16 lanes: pairs, quads,
+// halves mirrored, the row mirrored. All of the group's lanes get it.
 template <int CTRL>
-__device__ __forceinline__ float other(float x)
+__device__ __forceinline__ uint32_t other(uint32_t x)
 {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
 }
-template <int G>
-__device__ __forceinline__ void group_range(float &lo, float &hi)
+template <int G, typename F>
+__device__ __forceinline__ uint32_t over_group(uint32_t x, F f)
 {
-    lo = fminf(lo, other<0xb1>(lo));        // quad_perm 1, 0, 3, 2
-    hi = fmaxf(hi, other<0xb1>(hi));
-    lo = fminf(lo, other<0x4e>(lo));        // quad_perm 2, 3, 0, 1
-    hi = fmaxf(hi, other<0x4e>(hi));
-    if constexpr (G >= 64) {
-        lo = fminf(lo, other<0x141>(lo));   // row_half_mirror
-        hi = fmaxf(hi, other<0x141>(hi));
-    }
-    if constexpr (G >= 128) {
-        lo = fminf(lo, other<0x140>(lo));   // row_mirror
-        hi = fmaxf(hi, other<0x140>(hi));
+    x = f(x, other<0xb1>(x));               // quad_perm 1, 0, 3, 2
+    x = f(x, other<0x4e>(x));               // quad_perm 2, 3, 0, 1
+    if constexpr (G >= 64) x = f(x, other<0x141>(x));       // row_half_mirror
+    if constexpr (G >= 128) x = f(x, other<0x140>(x));      // row_mirror
+    return x;
+}
+
+// The smallest and largest of a group, of which the lane has the values v (bits raw).
+template <typename T, int G>
+__device__ __forceinline__ void group_range(const uint4 raw, const float (&v)[8], float &lo, float &hi)
+{
+    if constexpr (Types<T>::kBf16) {
+        lo = smaller(smaller(smaller(v[0], v[1]), smaller(v[2], v[3])), smaller(smaller(v[4], v[5]), smaller(v[6], v[7])));
+        hi = larger(larger(larger(v[0], v[1]), larger(v[2], v[3])), larger(larger(v[4], v[5]), larger(v[6], v[7])));
+        lo = __uint_as_float(over_group<G>(__float_as_uint(lo), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(smaller(__uint_as_float(a), __uint_as_float(b)));
+        }));
+        hi = __uint_as_float(over_group<G>(__float_as_uint(hi), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(larger(__uint_as_float(a), __uint_as_float(b)));
+        }));
+    } else {
+        // two at a time; then the smallest, negated, and the largest in one word
+        const uint32_t h = larger_halves(larger_halves(raw.x, raw.y), larger_halves(raw.z, raw.w));
+        const uint32_t l = smaller_halves(smaller_halves(raw.x, raw.y), smaller_halves(raw.z, raw.w)) ^ 0x80008000u;
+        const uint32_t both = larger_halves(__builtin_amdgcn_perm(h, l, 0x05040100u), __builtin_amdgcn_perm(h, l, 0x07060302u));
+        const uint32_t all = over_group<G>(both, [](uint32_t a, uint32_t b) { return larger_halves(a, b); });
+        lo = -to_f32<T>(all & 0xffffu);
+        hi = to_f32<T>(all >> 16);
     }
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t step_up(float span, int top, double range)
+// What a - b, rounded to `d`, leaves: a - b = d + less(a, b, d) exactly.
+__device__ __forceinline__ float less(float a, float b, float d)
 {
-    // The nearest number of the type to span/top is one of the two next to range/top; the
-    // exact product (at most 8 + 11 bits) says whether it is the lower one.
-    const float near = span * (1.0f / (float)top);
-    uint32_t bits = from_f32<T>(near);
-    if ((double)to_f32<T>(bits) * top < range) ++bits;
-    if (Types<T>::kBf16 && range > 0 && bits < 0x0d80u) bits = 0x0d80u;   // 2^-100
+    const float x = d - a;
+    return (a - (d - x)) + (-b - x);
+}
+
+// The bits of the smallest number of the type with number * top >= hi - lo. The nearest one to
+// their rounded quotient is it or the one below; its product with top has at most 11 + 8 bits
+// and lies next to the difference, so both the product and what it is above are exact.
+template <typename T>
+__device__ __forceinline__ uint32_t step_bits(float lo, float hi, int top)
+{
+    const float span = hi - lo;
+    uint32_t bits = from_f32<T>(span * (1.0f / (float)top));
+    if (to_f32<T>(bits) * (float)top - span < less(hi, lo, span)) ++bits;
+    if (Types<T>::kBf16 && span > 0.f) bits = max(bits, 0x0d80u);     // 2^-100
     return bits;
 }
 
 // ---- write ------------------------------------------------------------------------------------
-// Codes are decided exactly: a binary32 quotient errs by less than 2^-14, so only quotients
-// within 2^-12 of a half take the binary64 comparison with the midpoint (about one value in
-// 2000, so that one lane in 250 has one). q: the codes, as whole binary32 numbers.
+// Bound by the arithmetic as much as by memory: about 100 instructions for a lane's eight
+// values, of 24 bytes in and out with 4 bits. Codes are decided exactly: the quotient, by a
+// product with the reciprocal's estimate, errs by at most 2^(nbits - 22), so only within twice
+// that of a half is it held against the midpoint, again without rounding: (2k + 1) * step has
+// at most 9 + 11 bits and lies next to twice the difference. With binary16 one value in some
+// thousands is a tie, so a fifth of the waves come there. q: the codes, as binary32 numbers.
 template <typename T, int NB, int G>
 __device__ __forceinline__ uint32_t quantize8(const uint4 raw, float (&q)[8])
 {
     constexpr int kTop = (1 << NB) - 1;
-    float v[8];
+    constexpr float kNear = 0.5f - (NB == 4 ? 0x1p-17f : 0x1p-13f);
+    float v[8], lo, hi;
     unpack8<T>(raw, v);
-    float lo = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
-    float hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-    group_range<G>(lo, hi);
-    const uint32_t sb = step_up<T>(hi - lo, kTop, (double)hi - (double)lo);
+    group_range<T, G>(raw, v, lo, hi);
+    const uint32_t sb = step_bits<T>(lo, hi, kTop);
     const float step = to_f32<T>(sb);
-    const float inv = step > 0 ? 1.0f / step : 0.f;
+    const float inv = step > 0 ? __builtin_amdgcn_rcpf(step) : 0.f;
     float y[8], most = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -105,14 +150,13 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 raw, float (&q)[8])
         q[e] = rintf(y[e]);
         most = fmaxf(most, fabsf(y[e] - q[e]));
     }
-    if (most > 0.5f - 0x1p-12f) {
+    if (most > kNear) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (fabsf(y[e] - q[e]) <= 0.5f - 0x1p-12f) continue;
-            const float k = floorf(y[e]);
-            const double twice = 2.0 * ((double)v[e] - (double)lo);
-            const double mid = (2.0 * k + 1.0) * (double)step;
-            q[e] = twice > mid || (twice == mid && ((int)k & 1)) ? k + 1.f : k;
+            const float k = floorf(y[e]), d = v[e] - lo, odd = fmaf(2.f, k, 1.f);
+            const float above = 2.f * d - odd * step + 2.f * less(v[e], lo, d);
+            const float up = above > 0.f || (above == 0.f && ((int)k & 1)) ? k + 1.f : k;
+            q[e] = fabsf(y[e] - q[e]) > kNear ? up : q[e];
         }
     }
     // the last code stays finite in binary16
@@ -270,9 +314,8 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheView c, SeqVi
 template <typename T, int NB, int D, int G, int HEADS>
 void launch_heads(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p, hipStream_t stream)
 {
-    constexpr int kTokens = 512 / D;
-    const int64_t waves = ((int64_t)s.n_tokens + kTokens - 1) / kTokens * ((c.heads + HEADS - 1) / HEADS);
-    const dim3 grid((unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64)));
+    constexpr int kTokens = 8 * kThreads / D;
+    const dim3 grid((unsigned)(((int64_t)s.n_tokens + kTokens - 1) / kTokens * ((c.heads + HEADS - 1) / HEADS)));
     if (write) cache_write_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
     else cache_read_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
 }
