@@ -27,6 +27,7 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
@@ -108,8 +109,11 @@ __device__ __forceinline__ u32x4 key_frag(const uint32_t *w)
 // Code i of a value's row for two tokens (words x, y hold it), less the middle of the codes
 // (8 or 128), as binary16 numbers: exact, and half as large as the codes, so that the
 // rounding of the weights they meet weighs no more than it would on the values themselves.
+struct Masks {
+    uint32_t low, high;         // kept in vector registers: "and" and "or" are then one instruction
+};
 template <int NB>
-__device__ __forceinline__ uint32_t value_pair(const uint32_t *x, const uint32_t *y, int i)
+__device__ __forceinline__ uint32_t value_pair(const uint32_t *x, const uint32_t *y, int i, const Masks &masks)
 {
     uint32_t w;
     float off;
@@ -119,7 +123,7 @@ __device__ __forceinline__ uint32_t value_pair(const uint32_t *x, const uint32_t
         const int c = i >> 2, k = c & 1;
         uint32_t p = __builtin_amdgcn_perm(y[c >> 1], x[c >> 1], k ? 0x07060302u : 0x05040100u);
         if (i & 2) p >>= 8;
-        w = i & 1 ? (p & 0x00f000f0u) | 0x54005400u : (p & 0x000f000fu) | 0x64006400u;
+        w = i & 1 ? (p & masks.high) | 0x54005400u : (p & masks.low) | 0x64006400u;
         off = i & 1 ? 72.f : 1032.f;
     } else {
         const uint32_t p = __builtin_amdgcn_perm(y[i >> 2], x[i >> 2], i & 2 ? 0x07030602u : 0x05010400u);
@@ -136,23 +140,53 @@ __device__ __forceinline__ uint32_t round_pair(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2));
 }
 
-template <int BYTES>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[BYTES / 4])
+// Global memory from a pointer that is the same in all lanes, in scalar registers, and a
+// lane's offset from it in 32 bits (an addition per load less than with a pointer per lane).
+typedef const __attribute__((address_space(1))) uint8_t *Global;
+__device__ __forceinline__ Global uniform(const void *p)
 {
+    const uint64_t x = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (Global)((uint64_t)hi << 32 | lo);
+}
+template <typename V>
+__device__ __forceinline__ V load(Global p, uint32_t offset)
+{
+    asm volatile("" : "+v"(offset));        // widened here, where the load can take it as it is
+    return *(const __attribute__((address_space(1))) V *)(p + offset);
+}
+
+// The page of position pos (below the length) of the sequence whose pages are at `table`, or -1:
+// a scalar load, for nothing writes the table while the kernel runs.
+typedef const __attribute__((address_space(4))) int32_t *Constant;
+__device__ __forceinline__ int page_at(const SeqView &s, const int32_t *table, int pos)
+{
+    const int p = ((Constant)(uint64_t)table)[pos >> s.page_shift];
+    return (uint32_t)p < (uint32_t)s.n_pages ? p : -1;
+}
+
+__device__ __forceinline__ float larger3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(Global p, uint32_t offset, uint32_t (&w)[BYTES / 4])
+{
+    static_assert(BYTES == 8 || BYTES % 16 == 0, "8 or a multiple of 16");
     if constexpr (BYTES % 16 == 0) {
 #pragma unroll
         for (int k = 0; k < BYTES / 16; ++k) {
-            const uint4 x = reinterpret_cast<const uint4 *>(p)[k];
-            w[4 * k] = x.x;
-            w[4 * k + 1] = x.y;
-            w[4 * k + 2] = x.z;
-            w[4 * k + 3] = x.w;
+            const u32x4 x = load<u32x4>(p, offset + 16 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[4 * k + e] = x[e];
         }
     } else {
-        static_assert(BYTES == 8, "8 or a multiple of 16");
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        w[0] = x.x;
-        w[1] = x.y;
+        const u32x2 x = load<u32x2>(p, offset);
+        w[0] = x[0];
+        w[1] = x[1];
     }
 }
 
@@ -254,7 +288,9 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // where a lane's parts lie from the first byte (word) of 16 tokens'
     const unsigned key_at = col * kRow + quad * kKeyBytes, val_at = lane * 4 * kValBytes;
-    const unsigned grid_at = quad * kGrids + (col & (kGrids - 1));
+    const unsigned grid_at = 4 * (quad * kGrids + (col & (kGrids - 1)));
+    Masks masks = {0x000f000fu, 0x00f000f0u};
+    asm volatile("" : "+v"(masks.low), "+v"(masks.high));
 
     for (int u = first_unit(w, W, U); u < u_end;) {
         // the item that unit u is of
@@ -330,11 +366,11 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
         const int t_end = (int)min((int64_t)(u_in + count) * d.unit, (int64_t)lim_high);
         uint32_t kw[2][kKeyBytes / 4], vw[2][kValBytes], kgrid[2][kGridRegs], vgrid[2][kGridRegs];
         int page[2];
-        // Tokens of a half that are in the cache; their first byte of codes over kRow.
-        auto find = [&](int t0) {
+        // The pages of a step's halves, and the first token of one over all pages.
+        const int32_t *table = d.s.table + (int64_t)b * d.s.max_pages;
+        auto find = [&](int t0, int (&page)[2]) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-                page[half] = __builtin_amdgcn_readfirstlane(t0 + 16 * half < len ? page_of(d.s, b, t0 + 16 * half) : -1);
+            for (int half = 0; half < 2; ++half) page[half] = page_at(d.s, table, min(t0 + 16 * half, len - 1));
         };
         auto first = [&](int t0, int half) {
             const int at = (t0 + 16 * half) & ((1 << d.s.page_shift) - 1);
@@ -344,24 +380,26 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int64_t at = first(t0, half);
-                load_words<kKeyBytes>(a.c.k_codes + at * kRow + key_at, kw[half]);
+                load_words<kKeyBytes>(uniform(a.c.k_codes + at * kRow), key_at, kw[half]);
+                const Global grids = uniform(a.c.k_meta + at * kGroups);
 #pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) kgrid[half][k] = (a.c.k_meta + at * kGroups)[grid_at + 16 * k];
+                for (int k = 0; k < kGridRegs; ++k) kgrid[half][k] = load<uint32_t>(grids, grid_at + 64 * k);
             }
         };
         auto load_values = [&](int t0) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int64_t at = first(t0, half);
-                load_words<4 * kValBytes>(a.c.v_codes + at * kRow + val_at, vw[half]);
+                load_words<4 * kValBytes>(uniform(a.c.v_codes + at * kRow), val_at, vw[half]);
+                const Global grids = uniform(a.c.v_meta + at * kGroups);
 #pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) vgrid[half][k] = (a.c.v_meta + at * kGroups)[grid_at + 16 * k];
+                for (int k = 0; k < kGridRegs; ++k) vgrid[half][k] = load<uint32_t>(grids, grid_at + 64 * k);
             }
         };
 
         int t0 = (int)min((int64_t)u_in * d.unit + wave * kTile, (int64_t)t_end);
         if (t0 < t_end) {
-            find(t0);
+            find(t0, page);
             load_keys(t0);
             load_values(t0);
         }
@@ -370,17 +408,20 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             // its values once this one's are: both are under way during half a step, with no
             // registers but their own.
             const int next = t0 + kStep < t_end ? t0 + kStep : t0;
-            int good[2];
+            int good[2], page_next[2];
+            find(next, page_next);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
                 good[half] = page[half] < 0 ? 0 : min(16, len - t0 - 16 * half);
             const bool open = t0 + kTile <= lim_low && good[0] == 16 && good[1] == 16;
             if (!open) {
+                int first = 4 * quad;
+                asm volatile("" : "+v"(first));
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int k = 0; k < kGridRegs; ++k) {
-                        const int token = 4 * quad + ((col & (kGrids - 1)) + 16 * k) / kGroups;
+                        const int token = first + ((col & (kGrids - 1)) + 16 * k) / kGroups;
                         if (token >= good[half]) kgrid[half][k] = vgrid[half][k] = 0;
                     }
             }
@@ -405,7 +446,8 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                     }
                 }
             }
-            find(next);
+            page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
+            page[1] = __builtin_amdgcn_readfirstlane(page_next[1]);
             load_keys(next);
             __builtin_amdgcn_sched_barrier(0);
 
@@ -423,14 +465,16 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                     s[t][i.value] = x;
                 });
                 if (!open) {
+                    int first = t0 + 4 * quad;
+                    asm volatile("" : "+v"(first));         // a branch, not a choice in every step
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int at = 4 * quad + (i & 3);
-                        if (t0 + 16 * (i >> 2) + at >= lim[t] || at >= good[i >> 2]) s[t][i] = -INFINITY;
+                        const int at = first + 16 * (i >> 2) + (i & 3);
+                        if (at >= min(lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
                     }
                 }
-                float top = fmaxf(fmaxf(fmaxf(s[t][0], s[t][1]), fmaxf(s[t][2], s[t][3])),
-                                  fmaxf(fmaxf(s[t][4], s[t][5]), fmaxf(s[t][6], s[t][7])));
+                float top = larger3(larger3(larger3(s[t][0], s[t][1], s[t][2]), s[t][3], s[t][4]),
+                                    larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
                 if (__any(top > above[t])) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
@@ -516,7 +560,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
                             x[0] = v[i % 2];
                             y[0] = v[i % 2] >> 16;
                         }
-                        vf[i] = value_pair<NB>(x, y, j);
+                        vf[i] = value_pair<NB>(x, y, j, masks);
                     }
 #pragma unroll
                     for (int t = 0; t < RT; ++t) o[t][j] = mfma32<false>(vf, pf[t], o[t][j]);
