@@ -251,153 +251,479 @@ constexpr float kSlack = 6.f;
 // weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
 constexpr int kStepBits = 8;
 
-template <typename T, int NB, int D, int G, int RT>
-__global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
+// A run's next item, or the part of it that the run has.
+struct Item {
+    int b;                      // sequence
+    Rows rows;                  // its rows of the call
+    int len, n_rows;            // tokens; query rows of this head
+    int row0;                   // the item's first
+    int along, u_in, count;     // units of the item, the first of this part, how many
+};
+template <int ROWS>
+__device__ __forceinline__ Item item_at(const AttnSide &d, const int32_t *starts, int per, int u, int u_end)
+{
+    Item x;
+    x.b = 0;
+    for (int hi = d.s.n_seqs; hi - x.b > 1;) {
+        const int mid = (x.b + hi) >> 1;
+        if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) x.b = mid; else hi = mid;
+    }
+    x.rows = rows_of(d.s, x.b);
+    x.len = len_of(d.s, x.b);
+    x.n_rows = (x.rows.end - x.rows.begin) * per;
+    x.along = units_along(x.len, d.unit);
+    const int in_seq = u - __builtin_amdgcn_readfirstlane(starts[x.b]);
+    x.row0 = in_seq / x.along * ROWS;
+    x.u_in = in_seq % x.along;
+    x.count = min(u_end - u, x.along - x.u_in);
+    return x;
+}
+
+// What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16).
+template <int D, int G, int RT>
+struct Wave {
+    static constexpr int kGroups = D / G;
+    u32x4 qf[RT][D / 32];       // queries, as B fragments
+    float qsum[RT][kGroups];    // their sums over each group, scaled
+    int lim[RT];                // what a row sees ends here
+    int lim_low, lim_high;      // for all rows, for any
+    f32x4 o[RT][D / 16];
+    // m: scores are taken from it; above: how far one may lie above before m moves (none
+    // while m has not been set)
+    float m[RT], above[RT], l[RT], bsum[RT][kGroups];
+    float step_lim, step_by;    // V's steps are below step_lim and multiplied by step_by
+};
+
+template <typename T, int D, int G, int RT>
+__device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
+{
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    w.lim_low = x.len;
+    w.lim_high = 0;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int row = row0 + 16 * t + col;
+        const bool have = row < x.n_rows;
+        const int tok = have ? row / a.per : 0, hq = h * a.per + (have ? row % a.per : 0);
+        const uint16_t *q = a.q + (x.rows.begin + tok) * a.q_ts + hq * a.q_hs;
+        w.lim[t] = !have ? 0 : causal ? x.len - (x.rows.end - x.rows.begin) + tok + 1 : x.len;
+        if (have) {
+            w.lim_low = min(w.lim_low, w.lim[t]);
+            w.lim_high = max(w.lim_high, w.lim[t]);
+        }
+#pragma unroll
+        for (int g = 0; g < D / G; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int m = g * G / 32; m < (g + 1) * G / 32; ++m) {
+                uint4 raw = {0, 0, 0, 0};
+                if (have) raw = *reinterpret_cast<const uint4 *>(q + 32 * m + 8 * quad);
+                w.qf[t][m] = u32x4{raw.x, raw.y, raw.z, raw.w};
+                float v[8];
+                unpack8<T>(raw, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += v[e];
+            }
+            w.qsum[t][g] = column_sum(sum) * a.scale;
+            w.bsum[t][g] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) w.o[t][j] = f32x4{0, 0, 0, 0};
+        w.m[t] = 0.f;
+        w.above[t] = -INFINITY;
+        w.l[t] = 0.f;
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) {
+        w.lim_low = min(w.lim_low, __shfl_xor(w.lim_low, x));
+        w.lim_high = max(w.lim_high, __shfl_xor(w.lim_high, x));
+    }
+    w.lim_low = __builtin_amdgcn_readfirstlane(w.lim_low);
+    w.lim_high = __builtin_amdgcn_readfirstlane(w.lim_high);
+    w.step_lim = w.step_by = 0.f;
+}
+
+// The grids of a step's two halves of 16 tokens, as the lanes hold them, and how many tokens
+// of each half there are (negative: none).
+template <int D, int G>
+struct Grids {
+    static constexpr int kGrids = 4 * (D / G), kRegs = (kGrids + 15) / 16;
+    uint32_t k[2][kRegs], v[2][kRegs];
+    int good[2];
+};
+
+// One step: 32 tokens from t0 for the wave's rows. key(half, mm) and value(j) give the A
+// fragments; after_keys() is called when no more keys are needed.
+template <typename T, int NB, int D, int G, int RT, typename Key, typename Value, typename After>
+__device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, float scale, int t0, Key key, Value value,
+                                            After after_keys)
 {
     constexpr bool kBf16 = Types<T>::kBf16;
-    constexpr int kGroups = D / G, kRows = 16 * RT;
-    constexpr int kRow = D * NB / 8;            // bytes of a token's codes
-    constexpr int kKeyBytes = kRow / 4;         // a lane's quarter of a token's key
-    constexpr int kValBytes = kRow / 16;        // a row of a token's value
-    constexpr int kUnitWords = NB / 4;
-    constexpr int kGrids = 4 * kGroups;         // of four tokens
-    constexpr int kGridRegs = (kGrids + 15) / 16;
-    constexpr int kPart = D < 128 ? D : 128;    // dimensions joined over the waves at a time
-    constexpr int kStride = kPart + 4;
-    const unsigned blocks0 = (unsigned)a.side[0].workers * a.c.heads;
-    AttnSide d = a.side[0];
-    unsigned block = blockIdx.x;
-    if (block >= blocks0) {
-        d = a.side[1];
-        block -= blocks0;
+    constexpr int kGroups = D / G, kGrids = Grids<D, G>::kGrids, kRegs = Grids<D, G>::kRegs;
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    const bool open = t0 + kTile <= w.lim_low && gr.good[0] >= 16 && gr.good[1] >= 16;
+    if (!open) {
+        int first = 4 * quad;
+        asm volatile("" : "+v"(first));                     // a branch, not a choice in every step
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k) {
+                const int token = first + ((col & (kGrids - 1)) + 16 * k) / kGroups;
+                if (token >= gr.good[half]) gr.k[half][k] = gr.v[half][k] = 0;
+            }
     }
-    extern __shared__ int32_t shared[];
-    int32_t *starts = shared;                                       // [n_seqs + 1]
-    int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [kWaves]
-    float *ml = reinterpret_cast<float *>(scan + 4);                // [kWaves][kRows][2]
-    float *part = ml + kWaves * kRows * 2;                          // [kWaves][16][kStride]
+    f32x4 acc[2][RT][kGroups];
+    float kstep[2][kRegs], kbase[2][kRegs];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k) {
+            kstep[half][k] = to_f32<T>(gr.k[half][k] & 0xffffu) * scale;
+            kbase[half][k] = to_f32<T>(gr.k[half][k] >> 16);
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[half][t][g] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int mm = g * G / 32; mm < (g + 1) * G / 32; ++mm) {
+                const u32x4 kf = key(half, mm);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[half][t][g] = mfma32<kBf16>(kf, w.qf[t][mm], acc[half][t][g]);
+            }
+        }
+    }
+    after_keys();
 
-    lay_out<kRows>(d, a.per, starts, scan);
-    const int h = (int)(block % (unsigned)a.c.heads), w = (int)(block / (unsigned)a.c.heads);
+    float s[RT][8];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        static_for<8>([&](auto i) {
+            constexpr int half = i.value / 4, r = i.value % 4;
+            float x = -w.m[t];
+            static_for<kGroups>([&](auto g) {
+                constexpr int at = r * kGroups + g.value;
+                x = fmaf(row_lane<at % 16>(kbase[half][at / 16]), w.qsum[t][g.value], x);
+                x = fmaf(row_lane<at % 16>(kstep[half][at / 16]), acc[half][t][g.value][r], x);
+            });
+            s[t][i.value] = x;
+        });
+        if (!open) {
+            int first = t0 + 4 * quad;
+            asm volatile("" : "+v"(first));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = first + 16 * (i >> 2) + (i & 3);
+                if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + gr.good[i >> 2])) s[t][i] = -INFINITY;
+            }
+        }
+        float top = larger3(larger3(larger3(s[t][0], s[t][1], s[t][2]), s[t][3], s[t][4]),
+                            larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
+        if (__any(top > w.above[t])) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            // m moves up to the largest score, or at first to it wherever it is
+            const float up = top > fminf(w.above[t], 0.f) ? top : 0.f;
+            const float f = w.above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-up);
+            if (top > -INFINITY) w.above[t] = kSlack;
+            w.m[t] += up;
+            w.l[t] *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[t][i] -= up;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) w.bsum[t][g] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) w.o[t][j] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
+            w.l[t] += s[t][i];
+        }
+    }
+
+    float vstep[2][kRegs], vmid[2][kRegs];
+    float most = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k) {
+            vstep[half][k] = to_f32<T>(gr.v[half][k] & 0xffffu);
+            vmid[half][k] = fmaf(vstep[half][k], NB == 4 ? 8.f : 128.f, to_f32<T>(gr.v[half][k] >> 16));
+            most = fmaxf(most, vstep[half][k]);
+        }
+    if (__any(most >= w.step_lim && most > 0.f)) {
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
+        // the power of two at or below it
+        const float p2 = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
+        const float by = ldexpf(1.f / p2, kStepBits), f = w.step_by > 0.f ? by / w.step_by : 1.f;
+        w.step_lim = 2.f * p2;
+        w.step_by = by;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) w.o[t][j] *= f;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k) vstep[half][k] *= w.step_by;
+
+    // weights times V's step, in binary16
+    static_for<kGroups>([&](auto g) {
+        u32x4 pf[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            static_for<4>([&](auto i) {
+                constexpr int half = i.value / 2, r = i.value % 2 * 2;
+                constexpr int at = r * kGroups + g.value, at1 = at + kGroups;
+                const float x = s[t][2 * i.value], y = s[t][2 * i.value + 1];
+                w.bsum[t][g.value] = fmaf(row_lane<at % 16>(vmid[half][at / 16]), x, w.bsum[t][g.value]);
+                w.bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vmid[half][at1 / 16]), y, w.bsum[t][g.value]);
+                pf[t][i.value] = round_pair(row_lane<at % 16>(vstep[half][at / 16]) * x,
+                                            row_lane<at1 % 16>(vstep[half][at1 / 16]) * y);
+            });
+        }
+#pragma unroll
+        for (int jj = 0; jj < G / 16; ++jj) {
+            const int j = g.value * (G / 16) + jj;
+            const u32x4 vf = value(j);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) w.o[t][j] = mfma32<false>(vf, pf[t], w.o[t][j]);
+        }
+    });
+}
+
+constexpr int part_dims(int dim) { return dim < 128 ? dim : 128; }      // joined over the waves at a time
+constexpr int kPartPad = 4;
+
+// Joins what TW waves found for the same rows, each on its own tokens, on the largest of their
+// maxima, and writes it: waves TW * r .. TW * r + TW - 1 have rows 16 * RT * r .. of the item.
+// ml: [kWaves][16 * RT][2]; part: [kWaves][16][part_dims + kPartPad]. Blocks come and leave in
+// step.
+template <typename T, int D, int G, int RT, int TW>
+__device__ __forceinline__ void finish(Wave<D, G, RT> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
+                                       float *ml, float *part)
+{
+    constexpr int kGroups = D / G, kPart = part_dims(D), kStride = kPart + kPartPad;
+    constexpr int kRowWaves = kWaves / TW, kRows = 16 * RT * kRowWaves;
+    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
+    const float unstep = w.step_by > 0.f ? 1.f / w.step_by : 0.f;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        w.l[t] = column_sum(w.l[t]);
+        if (quad == 0) {
+            ml[(wave * 16 * RT + 16 * t + col) * 2] = w.above[t] < 0.f ? -INFINITY : w.m[t];
+            ml[(wave * 16 * RT + 16 * t + col) * 2 + 1] = w.l[t];
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) w.bsum[t][g] = column_sum(w.bsum[t][g]);
+    }
+    const bool whole = x.count == x.along;
+    const int slot = 2 * run + (x.u_in > 0 ? 0 : 1);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int d0 = 0; d0 < D; d0 += kPart) {
+            // a lane has runs of G/16 neighbouring dimensions of its column
+#pragma unroll
+            for (int g = d0 / G; g < (d0 + kPart) / G; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int jj = 0; jj < G / 16; ++jj)
+                        part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
+                            fmaf(w.o[t][g * (G / 16) + jj][i], unstep, w.bsum[t][g]);
+            __syncthreads();
+            for (int y = threadIdx.x; y < kRowWaves * 16 * kPart / 4; y += kAttnThreads) {
+                const int r = y / (kPart / 4) % 16, first = y / (kPart / 4) / 16 * TW, e0 = d0 + y % (kPart / 4) * 4;
+                const int in_item = first / TW * 16 * RT + 16 * t + r, row = x.row0 + in_item;
+                if (row >= x.n_rows) break;
+                float mk[TW], top = -INFINITY, all = 0.f;
+#pragma unroll
+                for (int k = 0; k < TW; ++k) {
+                    mk[k] = ml[((first + k) * 16 * RT + 16 * t + r) * 2];
+                    top = fmaxf(top, mk[k]);
+                }
+                f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < TW; ++k) {
+                    if (mk[k] == -INFINITY) continue;
+                    const float f = TW == 1 ? 1.f : __builtin_amdgcn_exp2f(mk[k] - top);
+                    all = fmaf(f, ml[((first + k) * 16 * RT + 16 * t + r) * 2 + 1], all);
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(part + ((first + k) * 16 + r) * kStride + e0 - d0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[e] = fmaf(f, v[e], sum[e]);
+                }
+                float *to_o, *to_ml;
+                int64_t at;
+                if (!whole) {
+                    at = ((int64_t)h * 2 * d.workers + slot) * kRows + in_item;
+                    to_o = d.slot_o;
+                    to_ml = d.slot_ml;
+                } else {
+                    at = (int64_t)h * d.s.n_tokens * a.per + (int64_t)x.rows.begin * a.per + row;
+                    to_o = d.row_o;
+                    to_ml = d.row_ml;
+                }
+                if (to_o) {
+                    *reinterpret_cast<f32x4 *>(to_o + at * D + e0) = sum;
+                    if (e0 == 0) *reinterpret_cast<f32x2 *>(to_ml + at * 2) = f32x2{top, all};
+                    continue;
+                }
+                const float inv = all > 0.f ? 1.f / all : 0.f;
+                const int tok = x.rows.begin + row / a.per, hq = h * a.per + row % a.per;
+                const uint2 packed = {from_f32<T>(sum[0] * inv) | from_f32<T>(sum[1] * inv) << 16,
+                                      from_f32<T>(sum[2] * inv) | from_f32<T>(sum[3] * inv) << 16};
+                *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + e0) = packed;
+                if (a.lse && e0 == 0)
+                    a.lse[(int64_t)tok * a.c.heads * a.per + hq] =
+                        all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
+            }
+            __syncthreads();
+        }
+}
+
+// Where the codes and grids of 16 tokens lie, and a lane's parts of them.
+template <int NB, int D, int G>
+struct Spot {
+    static constexpr int kRow = D * NB / 8;         // bytes of a token's codes
+    static constexpr int kKeyBytes = kRow / 4;      // a lane's quarter of a token's key
+    static constexpr int kValBytes = kRow / 16;     // a row of a token's value
+    static constexpr int kGrids = Grids<D, G>::kGrids, kRegs = Grids<D, G>::kRegs;
+    unsigned key_at, val_at, grid_at;
+    __device__ __forceinline__ Spot()
+    {
+        const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+        key_at = col * kRow + quad * kKeyBytes;
+        val_at = lane * 4 * kValBytes;
+        grid_at = 4 * (quad * kGrids + (col & (kGrids - 1)));
+    }
+    // The first of the 16 tokens at position t (page `page`, any value) over all pages.
+    static __device__ __forceinline__ int64_t first(const AttnArgs &a, const SeqView &s, int h, int page, int t)
+    {
+        const int64_t slice = (int64_t)max(page, 0) * a.c.heads + h;
+        return (slice << s.page_shift) + (t & ((1 << s.page_shift) - 1));
+    }
+    __device__ __forceinline__ void keys(const AttnArgs &a, int64_t at, uint32_t (&w)[kKeyBytes / 4]) const
+    {
+        load_words<kKeyBytes>(uniform(a.c.k_codes + at * kRow), key_at, w);
+    }
+    __device__ __forceinline__ void values(const AttnArgs &a, int64_t at, uint32_t (&w)[kValBytes]) const
+    {
+        load_words<4 * kValBytes>(uniform(a.c.v_codes + at * kRow), val_at, w);
+    }
+    __device__ __forceinline__ void grids(const uint32_t *meta, int64_t at, uint32_t (&g)[kRegs]) const
+    {
+        const Global p = uniform(meta + at * (D / G));
+#pragma unroll
+        for (int k = 0; k < kRegs; ++k) g[k] = load<uint32_t>(p, grid_at + 64 * k);
+    }
+};
+
+// Register i (0, 1) of code j's fragment: tokens 2i and 2i + 1 of a lane's four, whose rows of
+// values are v.
+template <int NB, int D>
+__device__ __forceinline__ uint32_t value_reg(const uint32_t *v, int i, int j, const Masks &masks)
+{
+    constexpr int kBytes = D * NB / 128, kWords = kBytes > 4 ? kBytes / 4 : 1;
+    uint32_t x[kWords], y[kWords];
+    if constexpr (kBytes >= 4) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            x[k] = v[2 * i * kWords + k];
+            y[k] = v[(2 * i + 1) * kWords + k];
+        }
+    } else {
+        x[0] = v[i];
+        y[0] = v[i] >> 16;
+    }
+    return value_pair<NB>(x, y, j, masks);
+}
+
+__device__ __forceinline__ Masks make_masks()
+{
+    Masks m = {0x000f000fu, 0x00f000f0u};
+    asm volatile("" : "+v"(m.low), "+v"(m.high));
+    return m;
+}
+
+// Which side and run a block has; the units laid out in LDS. False if it has nothing to do.
+template <int ROWS>
+__device__ __forceinline__ bool take_run(const AttnArgs &a, AttnSide &d, int32_t *starts, int32_t *scan, int &h, int &run,
+                                         int &u, int &u_end)
+{
+    const unsigned blocks0 = (unsigned)a.side[0].workers * a.c.heads;
+    unsigned block = blockIdx.x;
+    if (block >= blocks0) block -= blocks0;
+    lay_out<ROWS>(d, a.per, starts, scan);
+    h = (int)(block % (unsigned)a.c.heads);
+    run = (int)(block / (unsigned)a.c.heads);
     if (block == 0 && d.starts)
         for (int b = threadIdx.x; b <= d.s.n_seqs; b += kAttnThreads) d.starts[b] = starts[b];
     const int U = __builtin_amdgcn_readfirstlane(starts[d.s.n_seqs]), W = runs_of(d.workers, U);
-    if (w >= W) return;
-    const int u_end = first_unit(w + 1, W, U);
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    if (run >= W) return false;
+    u = first_unit(run, W, U);
+    u_end = first_unit(run + 1, W, U);
+    return true;
+}
+__device__ __forceinline__ AttnSide side_of(const AttnArgs &a)
+{
+    return blockIdx.x < (unsigned)a.side[0].workers * a.c.heads ? a.side[0] : a.side[1];
+}
+
+// ---- few rows: the cache is read, and little else ------------------------------------------
+// Each wave takes 32 tokens of every 128 for all of the tile's rows, straight from memory into
+// its products: no barrier but at an item's end.
+template <typename T, int NB, int D, int G, int RT>
+__global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
+{
+    constexpr int kRows = 16 * RT;
+    extern __shared__ int32_t shared[];
+    AttnSide d = side_of(a);
+    int32_t *starts = shared;                                       // [n_seqs + 1]
+    int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [kWaves]
+    float *ml = reinterpret_cast<float *>(scan + 4);
+    float *part = ml + kWaves * kRows * 2;
+    int h, run, u, u_end;
+    if (!take_run<kRows>(a, d, starts, scan, h, run, u, u_end)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // where a lane's parts lie from the first byte (word) of 16 tokens'
-    const unsigned key_at = col * kRow + quad * kKeyBytes, val_at = lane * 4 * kValBytes;
-    const unsigned grid_at = 4 * (quad * kGrids + (col & (kGrids - 1)));
-    Masks masks = {0x000f000fu, 0x00f000f0u};
-    asm volatile("" : "+v"(masks.low), "+v"(masks.high));
+    const Spot<NB, D, G> spot;
+    const Masks masks = make_masks();
 
-    for (int u = first_unit(w, W, U); u < u_end;) {
-        // the item that unit u is of
-        int b = 0;
-        for (int hi = d.s.n_seqs; hi - b > 1;) {
-            const int mid = (b + hi) >> 1;
-            if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) b = mid; else hi = mid;
-        }
-        const Rows rows = rows_of(d.s, b);
-        const int len = len_of(d.s, b), n_rows = (rows.end - rows.begin) * a.per;
-        const int along = units_along(len, d.unit), u_item = u - __builtin_amdgcn_readfirstlane(starts[b]);
-        const int tile = u_item / along, u_in = u_item % along;
-        const int count = min(u_end - u, along - u_in);
-        const int row0 = tile * kRows;
-        u += count;
-
-        // queries, as B fragments; what a column sees ends at lim
-        u32x4 qf[RT][D / 32];
-        float qsum[RT][kGroups];
-        int lim[RT], lim_low = len, lim_high = 0;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int row = row0 + 16 * t + col;
-            const bool have = row < n_rows;
-            const int tok = have ? row / a.per : 0, hq = h * a.per + (have ? row % a.per : 0);
-            const uint16_t *q = a.q + (rows.begin + tok) * a.q_ts + hq * a.q_hs;
-            lim[t] = !have ? 0 : d.causal ? len - (rows.end - rows.begin) + tok + 1 : len;
-            if (have) {
-                lim_low = min(lim_low, lim[t]);
-                lim_high = max(lim_high, lim[t]);
-            }
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float x = 0.f;
-#pragma unroll
-                for (int m = g * G / 32; m < (g + 1) * G / 32; ++m) {
-                    uint4 raw = {0, 0, 0, 0};
-                    if (have) raw = *reinterpret_cast<const uint4 *>(q + 32 * m + 8 * quad);
-                    qf[t][m] = u32x4{raw.x, raw.y, raw.z, raw.w};
-                    float v[8];
-                    unpack8<T>(raw, v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x += v[e];
-                }
-                qsum[t][g] = column_sum(x) * a.scale;
-            }
-        }
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) {
-            lim_low = min(lim_low, __shfl_xor(lim_low, x));
-            lim_high = max(lim_high, __shfl_xor(lim_high, x));
-        }
-        lim_low = __builtin_amdgcn_readfirstlane(lim_low);
-        lim_high = __builtin_amdgcn_readfirstlane(lim_high);
-
-        f32x4 o[RT][D / 16];
-        // m: scores are taken from it; above: how far one may lie above before m moves (none
-        // while m has not been set)
-        float m[RT], above[RT], l[RT], bsum[RT][kGroups];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            m[t] = 0.f;
-            above[t] = -INFINITY;
-            l[t] = 0.f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) bsum[t][g] = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) o[t][j] = f32x4{0, 0, 0, 0};
-        }
-        // V's steps are below step_lim and multiplied by step_by
-        float step_lim = 0.f, step_by = 0.f;
-
-        const int t_end = (int)min((int64_t)(u_in + count) * d.unit, (int64_t)lim_high);
-        uint32_t kw[2][kKeyBytes / 4], vw[2][kValBytes], kgrid[2][kGridRegs], vgrid[2][kGridRegs];
+    while (u < u_end) {
+        const Item x = item_at<kRows>(d, starts, a.per, u, u_end);
+        u += x.count;
+        Wave<D, G, RT> w;
+        begin<T>(w, a, d.causal, x, h, x.row0);
+        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)w.lim_high);
+        const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
+        uint32_t kw[2][Spot<NB, D, G>::kKeyBytes / 4], vw[2][Spot<NB, D, G>::kValBytes];
+        Grids<D, G> gr;
         int page[2];
-        // The pages of a step's halves, and the first token of one over all pages.
-        const int32_t *table = d.s.table + (int64_t)b * d.s.max_pages;
         auto find = [&](int t0, int (&page)[2]) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) page[half] = page_at(d.s, table, min(t0 + 16 * half, len - 1));
-        };
-        auto first = [&](int t0, int half) {
-            const int at = (t0 + 16 * half) & ((1 << d.s.page_shift) - 1);
-            return (((int64_t)max(page[half], 0) * a.c.heads + h) << d.s.page_shift) + at;
+            for (int half = 0; half < 2; ++half) page[half] = page_at(d.s, table, min(t0 + 16 * half, x.len - 1));
         };
         auto load_keys = [&](int t0) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int64_t at = first(t0, half);
-                load_words<kKeyBytes>(uniform(a.c.k_codes + at * kRow), key_at, kw[half]);
-                const Global grids = uniform(a.c.k_meta + at * kGroups);
-#pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) kgrid[half][k] = load<uint32_t>(grids, grid_at + 64 * k);
+                const int64_t at = spot.first(a, d.s, h, page[half], t0 + 16 * half);
+                spot.keys(a, at, kw[half]);
+                spot.grids(a.c.k_meta, at, gr.k[half]);
             }
         };
         auto load_values = [&](int t0) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int64_t at = first(t0, half);
-                load_words<4 * kValBytes>(uniform(a.c.v_codes + at * kRow), val_at, vw[half]);
-                const Global grids = uniform(a.c.v_meta + at * kGroups);
-#pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) vgrid[half][k] = load<uint32_t>(grids, grid_at + 64 * k);
+                const int64_t at = spot.first(a, d.s, h, page[half], t0 + 16 * half);
+                spot.values(a, at, vw[half]);
+                spot.grids(a.c.v_meta, at, gr.v[half]);
             }
         };
-
-        int t0 = (int)min((int64_t)u_in * d.unit + wave * kTile, (int64_t)t_end);
+        int t0 = (int)min((int64_t)x.u_in * d.unit + wave * kTile, (int64_t)t_end);
         if (t0 < t_end) {
             find(t0, page);
             load_keys(t0);
@@ -408,263 +734,154 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             // its values once this one's are: both are under way during half a step, with no
             // registers but their own.
             const int next = t0 + kStep < t_end ? t0 + kStep : t0;
-            int good[2], page_next[2];
+            int page_next[2];
             find(next, page_next);
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-                good[half] = page[half] < 0 ? 0 : min(16, len - t0 - 16 * half);
-            const bool open = t0 + kTile <= lim_low && good[0] == 16 && good[1] == 16;
-            if (!open) {
-                int first = 4 * quad;
-                asm volatile("" : "+v"(first));
+            for (int half = 0; half < 2; ++half) gr.good[half] = page[half] < 0 ? 0 : x.len - t0 - 16 * half;
+            attend_step<T, NB>(
+                w, gr, a.scale, t0,
+                [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
+                [&](int j) {
+                    u32x4 f;
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int k = 0; k < kGridRegs; ++k) {
-                        const int token = first + ((col & (kGrids - 1)) + 16 * k) / kGroups;
-                        if (token >= good[half]) kgrid[half][k] = vgrid[half][k] = 0;
-                    }
-            }
-            f32x4 acc[2][RT][kGroups];
-            float kstep[2][kGridRegs], kbase[2][kGridRegs];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) {
-                    kstep[half][k] = to_f32<T>(kgrid[half][k] & 0xffffu) * a.scale;
-                    kbase[half][k] = to_f32<T>(kgrid[half][k] >> 16);
-                }
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) acc[half][t][g] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int mm = g * G / 32; mm < (g + 1) * G / 32; ++mm) {
-                        const u32x4 kf = key_frag<kBf16, NB>(kw[half] + mm * kUnitWords);
-#pragma unroll
-                        for (int t = 0; t < RT; ++t) acc[half][t][g] = mfma32<kBf16>(kf, qf[t][mm], acc[half][t][g]);
-                    }
-                }
-            }
-            page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
-            page[1] = __builtin_amdgcn_readfirstlane(page_next[1]);
-            load_keys(next);
-            __builtin_amdgcn_sched_barrier(0);
-
-            float s[RT][8];
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                static_for<8>([&](auto i) {
-                    constexpr int half = i.value / 4, r = i.value % 4;
-                    float x = -m[t];
-                    static_for<kGroups>([&](auto g) {
-                        constexpr int at = r * kGroups + g.value;
-                        x = fmaf(row_lane<at % 16>(kbase[half][at / 16]), qsum[t][g.value], x);
-                        x = fmaf(row_lane<at % 16>(kstep[half][at / 16]), acc[half][t][g.value][r], x);
-                    });
-                    s[t][i.value] = x;
+                    for (int i = 0; i < 4; ++i) f[i] = value_reg<NB, D>(vw[i / 2], i % 2, j, masks);
+                    return f;
+                },
+                [&] {
+                    page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
+                    page[1] = __builtin_amdgcn_readfirstlane(page_next[1]);
+                    load_keys(next);
+                    __builtin_amdgcn_sched_barrier(0);
                 });
-                if (!open) {
-                    int first = t0 + 4 * quad;
-                    asm volatile("" : "+v"(first));         // a branch, not a choice in every step
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = first + 16 * (i >> 2) + (i & 3);
-                        if (at >= min(lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
-                    }
-                }
-                float top = larger3(larger3(larger3(s[t][0], s[t][1], s[t][2]), s[t][3], s[t][4]),
-                                    larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
-                if (__any(top > above[t])) {
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    // m moves up to the largest score, or at first to it wherever it is
-                    const float up = top > fminf(above[t], 0.f) ? top : 0.f;
-                    const float f = above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-up);
-                    if (top > -INFINITY) above[t] = kSlack;
-                    m[t] += up;
-                    l[t] *= f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[t][i] -= up;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) bsum[t][g] *= f;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) o[t][j] *= f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
-                    l[t] += s[t][i];
-                }
-            }
-
-            float vstep[2][kGridRegs], vmid[2][kGridRegs];
-            float most = 0.f;
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) {
-                    vstep[half][k] = to_f32<T>(vgrid[half][k] & 0xffffu);
-                    vmid[half][k] = fmaf(vstep[half][k], NB == 4 ? 8.f : 128.f, to_f32<T>(vgrid[half][k] >> 16));
-                    most = fmaxf(most, vstep[half][k]);
-                }
-            if (__any(most >= step_lim && most > 0.f)) {
-#pragma unroll
-                for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
-                // the power of two at or below it
-                const float p2 = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
-                const float by = ldexpf(1.f / p2, kStepBits), f = step_by > 0.f ? by / step_by : 1.f;
-                step_lim = 2.f * p2;
-                step_by = by;
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) o[t][j] *= f;
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int k = 0; k < kGridRegs; ++k) vstep[half][k] *= step_by;
-
-            // weights times V's step, in binary16
-            static_for<kGroups>([&](auto g) {
-                u32x4 pf[RT];
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    static_for<4>([&](auto i) {
-                        constexpr int half = i.value / 2, r = i.value % 2 * 2;
-                        constexpr int at = r * kGroups + g.value, at1 = at + kGroups;
-                        const float x = s[t][2 * i.value], y = s[t][2 * i.value + 1];
-                        bsum[t][g.value] = fmaf(row_lane<at % 16>(vmid[half][at / 16]), x, bsum[t][g.value]);
-                        bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vmid[half][at1 / 16]), y, bsum[t][g.value]);
-                        pf[t][i.value] = round_pair(row_lane<at % 16>(vstep[half][at / 16]) * x,
-                                                    row_lane<at1 % 16>(vstep[half][at1 / 16]) * y);
-                    });
-                }
-#pragma unroll
-                for (int jj = 0; jj < G / 16; ++jj) {
-                    const int j = g.value * (G / 16) + jj;
-                    u32x4 vf;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // tokens 2i and 2i + 1 of the lane's eight
-                        uint32_t x[kValBytes > 4 ? kValBytes / 4 : 1], y[kValBytes > 4 ? kValBytes / 4 : 1];
-                        const uint32_t *v = vw[i / 2];
-                        if constexpr (kValBytes >= 4) {
-#pragma unroll
-                            for (int k = 0; k < kValBytes / 4; ++k) {
-                                x[k] = v[(i % 2 * 2) * (kValBytes / 4) + k];
-                                y[k] = v[(i % 2 * 2 + 1) * (kValBytes / 4) + k];
-                            }
-                        } else {
-                            x[0] = v[i % 2];
-                            y[0] = v[i % 2] >> 16;
-                        }
-                        vf[i] = value_pair<NB>(x, y, j, masks);
-                    }
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) o[t][j] = mfma32<false>(vf, pf[t], o[t][j]);
-                }
-            });
             load_values(next);
             __builtin_amdgcn_sched_barrier(0);
         }
-
-        // The four waves' parts, on the largest of their maxima.
-        const float unstep = step_by > 0.f ? 1.f / step_by : 0.f;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            l[t] = column_sum(l[t]);
-            if (quad == 0) {
-                ml[(wave * kRows + 16 * t + col) * 2] = above[t] < 0.f ? -INFINITY : m[t];
-                ml[(wave * kRows + 16 * t + col) * 2 + 1] = l[t];
-            }
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) bsum[t][g] = column_sum(bsum[t][g]);
-        }
-        const bool whole = count == along;
-        const int slot = 2 * w + (u_in > 0 ? 0 : 1);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int d0 = 0; d0 < D; d0 += kPart) {
-                // a lane has runs of G/16 neighbouring dimensions of its column
-#pragma unroll
-                for (int g = d0 / G; g < (d0 + kPart) / G; ++g)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int jj = 0; jj < G / 16; ++jj)
-                            part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
-                                fmaf(o[t][g * (G / 16) + jj][i], unstep, bsum[t][g]);
-                __syncthreads();
-                for (int x = threadIdx.x; x < 16 * kPart / 4; x += kAttnThreads) {
-                    const int r = x / (kPart / 4), e0 = d0 + x % (kPart / 4) * 4, row = row0 + 16 * t + r;
-                    if (row >= n_rows) break;
-                    float mk[kWaves], top = -INFINITY, all = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kWaves; ++k) {
-                        mk[k] = ml[(k * kRows + 16 * t + r) * 2];
-                        top = fmaxf(top, mk[k]);
-                    }
-                    f32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < kWaves; ++k) {
-                        if (mk[k] == -INFINITY) continue;
-                        const float f = __builtin_amdgcn_exp2f(mk[k] - top);
-                        all = fmaf(f, ml[(k * kRows + 16 * t + r) * 2 + 1], all);
-                        const f32x4 v = *reinterpret_cast<const f32x4 *>(part + (k * 16 + r) * kStride + e0 - d0);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[e] = fmaf(f, v[e], sum[e]);
-                    }
-                    float *to_o, *to_ml;
-                    int64_t at;
-                    if (!whole) {
-                        at = ((int64_t)h * 2 * d.workers + slot) * kRows + 16 * t + r;
-                        to_o = d.slot_o;
-                        to_ml = d.slot_ml;
-                    } else {
-                        at = (int64_t)h * d.s.n_tokens * a.per + (int64_t)rows.begin * a.per + row;
-                        to_o = d.row_o;
-                        to_ml = d.row_ml;
-                    }
-                    if (to_o) {
-                        *reinterpret_cast<f32x4 *>(to_o + at * D + e0) = sum;
-                        if (e0 == 0) *reinterpret_cast<f32x2 *>(to_ml + at * 2) = f32x2{top, all};
-                        continue;
-                    }
-                    const float inv = all > 0.f ? 1.f / all : 0.f;
-                    const int tok = rows.begin + row / a.per, hq = h * a.per + row % a.per;
-                    const uint2 packed = {from_f32<T>(sum[0] * inv) | from_f32<T>(sum[1] * inv) << 16,
-                                          from_f32<T>(sum[2] * inv) | from_f32<T>(sum[3] * inv) << 16};
-                    *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + e0) = packed;
-                    if (a.lse && e0 == 0)
-                        a.lse[(int64_t)tok * a.c.heads * a.per + hq] =
-                            all > 0.f ? (top + log2f(all)) * 0.6931471805599453f : -INFINITY;
-                }
-                __syncthreads();
-            }
+        finish<T, D, G, RT, kWaves>(w, a, d, x, h, run, ml, part);
     }
 }
 
-template <typename T, int NB, int D, int G, int RT>
+// ---- many rows: the products bound it --------------------------------------------------------
+// TW waves share each 16 * RT rows and take turns at tiles of 32 tokens; all waves of the block
+// meet the same 64 tokens a step, whose codes they widen together, a quarter each, into
+// fragments in LDS: widening is paid once for the block's rows. The next step's codes are on
+// their way during the products.
+constexpr int kWideStep = 64;
+
+template <int D>
+constexpr int wide_frags() { return kWideStep / 16 * (D / 32) + kWideStep / 32 * (D / 16); }     // of 1 KB
+
+template <typename T, int NB, int D, int G, int RT, int TW>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
+{
+    constexpr int kRows = 16 * RT * (kWaves / TW), kTurns = 2 / TW;
+    extern __shared__ int32_t shared[];
+    AttnSide d = side_of(a);
+    u32x4 *key_frags = reinterpret_cast<u32x4 *>(shared);                       // [4][D / 32][64]
+    u32x4 *val_frags = key_frags + 4 * (D / 32) * 64;                           // [2][D / 16][64]
+    float *part = reinterpret_cast<float *>(shared);                            // in their place
+    constexpr int kPart = kWaves * 16 * (part_dims(D) + kPartPad), kFrags = wide_frags<D>() * 256;
+    constexpr int kFloats = kFrags > kPart ? kFrags : kPart;
+    float *ml = part + kFloats;
+    int32_t *starts = reinterpret_cast<int32_t *>(ml + kWaves * 16 * RT * 2);
+    int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
+    int h, run, u, u_end;
+    if (!take_run<kRows>(a, d, starts, scan, h, run, u, u_end)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int turn0 = wave % TW;
+    const Spot<NB, D, G> spot;
+    const Masks masks = make_masks();
+
+    while (u < u_end) {
+        const Item x = item_at<kRows>(d, starts, a.per, u, u_end);
+        u += x.count;
+        Wave<D, G, RT> w;
+        begin<T>(w, a, d.causal, x, h, x.row0 + wave / TW * 16 * RT);
+        // what the block's rows see: the same for its waves, which go in step
+        const int last = (min(x.row0 + kRows, x.n_rows) - 1) / a.per;
+        const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
+        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
+        const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
+        uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4], vw[Spot<NB, D, G>::kValBytes];
+        Grids<D, G> gr[kTurns];
+        auto load_step = [&](int t0) {
+            const int mine = min(t0 + 16 * wave, x.len - 1);
+            const int64_t at = spot.first(a, d.s, h, page_at(d.s, table, mine), t0 + 16 * wave);
+            spot.keys(a, at, kw);
+            spot.values(a, at, vw);
+#pragma unroll
+            for (int turn = 0; turn < kTurns; ++turn)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int t = t0 + 32 * (turn0 + turn) + 16 * half;
+                    const int page = page_at(d.s, table, min(t, x.len - 1));
+                    const int64_t at = spot.first(a, d.s, h, page, t);
+                    spot.grids(a.c.k_meta, at, gr[turn].k[half]);
+                    spot.grids(a.c.v_meta, at, gr[turn].v[half]);
+                    gr[turn].good[half] = page < 0 ? 0 : x.len - t;
+                }
+        };
+        int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end);
+        if (t0 < t_end) load_step(t0);
+        for (; t0 < t_end; t0 += kWideStep) {
+            __syncthreads();                    // the last step's products have been made
+#pragma unroll
+            for (int mm = 0; mm < D / 32; ++mm)
+                key_frags[(wave * (D / 32) + mm) * 64 + lane] = key_frag<Types<T>::kBf16, NB>(kw + mm * (NB / 4));
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                const u32x2 f = {value_reg<NB, D>(vw, 0, j, masks), value_reg<NB, D>(vw, 1, j, masks)};
+                reinterpret_cast<u32x2 *>(val_frags + (wave / 2 * (D / 16) + j) * 64 + lane)[wave % 2] = f;
+            }
+            __syncthreads();
+            Grids<D, G> now[kTurns];
+#pragma unroll
+            for (int turn = 0; turn < kTurns; ++turn) now[turn] = gr[turn];
+            load_step(t0 + kWideStep < t_end ? t0 + kWideStep : t0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int turn = 0; turn < kTurns; ++turn) {
+                const int pair = turn0 + turn, t = t0 + 32 * pair;
+                if (t >= min(w.lim_high, t_end)) continue;
+                attend_step<T, NB>(
+                    w, now[turn], a.scale, t,
+                    [&](int half, int mm) { return key_frags[((2 * pair + half) * (D / 32) + mm) * 64 + lane]; },
+                    [&](int j) { return val_frags[(pair * (D / 16) + j) * 64 + lane]; }, [] {});
+            }
+        }
+        __syncthreads();                        // `part` lies over the fragments
+        finish<T, D, G, RT, TW>(w, a, d, x, h, run, ml, part);
+    }
+}
+
+template <typename T, int NB, int D, int G, int RT, int TW>
 hipError_t launch_one(const AttnArgs &a, hipStream_t stream)
 {
-    // at most 16 KB of starts, 1 KB and 33 KB: within what any launch may ask for
-    const int part = D < 128 ? D : 128, n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
+    // for few rows at most 16 KB of starts, 1 KB and 33 KB; for many 16 KB, 1 KB and 64 KB
+    const int n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
+    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad), frags = 1024 * wide_frags<D>();
     const size_t lds = 4 * (((size_t)n + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
-                       4 * (size_t)kWaves * 16 * (part + 4);
+                       (TW == kWaves ? part : max(part, frags));
     const int64_t runs = a.side[0].workers + (a.sides == 2 ? a.side[1].workers : 0);
-    attn_kernel<T, NB, D, G, RT><<<dim3((unsigned)(runs * a.c.heads)), kAttnThreads, lds, stream>>>(a);
+    const dim3 grid((unsigned)(runs * a.c.heads));
+    if constexpr (TW == kWaves) attn_kernel<T, NB, D, G, RT><<<grid, kAttnThreads, lds, stream>>>(a);
+    else attn_wide_kernel<T, NB, D, G, RT, TW><<<grid, kAttnThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, int NB, int D, int G>
 hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
-    if (a.side[0].tiles16 == 1) return launch_one<T, NB, D, G, 1>(a, stream);
-    if constexpr (D <= 128)
-        if (a.side[0].tiles16 == 2) return launch_one<T, NB, D, G, 2>(a, stream);
+    // rows to a tile: 16 to 128, or to 64 for 256-wide heads (whose sums fill the registers)
+    const int n = a.side[0].tiles16;
+    if (n == 1) return launch_one<T, NB, D, G, 1, 4>(a, stream);
+    if constexpr (D <= 128) {
+        if (n == 2) return launch_one<T, NB, D, G, 2, 4>(a, stream);
+        if (n == 4) return launch_one<T, NB, D, G, 2, 2>(a, stream);
+        if (n == 8) return launch_one<T, NB, D, G, 2, 1>(a, stream);
+    } else {
+        if (n == 2) return launch_one<T, NB, D, G, 1, 2>(a, stream);
+        if (n == 4) return launch_one<T, NB, D, G, 1, 1>(a, stream);
+    }
     return hipErrorInvalidValue;
 }
 

@@ -121,12 +121,14 @@ struct Plan {
     size_t bytes;
 };
 
-// Query rows to a tile: 16 where a sequence has no more, for its work is to read the cache;
-// else 32, so that each code read and widened meets more rows (256-wide heads fill the
-// registers with 16).
+// Query rows to a tile, in 16s: 16 where a sequence has no more, for its work is to read the
+// cache; else as many as its rows fill, up to 128 (64 for 256-wide heads).
 int tiles_for(int64_t rows, int dim)
 {
-    return rows <= 16 || dim == 256 ? 1 : 2;
+    const int most = dim == 256 ? 4 : 8;
+    int t = 1;
+    while (t < most && 16 * t < rows) t *= 2;
+    return t;
 }
 
 // The longest side that one block takes alone: cutting it saves four steps at most, and
@@ -149,10 +151,11 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         x.tiles16 = tiles_for(tile_rows, c->head_dim);
         const int64_t step = hqq::kStep;
         x.unit = (int)(longest <= kWhole ? (longest + step) / step * step : step);
-        // what the 256 CUs hold at once, or the most units that there can be
+        // no more than the 256 CUs hold at once (a block more would take as long again), nor than
+        // the units that there can be
         const int64_t blocks = x.tiles16 == 1 ? 768 : 512;
         const int64_t units = (rows / (16 * x.tiles16) + n_seqs) * hqq::units_along((int32_t)longest, x.unit);
-        const int64_t each = (blocks + c->n_heads - 1) / c->n_heads;
+        const int64_t each = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
         x.workers = (int)(each < units ? each : units);
         const size_t slots = (size_t)c->n_heads * 2 * x.workers * 16 * x.tiles16;
         x.starts = take(4 * ((size_t)n_seqs + 1));

@@ -99,7 +99,7 @@ struct AttnSide {
     float *row_o, *row_ml;      // [heads][n_tokens * per][dim], [..][2], or null
     int32_t workers;            // most runs of a head's units
     int32_t unit;               // tokens
-    int32_t tiles16;            // rows_per / 16: 1 or 2
+    int32_t tiles16;            // rows_per / 16: 1, 2, 4 or 8
     int32_t causal;             // rows see their own position and what is before it, else all
 };
 

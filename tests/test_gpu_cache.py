@@ -222,6 +222,13 @@ ATTEND = [
     (B, 8, 128, 64, 16, 2, 2, [3, 5], [6, 5]),                 # more rows than tokens: they see nothing
     (F, 4, 128, 64, 64, 1, 1, [130, 64], [0, 64]),
     (B, 8, 64, 32, 16, 2, 40, [65], [1]),                      # more query heads than a tile holds
+    (B, 4, 128, 64, 16, 2, 8, [700, 33, 90, 5], [6, 7, 5, 5]),
+    (F, 8, 128, 64, 64, 1, 5, [1000, 64], [9, 10]),
+    (F, 4, 64, 32, 32, 2, 2, [900, 129], [300, 129]),
+    (B, 8, 64, 64, 16, 1, 1, [777, 100, 0, 65], [500, 100, 0, 64]),
+    (B, 4, 256, 128, 64, 1, 4, [600, 61], [30, 61]),
+    (F, 8, 256, 64, 16, 1, 16, [130, 400], [2, 1]),
+    (F, 4, 128, 128, 128, 2, 1, [1500, 20], [129, 20]),
 ]
 
 
@@ -249,11 +256,12 @@ def test_attention(H, dtype, nbits, dim, group, page, kv, per, lens, new):
     lse = torch.full((n + 2, kv * per), 13.0, dtype=torch.float32, device="cuda")
     H.hqq_cache_attention(cache, i32(table), i32(lens), q, out, lse=lse, cu_tokens=i32(cu))
     mine = torch.tensor([True] * n + [False] * 2)
-    R.check_attention(out, lse, R.attention(R.Held(cache), table, lens, cu + [], q, dim ** -0.5), mine)
+    ref = R.attention(R.Held(cache), table, lens, cu, q, dim ** -0.5)
+    R.check_attention(out, lse, ref, mine)
     assert (obuf[n:] == 11).all() and (obuf[:, 0] == 11).all() and (obuf[:, -1] == 11).all() and (lse[n:] == 13).all()
     if len(set(new)) == 1 and new[0] > 0:       # the same without row offsets
         again = H.cache_attention(cache, i32(table), i32(lens), q[:n])
-        assert torch.equal(again, out[:n])
+        R.check_attention(again, None, tuple(x[:n] for x in ref), mine[:n])
 
 
 @pytest.mark.parametrize("dtype,nbits,dim,group,page,kv,per,lens,new,prefix", [
