@@ -343,45 +343,39 @@ __device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool
     w.step_lim = w.step_by = 0.f;
 }
 
-// The grids of a step's two halves of 16 tokens, as the lanes hold them, and how many tokens
-// of each half there are (negative: none).
+// The lanes' places for the grids of 16 tokens: quad x holds those of tokens 4x..4x+3, lane c
+// of register k the one of token (c + 16 k) / kGroups of them, group (c + 16 k) % kGroups.
 template <int D, int G>
-struct Grids {
-    static constexpr int kGrids = 4 * (D / G), kRegs = (kGrids + 15) / 16;
-    uint32_t k[2][kRegs], v[2][kRegs];
-    int good[2];
+struct Places {
+    static constexpr int kGroups = D / G, kGrids = 4 * kGroups, kRegs = (kGrids + 15) / 16;
+    static __device__ __forceinline__ int token(int k)
+    {
+        const int lane = threadIdx.x & 63;
+        return lane / 16 * 4 + ((lane & 15 & (kGrids - 1)) + 16 * k) / kGroups;
+    }
 };
 
-// One step: 32 tokens from t0 for the wave's rows. key(half, mm) and value(j) give the A
-// fragments; after_keys() is called when no more keys are needed.
-template <typename T, int NB, int D, int G, int RT, typename Key, typename Value, typename After>
-__device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, float scale, int t0, Key key, Value value,
-                                            After after_keys)
+// One step: 32 tokens from t0 for the wave's rows, good[half] of each 16 there (or more; none
+// if negative). When some are not, or not for all rows, close() is called first, to make the
+// grids of the missing ones {0, 0}. key_grid(half, k) gives {step * scale, base} of a lane's
+// place, value_grid {step, middle}; key(half, mm) and value(j) the A fragments. after_keys() is
+// called when no more keys are needed, before the values' grids and fragments are.
+template <typename T, int D, int G, int RT, typename Close, typename KeyGrid, typename Key, typename After, typename ValueGrid,
+          typename Value>
+__device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
+                                            Key key, After after_keys, ValueGrid value_grid, Value value)
 {
     constexpr bool kBf16 = Types<T>::kBf16;
-    constexpr int kGroups = D / G, kGrids = Grids<D, G>::kGrids, kRegs = Grids<D, G>::kRegs;
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-    const bool open = t0 + kTile <= w.lim_low && gr.good[0] >= 16 && gr.good[1] >= 16;
-    if (!open) {
-        int first = 4 * quad;
-        asm volatile("" : "+v"(first));                     // a branch, not a choice in every step
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int k = 0; k < kRegs; ++k) {
-                const int token = first + ((col & (kGrids - 1)) + 16 * k) / kGroups;
-                if (token >= gr.good[half]) gr.k[half][k] = gr.v[half][k] = 0;
-            }
-    }
+    constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
+    const int quad = (threadIdx.x & 63) >> 4;
+    const bool open = t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
+    if (!open) close();
     f32x4 acc[2][RT][kGroups];
-    float kstep[2][kRegs], kbase[2][kRegs];
+    f32x2 kgrid[2][kRegs];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int k = 0; k < kRegs; ++k) {
-            kstep[half][k] = to_f32<T>(gr.k[half][k] & 0xffffu) * scale;
-            kbase[half][k] = to_f32<T>(gr.k[half][k] >> 16);
-        }
+        for (int k = 0; k < kRegs; ++k) kgrid[half][k] = key_grid(half, k);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
@@ -397,36 +391,48 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, 
     after_keys();
 
     float s[RT][8];
+    static_for<8>([&](auto i) {
+        constexpr int half = i.value / 4, r = i.value % 4;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        static_for<8>([&](auto i) {
-            constexpr int half = i.value / 4, r = i.value % 4;
-            float x = -w.m[t];
-            static_for<kGroups>([&](auto g) {
-                constexpr int at = r * kGroups + g.value;
-                x = fmaf(row_lane<at % 16>(kbase[half][at / 16]), w.qsum[t][g.value], x);
-                x = fmaf(row_lane<at % 16>(kstep[half][at / 16]), acc[half][t][g.value][r], x);
-            });
-            s[t][i.value] = x;
+        for (int t = 0; t < RT; ++t) s[t][i.value] = -w.m[t];
+        static_for<kGroups>([&](auto g) {
+            constexpr int at = r * kGroups + g.value;
+            const float step = row_lane<at % 16>(kgrid[half][at / 16][0]), base = row_lane<at % 16>(kgrid[half][at / 16][1]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                s[t][i.value] = fmaf(base, w.qsum[t][g.value], s[t][i.value]);
+                s[t][i.value] = fmaf(step, acc[half][t][g.value][r], s[t][i.value]);
+            }
         });
-        if (!open) {
-            int first = t0 + 4 * quad;
-            asm volatile("" : "+v"(first));
+    });
+    if (!open) {
+        int first = t0 + 4 * quad;
+        asm volatile("" : "+v"(first));                     // a branch, not a choice in every step
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int at = first + 16 * (i >> 2) + (i & 3);
-                if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + gr.good[i >> 2])) s[t][i] = -INFINITY;
+                if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
             }
-        }
-        float top = larger3(larger3(larger3(s[t][0], s[t][1], s[t][2]), s[t][3], s[t][4]),
-                            larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
-        if (__any(top > w.above[t])) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+    }
+    float top[RT];
+    bool grown = false;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        top[t] = larger3(larger3(larger3(s[t][0], s[t][1], s[t][2]), s[t][3], s[t][4]),
+                         larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
+        grown = grown || top[t] > w.above[t];
+    }
+    if (__any(grown)) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            top[t] = fmaxf(top[t], __shfl_xor(top[t], 16));
+            top[t] = fmaxf(top[t], __shfl_xor(top[t], 32));
             // m moves up to the largest score, or at first to it wherever it is
-            const float up = top > fminf(w.above[t], 0.f) ? top : 0.f;
+            const float up = top[t] > fminf(w.above[t], 0.f) ? top[t] : 0.f;
             const float f = w.above[t] < 0.f ? 1.f : __builtin_amdgcn_exp2f(-up);
-            if (top > -INFINITY) w.above[t] = kSlack;
+            if (top[t] > -INFINITY) w.above[t] = kSlack;
             w.m[t] += up;
             w.l[t] *= f;
 #pragma unroll
@@ -436,22 +442,16 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, 
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) w.o[t][j] *= f;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
-            w.l[t] += s[t][i];
-        }
     }
 
-    float vstep[2][kRegs], vmid[2][kRegs];
+    f32x2 vgrid[2][kRegs];
     float most = 0.f;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int k = 0; k < kRegs; ++k) {
-            vstep[half][k] = to_f32<T>(gr.v[half][k] & 0xffffu);
-            vmid[half][k] = fmaf(vstep[half][k], NB == 4 ? 8.f : 128.f, to_f32<T>(gr.v[half][k] >> 16));
-            most = fmaxf(most, vstep[half][k]);
+            vgrid[half][k] = value_grid(half, k);
+            most = fmaxf(most, vgrid[half][k][0]);
         }
     if (__any(most >= w.step_lim && most > 0.f)) {
 #pragma unroll
@@ -469,8 +469,15 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, 
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int k = 0; k < kRegs; ++k) vstep[half][k] *= w.step_by;
+        for (int k = 0; k < kRegs; ++k) vgrid[half][k][0] *= w.step_by;
 
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
+            w.l[t] += s[t][i];
+        }
     // weights times V's step, in binary16
     static_for<kGroups>([&](auto g) {
         u32x4 pf[RT];
@@ -480,10 +487,10 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, 
                 constexpr int half = i.value / 2, r = i.value % 2 * 2;
                 constexpr int at = r * kGroups + g.value, at1 = at + kGroups;
                 const float x = s[t][2 * i.value], y = s[t][2 * i.value + 1];
-                w.bsum[t][g.value] = fmaf(row_lane<at % 16>(vmid[half][at / 16]), x, w.bsum[t][g.value]);
-                w.bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vmid[half][at1 / 16]), y, w.bsum[t][g.value]);
-                pf[t][i.value] = round_pair(row_lane<at % 16>(vstep[half][at / 16]) * x,
-                                            row_lane<at1 % 16>(vstep[half][at1 / 16]) * y);
+                w.bsum[t][g.value] = fmaf(row_lane<at % 16>(vgrid[half][at / 16][1]), x, w.bsum[t][g.value]);
+                w.bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vgrid[half][at1 / 16][1]), y, w.bsum[t][g.value]);
+                pf[t][i.value] = round_pair(row_lane<at % 16>(vgrid[half][at / 16][0]) * x,
+                                            row_lane<at1 % 16>(vgrid[half][at1 / 16][0]) * y);
             });
         }
 #pragma unroll
@@ -495,6 +502,18 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, Grids<D, G> &gr, 
         }
     });
 }
+
+// {step * by, base + middle * step} of a grid.
+template <typename T>
+__device__ __forceinline__ f32x2 open_grid(uint32_t x, float by, float middle)
+{
+    const float step = to_f32<T>(x & 0xffffu);
+    return f32x2{step * by, fmaf(step, middle, to_f32<T>(x >> 16))};
+}
+template <typename T>
+__device__ __forceinline__ f32x2 open_key_grid(uint32_t x, float scale) { return open_grid<T>(x, scale, 0.f); }
+template <typename T, int NB>
+__device__ __forceinline__ f32x2 open_value_grid(uint32_t x) { return open_grid<T>(x, 1.f, NB == 4 ? 8.f : 128.f); }
 
 constexpr int part_dims(int dim) { return dim < 128 ? dim : 128; }      // joined over the waves at a time
 constexpr int kPartPad = 4;
@@ -592,7 +611,7 @@ struct Spot {
     static constexpr int kRow = D * NB / 8;         // bytes of a token's codes
     static constexpr int kKeyBytes = kRow / 4;      // a lane's quarter of a token's key
     static constexpr int kValBytes = kRow / 16;     // a row of a token's value
-    static constexpr int kGrids = Grids<D, G>::kGrids, kRegs = Grids<D, G>::kRegs;
+    static constexpr int kGrids = Places<D, G>::kGrids, kRegs = Places<D, G>::kRegs;
     unsigned key_at, val_at, grid_at;
     __device__ __forceinline__ Spot()
     {
@@ -701,7 +720,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)w.lim_high);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[2][Spot<NB, D, G>::kKeyBytes / 4], vw[2][Spot<NB, D, G>::kValBytes];
-        Grids<D, G> gr;
+        uint32_t kg[2][Places<D, G>::kRegs], vg[2][Places<D, G>::kRegs];
         int page[2];
         auto find = [&](int t0, int (&page)[2]) {
 #pragma unroll
@@ -712,7 +731,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             for (int half = 0; half < 2; ++half) {
                 const int64_t at = spot.first(a, d.s, h, page[half], t0 + 16 * half);
                 spot.keys(a, at, kw[half]);
-                spot.grids(a.c.k_meta, at, gr.k[half]);
+                spot.grids(a.c.k_meta, at, kg[half]);
             }
         };
         auto load_values = [&](int t0) {
@@ -720,7 +739,7 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             for (int half = 0; half < 2; ++half) {
                 const int64_t at = spot.first(a, d.s, h, page[half], t0 + 16 * half);
                 spot.values(a, at, vw[half]);
-                spot.grids(a.c.v_meta, at, gr.v[half]);
+                spot.grids(a.c.v_meta, at, vg[half]);
             }
         };
         int t0 = (int)min((int64_t)x.u_in * d.unit + wave * kTile, (int64_t)t_end);
@@ -734,24 +753,34 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             // its values once this one's are: both are under way during half a step, with no
             // registers but their own.
             const int next = t0 + kStep < t_end ? t0 + kStep : t0;
-            int page_next[2];
+            int page_next[2], good[2];
             find(next, page_next);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) gr.good[half] = page[half] < 0 ? 0 : x.len - t0 - 16 * half;
-            attend_step<T, NB>(
-                w, gr, a.scale, t0,
-                [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
-                [&](int j) {
-                    u32x4 f;
+            for (int half = 0; half < 2; ++half) good[half] = page[half] < 0 ? 0 : x.len - t0 - 16 * half;
+            attend_step<T>(
+                w, t0, good,
+                [&] {
+                    asm volatile("");
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = value_reg<NB, D>(vw[i / 2], i % 2, j, masks);
-                    return f;
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int k = 0; k < Places<D, G>::kRegs; ++k)
+                            if (Places<D, G>::token(k) >= good[half]) kg[half][k] = vg[half][k] = 0;
                 },
+                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); },
+                [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
                 [&] {
                     page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
                     page[1] = __builtin_amdgcn_readfirstlane(page_next[1]);
                     load_keys(next);
                     __builtin_amdgcn_sched_barrier(0);
+                },
+                [&](int half, int k) { return open_value_grid<T, NB>(vg[half][k]); },
+                [&](int j) {
+                    u32x4 f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = value_reg<NB, D>(vw[i / 2], i % 2, j, masks);
+                    return f;
                 });
             load_values(next);
             __builtin_amdgcn_sched_barrier(0);
@@ -760,34 +789,48 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
     }
 }
 
-// ---- many rows: the products bound it --------------------------------------------------------
+// ---- many rows: the arithmetic bounds it ------------------------------------------------------
 // TW waves share each 16 * RT rows and take turns at tiles of 32 tokens; all waves of the block
-// meet the same 64 tokens a step, whose codes they widen together, a quarter each, into
-// fragments in LDS: widening is paid once for the block's rows. The next step's codes are on
-// their way during the products.
-constexpr int kWideStep = 64;
+// meet the same 64 tokens a step. A quarter each, they widen the step's codes into fragments
+// and open its grids, in LDS: that is paid once for the block's rows. Where LDS has room for
+// two steps (heads of up to 128), the next step's are made in the other half, so that one
+// barrier a step is enough; the codes of the step after that are on their way meanwhile.
+constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;
 
+template <int D, int G>
+struct WideStep {
+    u32x4 key[kWideTiles][D / 32][64];          // A fragments
+    u32x4 value[kWideTiles / 2][D / 16][64];
+    f32x2 key_grid[kWideTiles][Places<D, G>::kRegs][64];
+    f32x2 value_grid[kWideTiles][Places<D, G>::kRegs][64];
+    int good[kWideTiles];
+};
 template <int D>
-constexpr int wide_frags() { return kWideStep / 16 * (D / 32) + kWideStep / 32 * (D / 16); }     // of 1 KB
+constexpr int wide_buffers() { return D <= 128 ? 2 : 1; }
+template <int D, int G>
+constexpr size_t wide_bytes()       // of the steps, or of what joins the waves in their place
+{
+    const size_t steps = wide_buffers<D>() * sizeof(WideStep<D, G>);
+    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
+    return (steps > part ? steps : part) + 15 & ~size_t(15);
+}
 
 template <typename T, int NB, int D, int G, int RT, int TW>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
 {
-    constexpr int kRows = 16 * RT * (kWaves / TW), kTurns = 2 / TW;
-    extern __shared__ int32_t shared[];
+    constexpr int kRows = 16 * RT * (kWaves / TW), kTurns = 2 / TW, kBuffers = wide_buffers<D>();
+    constexpr int kRegs = Places<D, G>::kRegs;
+    static_assert(kWaves == kWideTiles, "a wave widens 16 tokens");
+    extern __shared__ u32x4 shared4[];
     AttnSide d = side_of(a);
-    u32x4 *key_frags = reinterpret_cast<u32x4 *>(shared);                       // [4][D / 32][64]
-    u32x4 *val_frags = key_frags + 4 * (D / 32) * 64;                           // [2][D / 16][64]
-    float *part = reinterpret_cast<float *>(shared);                            // in their place
-    constexpr int kPart = kWaves * 16 * (part_dims(D) + kPartPad), kFrags = wide_frags<D>() * 256;
-    constexpr int kFloats = kFrags > kPart ? kFrags : kPart;
-    float *ml = part + kFloats;
+    WideStep<D, G> *steps = reinterpret_cast<WideStep<D, G> *>(shared4);
+    float *part = reinterpret_cast<float *>(shared4);
+    float *ml = reinterpret_cast<float *>(shared4 + wide_bytes<D, G>() / 16);
     int32_t *starts = reinterpret_cast<int32_t *>(ml + kWaves * 16 * RT * 2);
     int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
     int h, run, u, u_end;
     if (!take_run<kRows>(a, d, starts, scan, h, run, u, u_end)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int turn0 = wave % TW;
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
 
@@ -801,54 +844,77 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
-        uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4], vw[Spot<NB, D, G>::kValBytes];
-        Grids<D, G> gr[kTurns];
-        auto load_step = [&](int t0) {
-            const int mine = min(t0 + 16 * wave, x.len - 1);
-            const int64_t at = spot.first(a, d.s, h, page_at(d.s, table, mine), t0 + 16 * wave);
+        uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4], vw[Spot<NB, D, G>::kValBytes], kg[kRegs], vg[kRegs];
+        int good;
+        // this wave's 16 tokens of a step, at positions from t
+        auto page_of_step = [&](int t0) { return page_at(d.s, table, min(t0 + 16 * wave, x.len - 1)); };
+        auto fetch = [&](int t, int page) {
+            const int64_t at = spot.first(a, d.s, h, page, t);
             spot.keys(a, at, kw);
             spot.values(a, at, vw);
-#pragma unroll
-            for (int turn = 0; turn < kTurns; ++turn)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t = t0 + 32 * (turn0 + turn) + 16 * half;
-                    const int page = page_at(d.s, table, min(t, x.len - 1));
-                    const int64_t at = spot.first(a, d.s, h, page, t);
-                    spot.grids(a.c.k_meta, at, gr[turn].k[half]);
-                    spot.grids(a.c.v_meta, at, gr[turn].v[half]);
-                    gr[turn].good[half] = page < 0 ? 0 : x.len - t;
-                }
+            spot.grids(a.c.k_meta, at, kg);
+            spot.grids(a.c.v_meta, at, vg);
+            good = page < 0 ? 0 : x.len - t;
         };
-        int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end);
-        if (t0 < t_end) load_step(t0);
-        for (; t0 < t_end; t0 += kWideStep) {
-            __syncthreads();                    // the last step's products have been made
+        auto widen = [&](WideStep<D, G> &to) {
 #pragma unroll
-            for (int mm = 0; mm < D / 32; ++mm)
-                key_frags[(wave * (D / 32) + mm) * 64 + lane] = key_frag<Types<T>::kBf16, NB>(kw + mm * (NB / 4));
+            for (int mm = 0; mm < D / 32; ++mm) to.key[wave][mm][lane] = key_frag<Types<T>::kBf16, NB>(kw + mm * (NB / 4));
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 const u32x2 f = {value_reg<NB, D>(vw, 0, j, masks), value_reg<NB, D>(vw, 1, j, masks)};
-                reinterpret_cast<u32x2 *>(val_frags + (wave / 2 * (D / 16) + j) * 64 + lane)[wave % 2] = f;
+                reinterpret_cast<u32x2 *>(&to.value[wave / 2][j][lane])[wave % 2] = f;
             }
-            __syncthreads();
-            Grids<D, G> now[kTurns];
 #pragma unroll
-            for (int turn = 0; turn < kTurns; ++turn) now[turn] = gr[turn];
-            load_step(t0 + kWideStep < t_end ? t0 + kWideStep : t0);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int turn = 0; turn < kTurns; ++turn) {
-                const int pair = turn0 + turn, t = t0 + 32 * pair;
-                if (t >= min(w.lim_high, t_end)) continue;
-                attend_step<T, NB>(
-                    w, now[turn], a.scale, t,
-                    [&](int half, int mm) { return key_frags[((2 * pair + half) * (D / 32) + mm) * 64 + lane]; },
-                    [&](int j) { return val_frags[(pair * (D / 16) + j) * 64 + lane]; }, [] {});
+            for (int k = 0; k < kRegs; ++k) {
+                const bool in = Places<D, G>::token(k) < good;
+                to.key_grid[wave][k][lane] = open_key_grid<T>(in ? kg[k] : 0u, a.scale);
+                to.value_grid[wave][k][lane] = open_value_grid<T, NB>(in ? vg[k] : 0u);
+            }
+            if (lane == 0) to.good[wave] = good;
+        };
+        int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end), page = 0, buffer = 0;
+        // a step that there is not is fetched like the last one, and not used
+        auto within = [&](int t) { return t < t_end ? t : t0; };
+        if (t0 < t_end) {
+            fetch(t0 + 16 * wave, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
+            if constexpr (kBuffers == 2) {
+                widen(steps[0]);
+                const int next = within(t0 + kWideStep);
+                fetch(next + 16 * wave, __builtin_amdgcn_readfirstlane(page_of_step(next)));
+                page = page_of_step(within(t0 + 2 * kWideStep));
+            } else {
+                page = page_of_step(within(t0 + kWideStep));
             }
         }
-        __syncthreads();                        // `part` lies over the fragments
+        for (; t0 < t_end; t0 += kWideStep) {
+            __syncthreads();        // the last step's products have been made, this one's widened (two buffers)
+            constexpr int kAhead = kBuffers;
+            if constexpr (kBuffers == 2) {
+                widen(steps[buffer ^ 1]);
+            } else {
+                widen(steps[0]);
+                __syncthreads();
+            }
+            const int next = within(t0 + kAhead * kWideStep);
+            fetch(next + 16 * wave, __builtin_amdgcn_readfirstlane(page));
+            page = page_of_step(within(t0 + (kAhead + 1) * kWideStep));
+            __builtin_amdgcn_sched_barrier(0);
+            const WideStep<D, G> &now = steps[buffer];
+#pragma unroll
+            for (int turn = 0; turn < kTurns; ++turn) {
+                const int pair = wave % TW + turn, t = t0 + 32 * pair;
+                if (t >= min(w.lim_high, t_end)) continue;
+                const int both[2] = {__builtin_amdgcn_readfirstlane(now.good[2 * pair]),
+                                     __builtin_amdgcn_readfirstlane(now.good[2 * pair + 1])};
+                attend_step<T>(
+                    w, t, both, [] {}, [&](int half, int k) { return now.key_grid[2 * pair + half][k][lane]; },
+                    [&](int half, int mm) { return now.key[2 * pair + half][mm][lane]; }, [] {},
+                    [&](int half, int k) { return now.value_grid[2 * pair + half][k][lane]; },
+                    [&](int j) { return now.value[pair][j][lane]; });
+            }
+            if constexpr (kBuffers == 2) buffer ^= 1;
+        }
+        __syncthreads();                        // `part` lies over the steps
         finish<T, D, G, RT, TW>(w, a, d, x, h, run, ml, part);
     }
 }
@@ -856,11 +922,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
 template <typename T, int NB, int D, int G, int RT, int TW>
 hipError_t launch_one(const AttnArgs &a, hipStream_t stream)
 {
-    // for few rows at most 16 KB of starts, 1 KB and 33 KB; for many 16 KB, 1 KB and 64 KB
+    // for few rows at most 16 KB of starts, 1 KB and 33 KB; for many 16 KB, 1 KB and 72 KB
     const int n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
-    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad), frags = 1024 * wide_frags<D>();
+    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
     const size_t lds = 4 * (((size_t)n + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
-                       (TW == kWaves ? part : max(part, frags));
+                       (TW == kWaves ? part : wide_bytes<D, G>());
     const int64_t runs = a.side[0].workers + (a.sides == 2 ? a.side[1].workers : 0);
     const dim3 grid((unsigned)(runs * a.c.heads));
     if constexpr (TW == kWaves) attn_kernel<T, NB, D, G, RT><<<grid, kAttnThreads, lds, stream>>>(a);
