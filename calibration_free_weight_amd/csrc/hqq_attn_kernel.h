@@ -33,8 +33,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
-constexpr int kAttnThreads = 256;
-constexpr int kWaves = kAttnThreads / 64;
+constexpr int kWaves = 4;                   // of a block for few rows
 constexpr int kTile = 32;                   // tokens of a wave's step
 static_assert(kTile * kWaves == kStep, "a step is a tile for each wave");
 
@@ -175,8 +174,10 @@ __device__ __forceinline__ float larger3(float a, float b, float c)
 template <int BYTES>
 __device__ __forceinline__ void load_words(Global p, uint32_t offset, uint32_t (&w)[BYTES / 4])
 {
-    static_assert(BYTES == 8 || BYTES % 16 == 0, "8 or a multiple of 16");
-    if constexpr (BYTES % 16 == 0) {
+    static_assert(BYTES == 4 || BYTES == 8 || BYTES % 16 == 0, "4, 8 or a multiple of 16");
+    if constexpr (BYTES == 4) {
+        w[0] = load<uint32_t>(p, offset);
+    } else if constexpr (BYTES % 16 == 0) {
 #pragma unroll
         for (int k = 0; k < BYTES / 16; ++k) {
             const u32x4 x = load<u32x4>(p, offset + 16 * k);
@@ -211,11 +212,11 @@ __device__ __forceinline__ float column_sum(float x)
 }
 
 // The units before each sequence's, in LDS: starts[n_seqs] is their sum.
-template <int ROWS>
+template <int ROWS, int WAVES>
 __device__ void lay_out(const AttnSide &d, int per, int32_t *starts, int32_t *scan)
 {
     const int t = threadIdx.x, n = d.s.n_seqs;
-    const int each = (n + kAttnThreads - 1) / kAttnThreads, b0 = min(t * each, n), b1 = min(b0 + each, n);
+    const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
         const Rows r = rows_of(d.s, b);
@@ -232,7 +233,7 @@ __device__ void lay_out(const AttnSide &d, int per, int32_t *starts, int32_t *sc
     if ((t & 63) == 63) scan[t >> 6] = run;
     __syncthreads();
     int before = run - sum, total = 0;
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         if (w < (t >> 6)) before += scan[w];
         total += scan[w];
     }
@@ -370,39 +371,37 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, int t0, const int
     const int quad = (threadIdx.x & 63) >> 4;
     const bool open = t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
     if (!open) close();
-    f32x4 acc[2][RT][kGroups];
-    f32x2 kgrid[2][kRegs];
+    float s[RT][8];
+    static_for<2>([&](auto half) {
+        f32x4 acc[RT][kGroups];
+        f32x2 kgrid[kRegs];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int k = 0; k < kRegs; ++k) kgrid[half][k] = key_grid(half, k);
+        for (int k = 0; k < kRegs; ++k) kgrid[k] = key_grid(half.value, k);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) acc[half][t][g] = f32x4{0, 0, 0, 0};
+            for (int t = 0; t < RT; ++t) acc[t][g] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int mm = g * G / 32; mm < (g + 1) * G / 32; ++mm) {
-                const u32x4 kf = key(half, mm);
+                const u32x4 kf = key(half.value, mm);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) acc[half][t][g] = mfma32<kBf16>(kf, w.qf[t][mm], acc[half][t][g]);
+                for (int t = 0; t < RT; ++t) acc[t][g] = mfma32<kBf16>(kf, w.qf[t][mm], acc[t][g]);
             }
         }
-    }
-    after_keys();
-
-    float s[RT][8];
-    static_for<8>([&](auto i) {
-        constexpr int half = i.value / 4, r = i.value % 4;
+        if constexpr (half.value == 1) after_keys();
+        static_for<4>([&](auto r) {
+            constexpr int i = 4 * half.value + r.value;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) s[t][i.value] = -w.m[t];
-        static_for<kGroups>([&](auto g) {
-            constexpr int at = r * kGroups + g.value;
-            const float step = row_lane<at % 16>(kgrid[half][at / 16][0]), base = row_lane<at % 16>(kgrid[half][at / 16][1]);
+            for (int t = 0; t < RT; ++t) s[t][i] = -w.m[t];
+            static_for<kGroups>([&](auto g) {
+                constexpr int at = r.value * kGroups + g.value;
+                const float step = row_lane<at % 16>(kgrid[at / 16][0]), base = row_lane<at % 16>(kgrid[at / 16][1]);
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                s[t][i.value] = fmaf(base, w.qsum[t][g.value], s[t][i.value]);
-                s[t][i.value] = fmaf(step, acc[half][t][g.value][r], s[t][i.value]);
-            }
+                for (int t = 0; t < RT; ++t) {
+                    s[t][i] = fmaf(base, w.qsum[t][g.value], s[t][i]);
+                    s[t][i] = fmaf(step, acc[t][g.value][r.value], s[t][i]);
+                }
+            });
         });
     });
     if (!open) {
@@ -520,14 +519,14 @@ constexpr int kPartPad = 4;
 
 // Joins what TW waves found for the same rows, each on its own tokens, on the largest of their
 // maxima, and writes it: waves TW * r .. TW * r + TW - 1 have rows 16 * RT * r .. of the item.
-// ml: [kWaves][16 * RT][2]; part: [kWaves][16][part_dims + kPartPad]. Blocks come and leave in
+// ml: [WAVES][16 * RT][2]; part: [WAVES][16][part_dims + kPartPad]. Blocks come and leave in
 // step.
-template <typename T, int D, int G, int RT, int TW>
+template <typename T, int D, int G, int RT, int TW, int WAVES>
 __device__ __forceinline__ void finish(Wave<D, G, RT> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
                                        float *ml, float *part)
 {
     constexpr int kGroups = D / G, kPart = part_dims(D), kStride = kPart + kPartPad;
-    constexpr int kRowWaves = kWaves / TW, kRows = 16 * RT * kRowWaves;
+    constexpr int kRowWaves = WAVES / TW, kRows = 16 * RT * kRowWaves;
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
     const float unstep = w.step_by > 0.f ? 1.f / w.step_by : 0.f;
 #pragma unroll
@@ -556,7 +555,7 @@ __device__ __forceinline__ void finish(Wave<D, G, RT> &w, const AttnArgs &a, con
                         part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
                             fmaf(w.o[t][g * (G / 16) + jj][i], unstep, w.bsum[t][g]);
             __syncthreads();
-            for (int y = threadIdx.x; y < kRowWaves * 16 * kPart / 4; y += kAttnThreads) {
+            for (int y = threadIdx.x; y < kRowWaves * 16 * kPart / 4; y += 64 * WAVES) {
                 const int r = y / (kPart / 4) % 16, first = y / (kPart / 4) / 16 * TW, e0 = d0 + y % (kPart / 4) * 4;
                 const int in_item = first / TW * 16 * RT + 16 * t + r, row = x.row0 + in_item;
                 if (row >= x.n_rows) break;
@@ -670,18 +669,18 @@ __device__ __forceinline__ Masks make_masks()
 }
 
 // Which side and run a block has; the units laid out in LDS. False if it has nothing to do.
-template <int ROWS>
+template <int ROWS, int WAVES>
 __device__ __forceinline__ bool take_run(const AttnArgs &a, AttnSide &d, int32_t *starts, int32_t *scan, int &h, int &run,
                                          int &u, int &u_end)
 {
     const unsigned blocks0 = (unsigned)a.side[0].workers * a.c.heads;
     unsigned block = blockIdx.x;
     if (block >= blocks0) block -= blocks0;
-    lay_out<ROWS>(d, a.per, starts, scan);
+    lay_out<ROWS, WAVES>(d, a.per, starts, scan);
     h = (int)(block % (unsigned)a.c.heads);
     run = (int)(block / (unsigned)a.c.heads);
     if (block == 0 && d.starts)
-        for (int b = threadIdx.x; b <= d.s.n_seqs; b += kAttnThreads) d.starts[b] = starts[b];
+        for (int b = threadIdx.x; b <= d.s.n_seqs; b += 64 * WAVES) d.starts[b] = starts[b];
     const int U = __builtin_amdgcn_readfirstlane(starts[d.s.n_seqs]), W = runs_of(d.workers, U);
     if (run >= W) return false;
     u = first_unit(run, W, U);
@@ -697,17 +696,17 @@ __device__ __forceinline__ AttnSide side_of(const AttnArgs &a)
 // Each wave takes 32 tokens of every 128 for all of the tile's rows, straight from memory into
 // its products: no barrier but at an item's end.
 template <typename T, int NB, int D, int G, int RT>
-__global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
 {
     constexpr int kRows = 16 * RT;
     extern __shared__ int32_t shared[];
     AttnSide d = side_of(a);
     int32_t *starts = shared;                                       // [n_seqs + 1]
-    int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [kWaves]
-    float *ml = reinterpret_cast<float *>(scan + 4);
+    int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [8]
+    float *ml = reinterpret_cast<float *>(scan + 8);
     float *part = ml + kWaves * kRows * 2;
     int h, run, u, u_end;
-    if (!take_run<kRows>(a, d, starts, scan, h, run, u, u_end)) return;
+    if (!take_run<kRows, kWaves>(a, d, starts, scan, h, run, u, u_end)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
@@ -785,16 +784,18 @@ __global__ __launch_bounds__(kAttnThreads, RT *D <= 128 ? 3 : 2) void attn_kerne
             load_values(next);
             __builtin_amdgcn_sched_barrier(0);
         }
-        finish<T, D, G, RT, kWaves>(w, a, d, x, h, run, ml, part);
+        finish<T, D, G, RT, kWaves, kWaves>(w, a, d, x, h, run, ml, part);
     }
 }
 
 // ---- many rows: the arithmetic bounds it ------------------------------------------------------
-// TW waves share each 16 * RT rows and take turns at tiles of 32 tokens; all waves of the block
-// meet the same 64 tokens a step. A quarter each, they widen the step's codes into fragments
-// and open its grids, in LDS: that is paid once for the block's rows. Where LDS has room for
-// two steps (heads of up to 128), the next step's are made in the other half, so that one
-// barrier a step is enough; the codes of the step after that are on their way meanwhile.
+// TW waves share each 16 rows and take turns at tiles of 32 tokens; all waves of the block meet
+// the same 64 tokens a step. Together they widen the step's codes into fragments and open its
+// grids, in LDS: that is paid once for the block's rows. Where LDS has room for two steps
+// (heads of up to 128), the next step's are made in the other half, so that one barrier a step
+// is enough; the codes of the step after that are on their way meanwhile. Eight waves of 16
+// rows rather than four of 32: four waves to a SIMD hide each other's waits better than two
+// that share a broadcast grid between twice the rows.
 constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;
 
 template <int D, int G>
@@ -807,50 +808,54 @@ struct WideStep {
 };
 template <int D>
 constexpr int wide_buffers() { return D <= 128 ? 2 : 1; }
+template <int D>
+constexpr int wide_waves() { return D <= 128 ? 8 : 4; }
 template <int D, int G>
 constexpr size_t wide_bytes()       // of the steps, or of what joins the waves in their place
 {
     const size_t steps = wide_buffers<D>() * sizeof(WideStep<D, G>);
-    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
-    return (steps > part ? steps : part) + 15 & ~size_t(15);
+    const size_t part = 4 * (size_t)wide_waves<D>() * 16 * (part_dims(D) + kPartPad);
+    return ((steps > part ? steps : part) + 15) & ~size_t(15);
 }
 
-template <typename T, int NB, int D, int G, int RT, int TW>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
+template <typename T, int NB, int D, int G, int TW>
+__global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_wide_kernel(AttnArgs a)
 {
-    constexpr int kRows = 16 * RT * (kWaves / TW), kTurns = 2 / TW, kBuffers = wide_buffers<D>();
-    constexpr int kRegs = Places<D, G>::kRegs;
-    static_assert(kWaves == kWideTiles, "a wave widens 16 tokens");
+    constexpr int kWide = wide_waves<D>(), kRows = 16 * (kWide / TW), kTurns = 2 / TW, kBuffers = wide_buffers<D>();
+    constexpr int kRegs = Places<D, G>::kRegs, kParts = kWide / kWideTiles;
+    static_assert(kParts == 1 || kParts == 2, "a wave widens 16 tokens, or half their dimensions");
     extern __shared__ u32x4 shared4[];
     AttnSide d = side_of(a);
     WideStep<D, G> *steps = reinterpret_cast<WideStep<D, G> *>(shared4);
     float *part = reinterpret_cast<float *>(shared4);
     float *ml = reinterpret_cast<float *>(shared4 + wide_bytes<D, G>() / 16);
-    int32_t *starts = reinterpret_cast<int32_t *>(ml + kWaves * 16 * RT * 2);
+    int32_t *starts = reinterpret_cast<int32_t *>(ml + kWide * 16 * 2);
     int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
     int h, run, u, u_end;
-    if (!take_run<kRows>(a, d, starts, scan, h, run, u, u_end)) return;
+    if (!take_run<kRows, kWide>(a, d, starts, scan, h, run, u, u_end)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int sub = wave % kWideTiles, piece = wave / kWideTiles;       // what this wave widens
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
 
     while (u < u_end) {
         const Item x = item_at<kRows>(d, starts, a.per, u, u_end);
         u += x.count;
-        Wave<D, G, RT> w;
-        begin<T>(w, a, d.causal, x, h, x.row0 + wave / TW * 16 * RT);
+        Wave<D, G, 1> w;
+        begin<T>(w, a, d.causal, x, h, x.row0 + wave / TW * 16);
         // what the block's rows see: the same for its waves, which go in step
         const int last = (min(x.row0 + kRows, x.n_rows) - 1) / a.per;
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
-        uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4], vw[Spot<NB, D, G>::kValBytes], kg[kRegs], vg[kRegs];
+        uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4 / kParts], vw[Spot<NB, D, G>::kValBytes], kg[kRegs], vg[kRegs];
         int good;
         // this wave's 16 tokens of a step, at positions from t
-        auto page_of_step = [&](int t0) { return page_at(d.s, table, min(t0 + 16 * wave, x.len - 1)); };
+        auto page_of_step = [&](int t0) { return page_at(d.s, table, min(t0 + 16 * sub, x.len - 1)); };
         auto fetch = [&](int t, int page) {
             const int64_t at = spot.first(a, d.s, h, page, t);
-            spot.keys(a, at, kw);
+            load_words<Spot<NB, D, G>::kKeyBytes / kParts>(uniform(a.c.k_codes + at * spot.kRow),
+                                                           spot.key_at + piece * (spot.kKeyBytes / kParts), kw);
             spot.values(a, at, vw);
             spot.grids(a.c.k_meta, at, kg);
             spot.grids(a.c.v_meta, at, vg);
@@ -858,29 +863,33 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
         };
         auto widen = [&](WideStep<D, G> &to) {
 #pragma unroll
-            for (int mm = 0; mm < D / 32; ++mm) to.key[wave][mm][lane] = key_frag<Types<T>::kBf16, NB>(kw + mm * (NB / 4));
+            for (int mm = 0; mm < D / 32 / kParts; ++mm)
+                to.key[sub][piece * (D / 32 / kParts) + mm][lane] = key_frag<Types<T>::kBf16, NB>(kw + mm * (NB / 4));
+            static_for<kParts>([&](auto p) {
+                if (piece != p.value) return;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                const u32x2 f = {value_reg<NB, D>(vw, 0, j, masks), value_reg<NB, D>(vw, 1, j, masks)};
-                reinterpret_cast<u32x2 *>(&to.value[wave / 2][j][lane])[wave % 2] = f;
-            }
+                for (int j = p.value * (D / 16 / kParts); j < (p.value + 1) * (D / 16 / kParts); ++j) {
+                    const u32x2 f = {value_reg<NB, D>(vw, 0, j, masks), value_reg<NB, D>(vw, 1, j, masks)};
+                    reinterpret_cast<u32x2 *>(&to.value[sub / 2][j][lane])[sub % 2] = f;
+                }
+            });
 #pragma unroll
             for (int k = 0; k < kRegs; ++k) {
                 const bool in = Places<D, G>::token(k) < good;
-                to.key_grid[wave][k][lane] = open_key_grid<T>(in ? kg[k] : 0u, a.scale);
-                to.value_grid[wave][k][lane] = open_value_grid<T, NB>(in ? vg[k] : 0u);
+                if (piece == 0) to.key_grid[sub][k][lane] = open_key_grid<T>(in ? kg[k] : 0u, a.scale);
+                if (piece == kParts - 1) to.value_grid[sub][k][lane] = open_value_grid<T, NB>(in ? vg[k] : 0u);
             }
-            if (lane == 0) to.good[wave] = good;
+            if (lane == 0 && piece == 0) to.good[sub] = good;
         };
         int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end), page = 0, buffer = 0;
         // a step that there is not is fetched like the last one, and not used
         auto within = [&](int t) { return t < t_end ? t : t0; };
         if (t0 < t_end) {
-            fetch(t0 + 16 * wave, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
+            fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
             if constexpr (kBuffers == 2) {
                 widen(steps[0]);
                 const int next = within(t0 + kWideStep);
-                fetch(next + 16 * wave, __builtin_amdgcn_readfirstlane(page_of_step(next)));
+                fetch(next + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(next)));
                 page = page_of_step(within(t0 + 2 * kWideStep));
             } else {
                 page = page_of_step(within(t0 + kWideStep));
@@ -896,7 +905,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
                 __syncthreads();
             }
             const int next = within(t0 + kAhead * kWideStep);
-            fetch(next + 16 * wave, __builtin_amdgcn_readfirstlane(page));
+            fetch(next + 16 * sub, __builtin_amdgcn_readfirstlane(page));
             page = page_of_step(within(t0 + (kAhead + 1) * kWideStep));
             __builtin_amdgcn_sched_barrier(0);
             const WideStep<D, G> &now = steps[buffer];
@@ -915,22 +924,37 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_wide_kernel(AttnArgs a)
             if constexpr (kBuffers == 2) buffer ^= 1;
         }
         __syncthreads();                        // `part` lies over the steps
-        finish<T, D, G, RT, TW>(w, a, d, x, h, run, ml, part);
+        finish<T, D, G, 1, TW, kWide>(w, a, d, x, h, run, ml, part);
     }
 }
 
-template <typename T, int NB, int D, int G, int RT, int TW>
-hipError_t launch_one(const AttnArgs &a, hipStream_t stream)
+// Bytes of LDS beside what the waves work in: the units before each sequence's and their scan,
+// at most 16 KB.
+inline size_t starts_bytes(const AttnArgs &a)
 {
-    // for few rows at most 16 KB of starts, 1 KB and 33 KB; for many 16 KB, 1 KB and 72 KB
     const int n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
-    const size_t part = 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
-    const size_t lds = 4 * (((size_t)n + 4) & ~size_t(3)) + 16 + 4 * kWaves * 16 * RT * 2 +
-                       (TW == kWaves ? part : wide_bytes<D, G>());
+    return 4 * (((size_t)n + 4) & ~size_t(3)) + 4 * 8;
+}
+inline dim3 grid_of(const AttnArgs &a)
+{
     const int64_t runs = a.side[0].workers + (a.sides == 2 ? a.side[1].workers : 0);
-    const dim3 grid((unsigned)(runs * a.c.heads));
-    if constexpr (TW == kWaves) attn_kernel<T, NB, D, G, RT><<<grid, kAttnThreads, lds, stream>>>(a);
-    else attn_wide_kernel<T, NB, D, G, RT, TW><<<grid, kAttnThreads, lds, stream>>>(a);
+    return dim3((unsigned)(runs * a.c.heads));
+}
+
+template <typename T, int NB, int D, int G, int RT>
+hipError_t launch_few(const AttnArgs &a, hipStream_t stream)
+{
+    const size_t lds = starts_bytes(a) + 4 * kWaves * 16 * RT * 2 + 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
+    attn_kernel<T, NB, D, G, RT><<<grid_of(a), 64 * kWaves, lds, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, int NB, int D, int G, int TW>
+hipError_t launch_many(const AttnArgs &a, hipStream_t stream)
+{
+    const int waves = wide_waves<D>();
+    const size_t lds = wide_bytes<D, G>() + 4 * waves * 16 * 2 + starts_bytes(a);
+    attn_wide_kernel<T, NB, D, G, TW><<<grid_of(a), 64 * waves, lds, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -939,14 +963,14 @@ hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
     // rows to a tile: 16 to 128, or to 64 for 256-wide heads (whose sums fill the registers)
     const int n = a.side[0].tiles16;
-    if (n == 1) return launch_one<T, NB, D, G, 1, 4>(a, stream);
+    if (n == 1) return launch_few<T, NB, D, G, 1>(a, stream);
     if constexpr (D <= 128) {
-        if (n == 2) return launch_one<T, NB, D, G, 2, 4>(a, stream);
-        if (n == 4) return launch_one<T, NB, D, G, 2, 2>(a, stream);
-        if (n == 8) return launch_one<T, NB, D, G, 2, 1>(a, stream);
+        if (n == 2) return launch_few<T, NB, D, G, 2>(a, stream);
+        if (n == 4) return launch_many<T, NB, D, G, 2>(a, stream);
+        if (n == 8) return launch_many<T, NB, D, G, 1>(a, stream);
     } else {
-        if (n == 2) return launch_one<T, NB, D, G, 1, 2>(a, stream);
-        if (n == 4) return launch_one<T, NB, D, G, 1, 1>(a, stream);
+        if (n == 2) return launch_many<T, NB, D, G, 2>(a, stream);
+        if (n == 4) return launch_many<T, NB, D, G, 1>(a, stream);
     }
     return hipErrorInvalidValue;
 }
