@@ -211,46 +211,17 @@ __device__ __forceinline__ float column_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// The units before each sequence's, in LDS: starts[n_seqs] is their sum.
-template <int ROWS, int WAVES>
-__device__ void lay_out(const AttnSide &d, int per, int32_t *starts, int32_t *scan)
+// Inclusive sum over the lanes of a wave: within rows of 16, then from row to row.
+__device__ __forceinline__ int wave_sum(int x)
 {
-    const int t = threadIdx.x, n = d.s.n_seqs;
-    const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Rows r = rows_of(d.s, b);
-        const int u = tiles_of((r.end - r.begin) * per, ROWS) * units_along(len_of(d.s, b), d.unit);
-        starts[b] = u;
-        sum += u;
-    }
-    // exclusive sums over the threads: within the waves, then over them
-    int run = sum;
-    for (int x = 1; x < 64; x <<= 1) {
-        const int y = __shfl_up(run, x);
-        if ((t & 63) >= x) run += y;
-    }
-    if ((t & 63) == 63) scan[t >> 6] = run;
-    __syncthreads();
-    int before = run - sum, total = 0;
-    for (int w = 0; w < WAVES; ++w) {
-        if (w < (t >> 6)) before += scan[w];
-        total += scan[w];
-    }
-    for (int b = b0; b < b1; ++b) {
-        const int u = starts[b];
-        starts[b] = before;
-        before += u;
-    }
-    if (t == 0) starts[n] = total;
-    __syncthreads();
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);     // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);     // lane 15 of a row to the next one
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
+    return x;
 }
-
-// How far a score may lie above the maximum that weights are taken from: weights reach 2^6.
-constexpr float kSlack = 6.f;
-// V's steps are scaled to below 2^9 (by a power of two that follows the largest seen), so that
-// weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
-constexpr int kStepBits = 8;
 
 // A run's next item, or the part of it that the run has.
 struct Item {
@@ -260,25 +231,117 @@ struct Item {
     int row0;                   // the item's first
     int along, u_in, count;     // units of the item, the first of this part, how many
 };
-template <int ROWS>
-__device__ __forceinline__ Item item_at(const AttnSide &d, const int32_t *starts, int per, int u, int u_end)
-{
-    Item x;
-    x.b = 0;
-    for (int hi = d.s.n_seqs; hi - x.b > 1;) {
-        const int mid = (x.b + hi) >> 1;
-        if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) x.b = mid; else hi = mid;
+
+// The units of a side, end to end. Up to 64 sequences each wave has them in its lanes, and
+// nothing waits for another; more are summed up in LDS.
+template <int ROWS, int WAVES>
+struct Layout {
+    const AttnSide &d;
+    int per, total;
+    int start;                  // of sequence `lane` and its rows and length, with up to 64
+    Rows rows;
+    int len;
+    int32_t *starts;            // [n_seqs + 1] in LDS, with more
+    __device__ __forceinline__ bool few() const { return d.s.n_seqs <= 64; }
+    __device__ __forceinline__ int units(const Rows &r, int len) const
+    {
+        return tiles_of((r.end - r.begin) * per, ROWS) * units_along(len, d.unit);
     }
-    x.rows = rows_of(d.s, x.b);
-    x.len = len_of(d.s, x.b);
-    x.n_rows = (x.rows.end - x.rows.begin) * per;
-    x.along = units_along(x.len, d.unit);
-    const int in_seq = u - __builtin_amdgcn_readfirstlane(starts[x.b]);
-    x.row0 = in_seq / x.along * ROWS;
-    x.u_in = in_seq % x.along;
-    x.count = min(u_end - u, x.along - x.u_in);
-    return x;
-}
+
+    // scan: [WAVES] in LDS
+    __device__ __forceinline__ Layout(const AttnSide &side, int per, int32_t *starts, int32_t *scan)
+        : d(side), per(per), start(0), rows{0, 0}, len(0), starts(starts)
+    {
+        const int t = threadIdx.x, n = d.s.n_seqs;
+        if (few()) {
+            const int lane = t & 63;
+            int u = 0;
+            if (lane < n) {
+                rows = rows_of(d.s, lane);
+                len = len_of(d.s, lane);
+                u = units(rows, len);
+            }
+            const int upto = wave_sum(u);
+            start = upto - u;
+            total = __builtin_amdgcn_readlane(upto, 63);
+            return;
+        }
+        const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int u = units(rows_of(d.s, b), len_of(d.s, b));
+            starts[b] = u;
+            sum += u;
+        }
+        const int run = wave_sum(sum);
+        if ((t & 63) == 63) scan[t >> 6] = run;
+        __syncthreads();
+        int before = run - sum;
+        total = 0;
+        for (int w = 0; w < WAVES; ++w) {
+            if (w < (t >> 6)) before += scan[w];
+            total += scan[w];
+        }
+        for (int b = b0; b < b1; ++b) {
+            const int u = starts[b];
+            starts[b] = before;
+            before += u;
+        }
+        if (t == 0) starts[n] = total;
+        __syncthreads();
+        total = __builtin_amdgcn_readfirstlane(total);
+    }
+
+    // to: [n_seqs + 1] in memory
+    __device__ __forceinline__ void put(int32_t *to) const
+    {
+        const int t = threadIdx.x, n = d.s.n_seqs;
+        if (few()) {
+            if (t < n) to[t] = start;
+            if (t == 0) to[n] = total;
+        } else {
+            for (int b = t; b <= n; b += 64 * WAVES) to[b] = starts[b];
+        }
+    }
+
+    __device__ __forceinline__ Item item(int u, int u_end) const
+    {
+        Item x;
+        int first;
+        if (few()) {
+            const bool le = (int)(threadIdx.x & 63) < d.s.n_seqs && start <= u;
+            x.b = __popcll(__ballot(le)) - 1;
+            x.rows.begin = __builtin_amdgcn_readlane(rows.begin, x.b);
+            x.rows.end = __builtin_amdgcn_readlane(rows.end, x.b);
+            x.len = __builtin_amdgcn_readlane(len, x.b);
+            first = __builtin_amdgcn_readlane(start, x.b);
+        } else {
+            x.b = 0;
+            for (int hi = d.s.n_seqs; hi - x.b > 1;) {
+                const int mid = (x.b + hi) >> 1;
+                if (__builtin_amdgcn_readfirstlane(starts[mid]) <= u) x.b = mid; else hi = mid;
+            }
+            const Rows r = rows_of(d.s, x.b);
+            x.rows.begin = __builtin_amdgcn_readfirstlane(r.begin);
+            x.rows.end = __builtin_amdgcn_readfirstlane(r.end);
+            x.len = __builtin_amdgcn_readfirstlane(len_of(d.s, x.b));
+            first = __builtin_amdgcn_readfirstlane(starts[x.b]);
+        }
+        x.n_rows = (x.rows.end - x.rows.begin) * per;
+        x.along = units_along(x.len, d.unit);
+        const unsigned in_seq = u - first, tile = in_seq / (unsigned)x.along;
+        x.row0 = (int)tile * ROWS;
+        x.u_in = (int)(in_seq - tile * x.along);
+        x.count = min(u_end - u, x.along - x.u_in);
+        return x;
+    }
+};
+
+// How far a score may lie above the maximum that weights are taken from: weights reach 2^6.
+constexpr float kSlack = 6.f;
+// V's steps are scaled to below 2^9 (by a power of two that follows the largest seen), so that
+// weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
+constexpr int kStepBits = 8;
 
 // What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16).
 template <int D, int G, int RT>
@@ -299,29 +362,36 @@ template <typename T, int D, int G, int RT>
 __device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
 {
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
-    w.lim_low = x.len;
-    w.lim_high = 0;
+    const unsigned per = a.per;
+    // what the first and the last of the wave's rows see
+    const int before = causal ? x.len - (x.rows.end - x.rows.begin) + 1 : x.len;
+    const int last = min(row0 + 16 * RT, x.n_rows) - 1;
+    w.lim_low = row0 <= last ? before + (causal ? (int)((unsigned)row0 / per) : 0) : 0;
+    w.lim_high = row0 <= last ? before + (causal ? (int)((unsigned)last / per) : 0) : 0;
+    uint4 raw[RT][D / 32];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int row = row0 + 16 * t + col;
         const bool have = row < x.n_rows;
-        const int tok = have ? row / a.per : 0, hq = h * a.per + (have ? row % a.per : 0);
-        const uint16_t *q = a.q + (x.rows.begin + tok) * a.q_ts + hq * a.q_hs;
-        w.lim[t] = !have ? 0 : causal ? x.len - (x.rows.end - x.rows.begin) + tok + 1 : x.len;
-        if (have) {
-            w.lim_low = min(w.lim_low, w.lim[t]);
-            w.lim_high = max(w.lim_high, w.lim[t]);
+        const int tok = have ? (int)((unsigned)row / per) : 0, hq = h * a.per + (have ? row - tok * a.per : 0);
+        const uint16_t *q = a.q + (x.rows.begin + tok) * a.q_ts + hq * a.q_hs + 8 * quad;
+        w.lim[t] = !have ? 0 : before + (causal ? tok : 0);
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+            raw[t][m] = uint4{0, 0, 0, 0};
+            if (have) raw[t][m] = *reinterpret_cast<const uint4 *>(q + 32 * m);
         }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
 #pragma unroll
         for (int g = 0; g < D / G; ++g) {
             float sum = 0.f;
 #pragma unroll
             for (int m = g * G / 32; m < (g + 1) * G / 32; ++m) {
-                uint4 raw = {0, 0, 0, 0};
-                if (have) raw = *reinterpret_cast<const uint4 *>(q + 32 * m + 8 * quad);
-                w.qf[t][m] = u32x4{raw.x, raw.y, raw.z, raw.w};
+                w.qf[t][m] = u32x4{raw[t][m].x, raw[t][m].y, raw[t][m].z, raw[t][m].w};
                 float v[8];
-                unpack8<T>(raw, v);
+                unpack8<T>(raw[t][m], v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum += v[e];
             }
@@ -334,13 +404,6 @@ __device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool
         w.above[t] = -INFINITY;
         w.l[t] = 0.f;
     }
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) {
-        w.lim_low = min(w.lim_low, __shfl_xor(w.lim_low, x));
-        w.lim_high = max(w.lim_high, __shfl_xor(w.lim_high, x));
-    }
-    w.lim_low = __builtin_amdgcn_readfirstlane(w.lim_low);
-    w.lim_high = __builtin_amdgcn_readfirstlane(w.lim_high);
     w.step_lim = w.step_by = 0.f;
 }
 
@@ -668,28 +731,19 @@ __device__ __forceinline__ Masks make_masks()
     return m;
 }
 
-// Which side and run a block has; the units laid out in LDS. False if it has nothing to do.
-template <int ROWS, int WAVES>
-__device__ __forceinline__ bool take_run(const AttnArgs &a, AttnSide &d, int32_t *starts, int32_t *scan, int &h, int &run,
-                                         int &u, int &u_end)
+// The side of the call that the block works on, its head and run.
+struct Place {
+    AttnSide d;
+    int h, run;
+    bool first;                 // of the side's blocks
+};
+__device__ __forceinline__ Place place_of(const AttnArgs &a)
 {
     const unsigned blocks0 = (unsigned)a.side[0].workers * a.c.heads;
-    unsigned block = blockIdx.x;
-    if (block >= blocks0) block -= blocks0;
-    lay_out<ROWS, WAVES>(d, a.per, starts, scan);
-    h = (int)(block % (unsigned)a.c.heads);
-    run = (int)(block / (unsigned)a.c.heads);
-    if (block == 0 && d.starts)
-        for (int b = threadIdx.x; b <= d.s.n_seqs; b += 64 * WAVES) d.starts[b] = starts[b];
-    const int U = __builtin_amdgcn_readfirstlane(starts[d.s.n_seqs]), W = runs_of(d.workers, U);
-    if (run >= W) return false;
-    u = first_unit(run, W, U);
-    u_end = first_unit(run + 1, W, U);
-    return true;
-}
-__device__ __forceinline__ AttnSide side_of(const AttnArgs &a)
-{
-    return blockIdx.x < (unsigned)a.side[0].workers * a.c.heads ? a.side[0] : a.side[1];
+    const bool second = blockIdx.x >= blocks0;
+    const unsigned block = second ? blockIdx.x - blocks0 : blockIdx.x;
+    const unsigned run = block / (unsigned)a.c.heads;
+    return Place{second ? a.side[1] : a.side[0], (int)(block - run * a.c.heads), (int)run, block == 0};
 }
 
 // ---- few rows: the cache is read, and little else ------------------------------------------
@@ -700,23 +754,30 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel
 {
     constexpr int kRows = 16 * RT;
     extern __shared__ int32_t shared[];
-    AttnSide d = side_of(a);
+    const Place place = place_of(a);
+    const AttnSide &d = place.d;
+    const int h = place.h;
     int32_t *starts = shared;                                       // [n_seqs + 1]
     int32_t *scan = shared + (((unsigned)d.s.n_seqs + 4) & ~3u);    // [8]
     float *ml = reinterpret_cast<float *>(scan + 8);
     float *part = ml + kWaves * kRows * 2;
-    int h, run, u, u_end;
-    if (!take_run<kRows, kWaves>(a, d, starts, scan, h, run, u, u_end)) return;
+    const Layout<kRows, kWaves> layout(d, a.per, starts, scan);
+    if (place.first && d.starts) layout.put(d.starts);
+    const int W = runs_of(d.workers, layout.total);
+    if (place.run >= W) return;
+    const int u_end = first_unit(place.run + 1, W, layout.total);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
 
-    while (u < u_end) {
-        const Item x = item_at<kRows>(d, starts, a.per, u, u_end);
+    for (int u = first_unit(place.run, W, layout.total); u < u_end;) {
+        const Item x = layout.item(u, u_end);
         u += x.count;
         Wave<D, G, RT> w;
-        begin<T>(w, a, d.causal, x, h, x.row0);
-        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)w.lim_high);
+        // what the last of the item's rows sees
+        const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
+        const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
+        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[2][Spot<NB, D, G>::kKeyBytes / 4], vw[2][Spot<NB, D, G>::kValBytes];
         uint32_t kg[2][Places<D, G>::kRegs], vg[2][Places<D, G>::kRegs];
@@ -747,6 +808,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel
             load_keys(t0);
             load_values(t0);
         }
+        begin<T>(w, a, d.causal, x, h, x.row0);     // the queries, while the first codes are on their way
         for (; t0 < t_end; t0 += kStep) {
             // The next step's keys are asked for as soon as this one's are in the products,
             // its values once this one's are: both are under way during half a step, with no
@@ -784,7 +846,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel
             load_values(next);
             __builtin_amdgcn_sched_barrier(0);
         }
-        finish<T, D, G, RT, kWaves, kWaves>(w, a, d, x, h, run, ml, part);
+        finish<T, D, G, RT, kWaves, kWaves>(w, a, d, x, h, place.run, ml, part);
     }
 }
 
@@ -825,26 +887,30 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
     constexpr int kRegs = Places<D, G>::kRegs, kParts = kWide / kWideTiles;
     static_assert(kParts == 1 || kParts == 2, "a wave widens 16 tokens, or half their dimensions");
     extern __shared__ u32x4 shared4[];
-    AttnSide d = side_of(a);
+    const Place place = place_of(a);
+    const AttnSide &d = place.d;
+    const int h = place.h;
     WideStep<D, G> *steps = reinterpret_cast<WideStep<D, G> *>(shared4);
     float *part = reinterpret_cast<float *>(shared4);
     float *ml = reinterpret_cast<float *>(shared4 + wide_bytes<D, G>() / 16);
     int32_t *starts = reinterpret_cast<int32_t *>(ml + kWide * 16 * 2);
     int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
-    int h, run, u, u_end;
-    if (!take_run<kRows, kWide>(a, d, starts, scan, h, run, u, u_end)) return;
+    const Layout<kRows, kWide> layout(d, a.per, starts, scan);
+    if (place.first && d.starts) layout.put(d.starts);
+    const int W = runs_of(d.workers, layout.total);
+    if (place.run >= W) return;
+    const int u_end = first_unit(place.run + 1, W, layout.total);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int sub = wave % kWideTiles, piece = wave / kWideTiles;       // what this wave widens
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
 
-    while (u < u_end) {
-        const Item x = item_at<kRows>(d, starts, a.per, u, u_end);
+    for (int u = first_unit(place.run, W, layout.total); u < u_end;) {
+        const Item x = layout.item(u, u_end);
         u += x.count;
         Wave<D, G, 1> w;
-        begin<T>(w, a, d.causal, x, h, x.row0 + wave / TW * 16);
         // what the block's rows see: the same for its waves, which go in step
-        const int last = (min(x.row0 + kRows, x.n_rows) - 1) / a.per;
+        const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
@@ -884,8 +950,9 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
         int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end), page = 0, buffer = 0;
         // a step that there is not is fetched like the last one, and not used
         auto within = [&](int t) { return t < t_end ? t : t0; };
+        if (t0 < t_end) fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
+        begin<T>(w, a, d.causal, x, h, x.row0 + wave / TW * 16);        // while the first codes are on their way
         if (t0 < t_end) {
-            fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
             if constexpr (kBuffers == 2) {
                 widen(steps[0]);
                 const int next = within(t0 + kWideStep);
@@ -924,7 +991,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
             if constexpr (kBuffers == 2) buffer ^= 1;
         }
         __syncthreads();                        // `part` lies over the steps
-        finish<T, D, G, 1, TW, kWide>(w, a, d, x, h, run, ml, part);
+        finish<T, D, G, 1, TW, kWide>(w, a, d, x, h, place.run, ml, part);
     }
 }
 

@@ -102,22 +102,30 @@ constexpr int kStep = 128;      // tokens of a block's step; a unit is a multipl
 
 HQQ_HD int32_t units_along(int32_t len, int32_t unit)
 {
-    return len <= unit ? 1 : (int32_t)(((int64_t)len + unit - 1) / unit);
+    return len <= unit ? 1 : (int32_t)(((uint32_t)len + (uint32_t)unit - 1) / (uint32_t)unit);
 }
 
 HQQ_HD int32_t tiles_of(int32_t rows, int32_t rows_per)
 {
-    return (int32_t)(((int64_t)rows + rows_per - 1) / rows_per);
+    return (int32_t)(((uint32_t)rows + (uint32_t)rows_per - 1) / (uint32_t)rows_per);
 }
 
 HQQ_HD int32_t runs_of(int32_t workers, int32_t units) { return workers < units ? workers : units; }
 
-// First unit of run w of W over U units; run that has unit u. 1 <= W <= U: no run is empty.
-HQQ_HD int32_t first_unit(int32_t w, int32_t W, int32_t U) { return (int32_t)((int64_t)w * U / W); }
+// First unit of run w of W over U units; run that has unit u. 1 <= W <= U: no run is empty,
+// the first U % W have one unit more than the others.
+HQQ_HD int32_t first_unit(int32_t w, int32_t W, int32_t U)
+{
+    const int32_t each = (int32_t)((uint32_t)U / (uint32_t)W), more = U - each * W;
+    return w * each + (w < more ? w : more);
+}
 
 HQQ_HD int32_t run_of(int32_t u, int32_t W, int32_t U)
 {
-    return (int32_t)((((int64_t)u + 1) * W - 1) / U);
+    const int32_t each = (int32_t)((uint32_t)U / (uint32_t)W), more = U - each * W;
+    const int32_t longer = more * (each + 1);   // units of the longer runs; at most U
+    return u < longer ? (int32_t)((uint32_t)u / (uint32_t)(each + 1))
+                      : more + (int32_t)((uint32_t)(u - longer) / (uint32_t)each);
 }
 
 }  // namespace hqq
