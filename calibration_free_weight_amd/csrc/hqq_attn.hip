@@ -8,6 +8,10 @@ namespace {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWaves = kJoinThreads / 64;
 constexpr int kAhead = 8;       // pieces asked for at a time
+// From here on a block for each split item takes less time than a wave for each row, most of
+// which are of whole items.
+constexpr int64_t kManyRows = 2048;
+constexpr int kJoinRows = 16;   // of an item, to a block
 
 template <int E>
 struct Acc {                    // a row's result so far; a lane holds E dimensions
@@ -123,12 +127,62 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
         a.lse[x] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Many rows and one side: a block for each place where a run ends within an item, and head. The
+// item is joined where its first run ends; other blocks have nothing to do.
+template <typename T, int D>
+__global__ __launch_bounds__(kJoinThreads) void join_items_kernel(JoinArgs a)
+{
+    constexpr int kLanes = D / 4;                   // of a row, four dimensions each
+    const AttnSide &d = a.side[0];
+    const int w = (int)(blockIdx.x / (unsigned)a.heads) + 1, h = (int)(blockIdx.x % (unsigned)a.heads);
+    const int r0 = (int)blockIdx.y * kJoinRows;     // of the item, the block's rows
+    const int U = d.starts[d.s.n_seqs], W = runs_of(d.workers, U), per = 16 * d.tiles16;
+    if (w >= W) return;
+    const int u = first_unit(w, W, U);
+    SeqView by_unit = d.s;                          // the sequence of unit u, by the same search
+    by_unit.cu = d.starts;
+    const int b = __builtin_amdgcn_readfirstlane(find_seq(by_unit, u));
+    const Rows rows = rows_of(d.s, b);
+    const int along = units_along(len_of(d.s, b), d.unit), in_seq = u - d.starts[b];
+    const int tile = in_seq / along, u0 = u - in_seq % along;
+    if (u0 == u || run_of(u0, W, U) != w - 1) return;
+    const int w1 = run_of(u0 + along - 1, W, U), row0 = tile * per;
+    const int n_rows = min(min(per, r0 + kJoinRows), (rows.end - rows.begin) * a.per - row0);
+    // slot 2w + 1 of the first run, 2w of the others
+    const auto at = [&](int v, int r) { return ((int64_t)h * 2 * d.workers + 2 * v + (v == w - 1)) * per + r; };
+    for (int r = r0 + threadIdx.x / kLanes; r < n_rows; r += kJoinThreads / kLanes) {
+        const int e0 = threadIdx.x % kLanes * 4;
+        float m = -INFINITY, l = 0.f;
+        Floats<4> o = {};
+        for (int v = w - 1; v <= w1; ++v) {
+            const Floats<2> ml = *reinterpret_cast<const Floats<2> *>(d.slot_ml + at(v, r) * 2);
+            const Floats<4> x = *reinterpret_cast<const Floats<4> *>(d.slot_o + at(v, r) * D + e0);
+            const float top = fmaxf(m, ml.x[0]);
+            const float f = m == top ? 1.f : exp2f(m - top), g = ml.x[0] == -INFINITY ? 0.f : exp2f(ml.x[0] - top);
+            l = fmaf(g, ml.x[1], l * f);
+            m = top;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o.x[e] = fmaf(g, x.x[e], o.x[e] * f);
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int tok = rows.begin + (row0 + r) / a.per, hq = h * a.per + (row0 + r) % a.per;
+        const uint2 packed = {from_f32<T>(o.x[0] * inv) | from_f32<T>(o.x[1] * inv) << 16,
+                              from_f32<T>(o.x[2] * inv) | from_f32<T>(o.x[3] * inv) << 16};
+        *reinterpret_cast<uint2 *>(a.out + tok * a.o_ts + hq * a.o_hs + e0) = packed;
+        if (a.lse && e0 == 0)
+            a.lse[(int64_t)tok * a.heads * a.per + hq] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
 template <typename T, int D>
 void join_rows(const JoinArgs &a, hipStream_t stream)
 {
     // few rows have many pieces each: a block for each row
     const int64_t rows = (int64_t)a.side[0].s.n_tokens * a.heads * a.per;
-    if (rows <= 1024)
+    if (a.sides == 1 && rows > kManyRows) {
+        const int ends = a.side[0].workers - 1;
+        if (ends > 0) join_items_kernel<T, D><<<dim3((unsigned)(ends * a.heads), (unsigned)((16 * a.side[0].tiles16 + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, stream>>>(a);
+    } else if (rows <= 1024)
         join_kernel<T, D, kJoinWaves><<<dim3((unsigned)rows), kJoinThreads, 0, stream>>>(a);
     else
         join_kernel<T, D, 1><<<dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), kJoinThreads, 0, stream>>>(a);

@@ -254,16 +254,7 @@ struct Layout {
     {
         const int t = threadIdx.x, n = d.s.n_seqs;
         if (few()) {
-            const int lane = t & 63;
-            int u = 0;
-            if (lane < n) {
-                rows = rows_of(d.s, lane);
-                len = len_of(d.s, lane);
-                u = units(rows, len);
-            }
-            const int upto = wave_sum(u);
-            start = upto - u;
-            total = __builtin_amdgcn_readlane(upto, 63);
+            read();
             return;
         }
         const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
@@ -290,6 +281,25 @@ struct Layout {
         if (t == 0) starts[n] = total;
         __syncthreads();
         total = __builtin_amdgcn_readfirstlane(total);
+    }
+
+    __device__ __forceinline__ void read()
+    {
+        const int lane = threadIdx.x & 63;
+        int u = 0;
+        if (lane < d.s.n_seqs) {
+            rows = rows_of(d.s, lane);
+            len = len_of(d.s, lane);
+            u = units(rows, len);
+        }
+        const int upto = wave_sum(u);
+        start = upto - u;
+        total = __builtin_amdgcn_readlane(upto, 63);
+    }
+    // Before a further item: what the lanes had is read again rather than kept in registers.
+    __device__ __forceinline__ void again()
+    {
+        if (few()) read();
     }
 
     // to: [n_seqs + 1] in memory
@@ -343,8 +353,9 @@ constexpr float kSlack = 6.f;
 // weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
 constexpr int kStepBits = 8;
 
-// What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16).
-template <int D, int G, int RT>
+// What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16). BASE_FRAGS: the
+// bases' part of the scores is a product too, see base_query.
+template <int D, int G, int RT, bool BASE_FRAGS>
 struct Wave {
     static constexpr int kGroups = D / G;
     u32x4 qf[RT][D / 32];       // queries, as B fragments
@@ -352,16 +363,44 @@ struct Wave {
     int lim[RT];                // what a row sees ends here
     int lim_low, lim_high;      // for all rows, for any
     f32x4 o[RT][D / 16];
+    u32x4 qb[BASE_FRAGS ? RT : 1];      // the sums as a B fragment
     // m: scores are taken from it; above: how far one may lie above before m moves (none
     // while m has not been set)
     float m[RT], above[RT], l[RT], bsum[RT][kGroups];
     float step_lim, step_by;    // V's steps are below step_lim and multiplied by step_by
 };
 
-template <typename T, int D, int G, int RT>
-__device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
+// The bases' part of the scores as one product of bfloat16 parts, exact but for the last:
+// slot e of the contraction's quad 0, 1 and 2 has the base of group e (its first part) and the
+// first, second and third part of the column's sum over that group, of quad 3 the second part
+// of the base (none of a bfloat16 one) and the first of the sum. What is left out is below
+// 2^-16 of the largest.
+template <int GROUPS>
+__device__ __forceinline__ u32x4 base_query(const float (&sum)[GROUPS], int quad)
 {
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+    static_assert(GROUPS <= 8, "a slot for each group");
+    uint32_t bits[8] = {};
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        float x = sum[g];
+        const uint32_t first = from_f32<Bf16>(x);
+        x -= to_f32<Bf16>(first);
+        const uint32_t second = from_f32<Bf16>(x);
+        x -= to_f32<Bf16>(second);
+        bits[g] = quad == 1 ? second : quad == 2 ? from_f32<Bf16>(x) : first;
+    }
+    u32x4 f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = bits[2 * e] | bits[2 * e + 1] << 16;
+    return f;
+}
+
+template <typename T, int D, int G, int RT, bool BASE_FRAGS>
+__device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
+{
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int col = lane & 15, quad = lane >> 4;
     const unsigned per = a.per;
     // what the first and the last of the wave's rows see
     const int before = causal ? x.len - (x.rows.end - x.rows.begin) + 1 : x.len;
@@ -398,6 +437,7 @@ __device__ __forceinline__ void begin(Wave<D, G, RT> &w, const AttnArgs &a, bool
             w.qsum[t][g] = column_sum(sum) * a.scale;
             w.bsum[t][g] = 0.f;
         }
+        if constexpr (BASE_FRAGS) w.qb[t] = base_query<D / G>(w.qsum[t], quad);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) w.o[t][j] = f32x4{0, 0, 0, 0};
         w.m[t] = 0.f;
@@ -423,11 +463,13 @@ struct Places {
 // if negative). When some are not, or not for all rows, close() is called first, to make the
 // grids of the missing ones {0, 0}. key_grid(half, k) gives {step * scale, base} of a lane's
 // place, value_grid {step, middle}; key(half, mm) and value(j) the A fragments. after_keys() is
-// called when no more keys are needed, before the values' grids and fragments are.
-template <typename T, int D, int G, int RT, typename Close, typename KeyGrid, typename Key, typename After, typename ValueGrid,
-          typename Value>
-__device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
-                                            Key key, After after_keys, ValueGrid value_grid, Value value)
+// called when no more keys are needed, before the values' grids and fragments are. With
+// BASE_FRAGS base(half) is the A fragment of the bases (base_query has the other), and what
+// key_grid says of them is not used.
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
+          typename After, typename ValueGrid, typename Value>
+__device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
+                                            Base base, Key key, After after_keys, ValueGrid value_grid, Value value)
 {
     constexpr bool kBf16 = Types<T>::kBf16;
     constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
@@ -436,10 +478,17 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, int t0, const int
     if (!open) close();
     float s[RT][8];
     static_for<2>([&](auto half) {
-        f32x4 acc[RT][kGroups];
+        f32x4 acc[RT][kGroups], from[RT];
         f32x2 kgrid[kRegs];
 #pragma unroll
         for (int k = 0; k < kRegs; ++k) kgrid[k] = key_grid(half.value, k);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) from[t] = f32x4{-w.m[t], -w.m[t], -w.m[t], -w.m[t]};
+        if constexpr (BASE_FRAGS) {
+            const u32x4 bf = base(half.value);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) from[t] = mfma32<true>(bf, w.qb[t], from[t]);
+        }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
@@ -455,15 +504,17 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT> &w, int t0, const int
         static_for<4>([&](auto r) {
             constexpr int i = 4 * half.value + r.value;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) s[t][i] = -w.m[t];
+            for (int t = 0; t < RT; ++t) s[t][i] = from[t][r.value];
             static_for<kGroups>([&](auto g) {
                 constexpr int at = r.value * kGroups + g.value;
-                const float step = row_lane<at % 16>(kgrid[at / 16][0]), base = row_lane<at % 16>(kgrid[at / 16][1]);
+                const float step = row_lane<at % 16>(kgrid[at / 16][0]);
+                if constexpr (!BASE_FRAGS) {
+                    const float b = row_lane<at % 16>(kgrid[at / 16][1]);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    s[t][i] = fmaf(base, w.qsum[t][g.value], s[t][i]);
-                    s[t][i] = fmaf(step, acc[t][g.value][r.value], s[t][i]);
+                    for (int t = 0; t < RT; ++t) s[t][i] = fmaf(b, w.qsum[t][g.value], s[t][i]);
                 }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) s[t][i] = fmaf(step, acc[t][g.value][r.value], s[t][i]);
             });
         });
     });
@@ -584,13 +635,15 @@ constexpr int kPartPad = 4;
 // maxima, and writes it: waves TW * r .. TW * r + TW - 1 have rows 16 * RT * r .. of the item.
 // ml: [WAVES][16 * RT][2]; part: [WAVES][16][part_dims + kPartPad]. Blocks come and leave in
 // step.
-template <typename T, int D, int G, int RT, int TW, int WAVES>
-__device__ __forceinline__ void finish(Wave<D, G, RT> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
+template <typename T, int D, int G, int RT, int TW, int WAVES, bool BASE_FRAGS>
+__device__ __forceinline__ void finish(Wave<D, G, RT, BASE_FRAGS> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
                                        float *ml, float *part)
 {
     constexpr int kGroups = D / G, kPart = part_dims(D), kStride = kPart + kPartPad;
     constexpr int kRowWaves = WAVES / TW, kRows = 16 * RT * kRowWaves;
-    const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));        // its places are made here, not kept through the steps
+    const int lane = thread & 63, col = lane & 15, quad = lane >> 4, wave = thread >> 6;
     const float unstep = w.step_by > 0.f ? 1.f / w.step_by : 0.f;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -618,7 +671,7 @@ __device__ __forceinline__ void finish(Wave<D, G, RT> &w, const AttnArgs &a, con
                         part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
                             fmaf(w.o[t][g * (G / 16) + jj][i], unstep, w.bsum[t][g]);
             __syncthreads();
-            for (int y = threadIdx.x; y < kRowWaves * 16 * kPart / 4; y += 64 * WAVES) {
+            for (int y = thread; y < kRowWaves * 16 * kPart / 4; y += 64 * WAVES) {
                 const int r = y / (kPart / 4) % 16, first = y / (kPart / 4) / 16 * TW, e0 = d0 + y % (kPart / 4) * 4;
                 const int in_item = first / TW * 16 * RT + 16 * t + r, row = x.row0 + in_item;
                 if (row >= x.n_rows) break;
@@ -750,7 +803,7 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
 // Each wave takes 32 tokens of every 128 for all of the tile's rows, straight from memory into
 // its products: no barrier but at an item's end.
 template <typename T, int NB, int D, int G, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4 : 3) : 2) void attn_kernel(AttnArgs a)
 {
     constexpr int kRows = 16 * RT;
     extern __shared__ int32_t shared[];
@@ -773,7 +826,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel
     for (int u = first_unit(place.run, W, layout.total); u < u_end;) {
         const Item x = layout.item(u, u_end);
         u += x.count;
-        Wave<D, G, RT> w;
+        Wave<D, G, RT, false> w;
         // what the last of the item's rows sees
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
@@ -828,7 +881,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? 3 : 2) void attn_kernel
                         for (int k = 0; k < Places<D, G>::kRegs; ++k)
                             if (Places<D, G>::token(k) >= good[half]) kg[half][k] = vg[half][k] = 0;
                 },
-                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); },
+                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); }, [](int) { return u32x4{}; },
                 [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
                 [&] {
                     page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
@@ -864,10 +917,11 @@ template <int D, int G>
 struct WideStep {
     u32x4 key[kWideTiles][D / 32][64];          // A fragments
     u32x4 value[kWideTiles / 2][D / 16][64];
-    f32x2 key_grid[kWideTiles][Places<D, G>::kRegs][64];
+    float key_step[kWideTiles][Places<D, G>::kRegs][64];
+    uint16_t key_base[kWideTiles][2][16][D / G > 2 ? D / G : 2];    // first and second parts, of 16 tokens
     f32x2 value_grid[kWideTiles][Places<D, G>::kRegs][64];
     int good[kWideTiles];
-};
+};      // a multiple of 16 bytes
 template <int D>
 constexpr int wide_buffers() { return D <= 128 ? 2 : 1; }
 template <int D>
@@ -895,7 +949,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
     float *ml = reinterpret_cast<float *>(shared4 + wide_bytes<D, G>() / 16);
     int32_t *starts = reinterpret_cast<int32_t *>(ml + kWide * 16 * 2);
     int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
-    const Layout<kRows, kWide> layout(d, a.per, starts, scan);
+    Layout<kRows, kWide> layout(d, a.per, starts, scan);
     if (place.first && d.starts) layout.put(d.starts);
     const int W = runs_of(d.workers, layout.total);
     if (place.run >= W) return;
@@ -905,10 +959,10 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
     const Spot<NB, D, G> spot;
     const Masks masks = make_masks();
 
-    for (int u = first_unit(place.run, W, layout.total); u < u_end;) {
+    for (int u = first_unit(place.run, W, layout.total); u < u_end; layout.again()) {
         const Item x = layout.item(u, u_end);
         u += x.count;
-        Wave<D, G, 1> w;
+        Wave<D, G, 1, true> w;
         // what the block's rows see: the same for its waves, which go in step
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
@@ -942,7 +996,18 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
 #pragma unroll
             for (int k = 0; k < kRegs; ++k) {
                 const bool in = Places<D, G>::token(k) < good;
-                if (piece == 0) to.key_grid[sub][k][lane] = open_key_grid<T>(in ? kg[k] : 0u, a.scale);
+                if (piece == 0) {
+                    const f32x2 grid = open_key_grid<T>(in ? kg[k] : 0u, a.scale);
+                    to.key_step[sub][k][lane] = grid[0];
+                    // the places of a register, once each
+                    const int group = ((lane & 15) + 16 * k) % (D / G);
+                    if ((lane & 15) < Places<D, G>::kGrids) {
+                        const uint32_t first = from_f32<Bf16>(grid[1]);
+                        to.key_base[sub][0][Places<D, G>::token(k)][group] = (uint16_t)first;
+                        to.key_base[sub][1][Places<D, G>::token(k)][group] =
+                            (uint16_t)from_f32<Bf16>(grid[1] - to_f32<Bf16>(first));
+                    }
+                }
                 if (piece == kParts - 1) to.value_grid[sub][k][lane] = open_value_grid<T, NB>(in ? vg[k] : 0u);
             }
             if (lane == 0 && piece == 0) to.good[sub] = good;
@@ -976,14 +1041,23 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
             page = page_of_step(within(t0 + (kAhead + 1) * kWideStep));
             __builtin_amdgcn_sched_barrier(0);
             const WideStep<D, G> &now = steps[buffer];
-#pragma unroll
+#pragma unroll 1
             for (int turn = 0; turn < kTurns; ++turn) {
                 const int pair = wave % TW + turn, t = t0 + 32 * pair;
                 if (t >= min(w.lim_high, t_end)) continue;
                 const int both[2] = {__builtin_amdgcn_readfirstlane(now.good[2 * pair]),
                                      __builtin_amdgcn_readfirstlane(now.good[2 * pair + 1])};
                 attend_step<T>(
-                    w, t, both, [] {}, [&](int half, int k) { return now.key_grid[2 * pair + half][k][lane]; },
+                    w, t, both, [] {}, [&](int half, int k) { return f32x2{now.key_step[2 * pair + half][k][lane], 0.f}; },
+                    [&](int half) {
+                        constexpr int kWords = D / G > 2 ? D / G / 2 : 1;
+                        const uint16_t *b = now.key_base[2 * pair + half][lane >= 48][lane & 15];
+                        u32x4 f = {0, 0, 0, 0};
+#pragma unroll
+                        for (int e = 0; e < kWords; ++e) f[e] = reinterpret_cast<const uint32_t *>(b)[e];
+                        if (D / G == 1) f[0] &= 0xffffu;        // the other half is not written
+                        return f;
+                    },
                     [&](int half, int mm) { return now.key[2 * pair + half][mm][lane]; }, [] {},
                     [&](int half, int k) { return now.value_grid[2 * pair + half][k][lane]; },
                     [&](int j) { return now.value[pair][j][lane]; });

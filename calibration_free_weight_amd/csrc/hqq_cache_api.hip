@@ -131,6 +131,14 @@ int tiles_for(int64_t rows, int dim)
     return t;
 }
 
+// Blocks of a launch that a CU holds, by the registers that the kernels' sums and codes in
+// flight take (their launch bounds say the same).
+int resident(int tiles16, int dim, int nbits)
+{
+    if (tiles16 > 1 || dim == 256) return 2;
+    return nbits == 8 && dim == 128 ? 3 : 4;
+}
+
 // The longest side that one block takes alone: cutting it saves four steps at most, and
 // joining the pieces costs a launch.
 constexpr int64_t kWhole = 512;
@@ -153,7 +161,7 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         x.unit = (int)(longest <= kWhole ? (longest + step) / step * step : step);
         // no more than the 256 CUs hold at once (a block more would take as long again), nor than
         // the units that there can be
-        const int64_t blocks = x.tiles16 == 1 ? 768 : 512;
+        const int64_t blocks = 256 * resident(x.tiles16, c->head_dim, c->nbits);
         const int64_t units = (rows / (16 * x.tiles16) + n_seqs) * hqq::units_along((int32_t)longest, x.unit);
         const int64_t each = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
         x.workers = (int)(each < units ? each : units);
