@@ -203,3 +203,11 @@ def test_reference_grid_bound(dtype, nbits):
     smaller = (step.to(dtype).view(torch.int16) - 1).view(dtype).double()
     span = x.double().reshape(-1, 2, 64).amax(-1) - base
     assert (smaller * (2 ** nbits - 1) < span).all()
+
+
+def test_packed_structs_are_the_structs(H):
+    """The binding's packed bytes are what the C structures hold."""
+    a = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11)
+    assert H._pack_cache(*a) == bytes(H.hqq_cache(*a))
+    b = (1, 2, 3, 4, 5, 6)
+    assert H._pack_seqs(*b) == bytes(H.hqq_seqs(*b))
