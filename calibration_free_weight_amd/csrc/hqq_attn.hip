@@ -63,11 +63,11 @@ __device__ __forceinline__ void add_pieces(Acc<E> &acc, int n, float m, float l,
 
 // Adds what one side found for a row; false if the item is whole and its result elsewhere.
 template <int E, int WPR>
-__device__ __forceinline__ bool add_side(Acc<E> &acc, const AttnSide &d, int b, int row_in_item, int along,
+__device__ __forceinline__ bool add_side(Acc<E> &acc, const AttnSide &d, int b, int row_in_item, int len,
                                          int h, int64_t row, int64_t rows)
 {
     const int lane = threadIdx.x & 63, per = 16 * d.tiles16;
-    const int U = d.starts[d.s.n_seqs], W = runs_of(d.workers, U);
+    const int U = d.starts[d.s.n_seqs], W = runs_of(d.workers, U), along = units_along(len, d.starts[d.s.n_seqs + 1]);
     const int u0 = d.starts[b] + row_in_item / per * along;
     const int w0 = run_of(u0, W, U), w1 = run_of(u0 + along - 1, W, U);
     if (w0 == w1) {
@@ -105,9 +105,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
     Acc<E> acc;
     const int64_t row = (int64_t)i * a.per + hq % a.per, rows = (int64_t)n_tokens * a.per;
     if (a.sides == 2)
-        add_side<E, WPR>(acc, a.side[1], 0, (int)row, units_along(a.side[1].s.fixed_len, a.side[1].unit), h, row, rows);
+        add_side<E, WPR>(acc, a.side[1], 0, (int)row, a.side[1].s.fixed_len, h, row, rows);
     if (!add_side<E, WPR>(acc, a.side[0], b, (i - r.begin) * a.per + hq % a.per,
-                          units_along(len_of(a.side[0].s, b), a.side[0].unit), h, row, rows))
+                          len_of(a.side[0].s, b), h, row, rows))
         return;
     if constexpr (WPR > 1) {
 #pragma unroll
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_items_kernel(JoinArgs a)
     by_unit.cu = d.starts;
     const int b = __builtin_amdgcn_readfirstlane(find_seq(by_unit, u));
     const Rows rows = rows_of(d.s, b);
-    const int along = units_along(len_of(d.s, b), d.unit), in_seq = u - d.starts[b];
+    const int along = units_along(len_of(d.s, b), d.starts[d.s.n_seqs + 1]), in_seq = u - d.starts[b];
     const int tile = in_seq / along, u0 = u - in_seq % along;
     if (u0 == u || run_of(u0, W, U) != w - 1) return;
     const int w1 = run_of(u0 + along - 1, W, U), row0 = tile * per;

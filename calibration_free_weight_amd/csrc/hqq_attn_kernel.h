@@ -233,79 +233,107 @@ struct Item {
 };
 
 // The units of a side, end to end. Up to 64 sequences each wave has them in its lanes, and
-// nothing waits for another; more are summed up in LDS.
+// nothing waits for another; more are summed up in LDS. Where runs would be short, units are
+// made longer until there is one to a run: a run that ends one item and begins another pays
+// for its start and its end twice, which is as much as several steps.
+constexpr int kShortRun = 6;    // units
+
 template <int ROWS, int WAVES>
 struct Layout {
     const AttnSide &d;
-    int per, total;
+    int per, unit, total;
     int start;                  // of sequence `lane` and its rows and length, with up to 64
     Rows rows;
     int len;
-    int32_t *starts;            // [n_seqs + 1] in LDS, with more
+    int32_t *starts, *scan;     // in LDS, with more: [n_seqs + 1], [WAVES]
     __device__ __forceinline__ bool few() const { return d.s.n_seqs <= 64; }
     __device__ __forceinline__ int units(const Rows &r, int len) const
     {
-        return tiles_of((r.end - r.begin) * per, ROWS) * units_along(len, d.unit);
+        return tiles_of((r.end - r.begin) * per, ROWS) * units_along(len, unit);
     }
-
-    // scan: [WAVES] in LDS
-    __device__ __forceinline__ Layout(const AttnSide &side, int per, int32_t *starts, int32_t *scan)
-        : d(side), per(per), start(0), rows{0, 0}, len(0), starts(starts)
+    // The sum of what the threads have, before the caller's (`before`) and in all.
+    __device__ __forceinline__ int block_sum(int x, int &before)
     {
-        const int t = threadIdx.x, n = d.s.n_seqs;
-        if (few()) {
-            read();
-            return;
-        }
-        const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
-        int sum = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int u = units(rows_of(d.s, b), len_of(d.s, b));
-            starts[b] = u;
-            sum += u;
-        }
-        const int run = wave_sum(sum);
-        if ((t & 63) == 63) scan[t >> 6] = run;
+        const int t = threadIdx.x, upto = wave_sum(x);
         __syncthreads();
-        int before = run - sum;
-        total = 0;
+        if ((t & 63) == 63) scan[t >> 6] = upto;
+        __syncthreads();
+        before = upto - x;
+        int all = 0;
         for (int w = 0; w < WAVES; ++w) {
             if (w < (t >> 6)) before += scan[w];
-            total += scan[w];
+            all += scan[w];
         }
-        for (int b = b0; b < b1; ++b) {
-            const int u = starts[b];
-            starts[b] = before;
-            before += u;
-        }
-        if (t == 0) starts[n] = total;
-        __syncthreads();
-        total = __builtin_amdgcn_readfirstlane(total);
+        return __builtin_amdgcn_readfirstlane(all);
     }
-
+    // The units before the lane's sequences (`before`) and in all, and with more than 64 those
+    // of each of the thread's, to `starts`.
+    __device__ __forceinline__ int count(int &before, bool keep)
+    {
+        if (few()) {
+            const int u = (int)(threadIdx.x & 63) < d.s.n_seqs ? units(rows, len) : 0;
+            const int upto = wave_sum(u);
+            before = upto - u;
+            return __builtin_amdgcn_readlane(upto, 63);
+        }
+        const int t = threadIdx.x, n = d.s.n_seqs;
+        const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
+        int sum = 0;
+        for (int b = b0; b < b1; ++b) sum += units(rows_of(d.s, b), len_of(d.s, b));
+        const int all = block_sum(sum, before);
+        if (keep) {
+            int at = before;
+            for (int b = b0; b < b1; ++b) {
+                starts[b] = at;
+                at += units(rows_of(d.s, b), len_of(d.s, b));
+            }
+            if (t == 0) starts[n] = all;
+            __syncthreads();
+        }
+        return all;
+    }
     __device__ __forceinline__ void read()
     {
         const int lane = threadIdx.x & 63;
-        int u = 0;
         if (lane < d.s.n_seqs) {
             rows = rows_of(d.s, lane);
             len = len_of(d.s, lane);
-            u = units(rows, len);
         }
-        const int upto = wave_sum(u);
-        start = upto - u;
-        total = __builtin_amdgcn_readlane(upto, 63);
+    }
+
+    __device__ __forceinline__ Layout(const AttnSide &side, int per, int32_t *starts, int32_t *scan)
+        : d(side), per(per), unit(side.unit), start(0), rows{0, 0}, len(0), starts(starts), scan(scan)
+    {
+        if (few()) read();
+        total = count(start, false);
+        if (total > d.workers && total <= kShortRun * d.workers) {
+            const int times = (total + d.workers - 1) / d.workers, first = unit;
+            // two tries: rounding up by sequence may leave more units than runs
+            for (int more = 0; more < 2; ++more) {
+                unit = first * (times + more);
+                total = count(start, false);
+                if (total <= d.workers) break;
+            }
+            if (total > d.workers) {
+                unit = first;
+                total = count(start, false);
+            }
+        }
+        if (!few()) count(start, true);
     }
     // Before a further item: what the lanes had is read again rather than kept in registers.
     __device__ __forceinline__ void again()
     {
-        if (few()) read();
+        if (!few()) return;
+        read();
+        total = count(start, false);
     }
 
-    // to: [n_seqs + 1] in memory
+    // to: [n_seqs + 2] in memory, the last the unit
     __device__ __forceinline__ void put(int32_t *to) const
     {
         const int t = threadIdx.x, n = d.s.n_seqs;
+        if (t == 0) to[n + 1] = unit;
         if (few()) {
             if (t < n) to[t] = start;
             if (t == 0) to[n] = total;
@@ -338,7 +366,7 @@ struct Layout {
             first = __builtin_amdgcn_readfirstlane(starts[x.b]);
         }
         x.n_rows = (x.rows.end - x.rows.begin) * per;
-        x.along = units_along(x.len, d.unit);
+        x.along = units_along(x.len, unit);
         const unsigned in_seq = u - first, tile = in_seq / (unsigned)x.along;
         x.row0 = (int)tile * ROWS;
         x.u_in = (int)(in_seq - tile * x.along);
@@ -830,7 +858,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
         // what the last of the item's rows sees
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
-        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
+        const int t_end = (int)min((int64_t)(x.u_in + x.count) * layout.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[2][Spot<NB, D, G>::kKeyBytes / 4], vw[2][Spot<NB, D, G>::kValBytes];
         uint32_t kg[2][Places<D, G>::kRegs], vg[2][Places<D, G>::kRegs];
@@ -855,7 +883,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
                 spot.grids(a.c.v_meta, at, vg[half]);
             }
         };
-        int t0 = (int)min((int64_t)x.u_in * d.unit + wave * kTile, (int64_t)t_end);
+        int t0 = (int)min((int64_t)x.u_in * layout.unit + wave * kTile, (int64_t)t_end);
         if (t0 < t_end) {
             find(t0, page);
             load_keys(t0);
@@ -966,7 +994,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
         // what the block's rows see: the same for its waves, which go in step
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
         const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
-        const int t_end = (int)min((int64_t)(x.u_in + x.count) * d.unit, (int64_t)seen);
+        const int t_end = (int)min((int64_t)(x.u_in + x.count) * layout.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4 / kParts], vw[Spot<NB, D, G>::kValBytes], kg[kRegs], vg[kRegs];
         int good;
@@ -1012,7 +1040,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
             }
             if (lane == 0 && piece == 0) to.good[sub] = good;
         };
-        int t0 = (int)min((int64_t)x.u_in * d.unit, (int64_t)t_end), page = 0, buffer = 0;
+        int t0 = (int)min((int64_t)x.u_in * layout.unit, (int64_t)t_end), page = 0, buffer = 0;
         // a step that there is not is fetched like the last one, and not used
         auto within = [&](int t) { return t < t_end ? t : t0; };
         if (t0 < t_end) fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));

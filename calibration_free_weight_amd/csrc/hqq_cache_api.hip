@@ -166,7 +166,7 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         const int64_t each = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
         x.workers = (int)(each < units ? each : units);
         const size_t slots = (size_t)c->n_heads * 2 * x.workers * 16 * x.tiles16;
-        x.starts = take(4 * ((size_t)n_seqs + 1));
+        x.starts = take(4 * ((size_t)n_seqs + 2));
         x.slot_o = take(slots * c->head_dim * 4);
         x.slot_ml = take(slots * 8);
         if (prefix_len > 0) {

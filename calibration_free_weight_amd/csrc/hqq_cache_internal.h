@@ -92,13 +92,13 @@ hipError_t launch_cache_rows(bool write, const CacheView &c, const SeqView &s, c
 // goes on behind it. Whole items go to the output, or with two sides to `row_o`.
 struct AttnSide {
     SeqView s;
-    int32_t *starts;            // [n_seqs + 1]: units before each sequence's, of one head; null
-                                // without a joining launch, as the pieces
+    int32_t *starts;            // [n_seqs + 2]: units before each sequence's, of one head, and
+                                // their tokens; null without a joining launch, as the pieces
     float *slot_o;              // [heads][2 * workers][rows_per][dim], not divided by the sum
     float *slot_ml;             // [heads][2 * workers][rows_per][2]: maximum (base 2), sum
     float *row_o, *row_ml;      // [heads][n_tokens * per][dim], [..][2], or null
     int32_t workers;            // most runs of a head's units
-    int32_t unit;               // tokens
+    int32_t unit;               // tokens, at least
     int32_t tiles16;            // rows_per / 16: 1, 2, 4 or 8
     int32_t causal;             // rows see their own position and what is before it, else all
 };
