@@ -154,9 +154,9 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         at += (n + 255) / 256 * 256;
         return was;
     };
-    auto side = [&](int64_t tile_rows, int n_seqs, int64_t longest) {
+    auto cut = [&](int tiles16, int n_seqs, int64_t longest) {
         SidePlan x{};
-        x.tiles16 = tiles_for(tile_rows, c->head_dim);
+        x.tiles16 = tiles16;
         const int64_t step = hqq::kStep;
         x.unit = (int)(longest <= kWhole ? (longest + step) / step * step : step);
         // no more than the 256 CUs hold at once (a block more would take as long again), nor than
@@ -165,6 +165,9 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         const int64_t units = (rows / (16 * x.tiles16) + n_seqs) * hqq::units_along((int32_t)longest, x.unit);
         const int64_t each = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
         x.workers = (int)(each < units ? each : units);
+        return x;
+    };
+    auto lay = [&](SidePlan &x, int n_seqs) {
         const size_t slots = (size_t)c->n_heads * 2 * x.workers * 16 * x.tiles16;
         x.starts = take(4 * ((size_t)n_seqs + 2));
         x.slot_o = take(slots * c->head_dim * 4);
@@ -173,11 +176,20 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
             x.row_o = take((size_t)c->n_heads * rows * c->head_dim * 4);
             x.row_ml = take((size_t)c->n_heads * rows * 8);
         }
-        return x;
     };
     const int64_t longest = (int64_t)s->max_pages * c->page_size;
-    p.own = side((rows + s->n_seqs - 1) / s->n_seqs, s->n_seqs, longest);
-    if (prefix_len > 0) p.prefix = side(rows, 1, prefix_len);
+    p.own = cut(tiles_for((rows + s->n_seqs - 1) / s->n_seqs, c->head_dim), s->n_seqs, longest);
+    if (prefix_len > 0) {
+        p.prefix = cut(tiles_for(rows, c->head_dim), 1, prefix_len);
+        // Short sequences behind a prefix go in its launch, in its larger tiles, while the GPU
+        // holds the blocks of both: few steps in mostly empty tiles beside the prefix's cost
+        // less than a launch of their own.
+        const SidePlan with = cut(p.prefix.tiles16, s->n_seqs, longest);
+        const int64_t both = (int64_t)(with.workers + p.prefix.workers) * c->n_heads;
+        if (longest <= kWhole && both <= 256 * resident(with.tiles16, c->head_dim, c->nbits)) p.own = with;
+    }
+    lay(p.own, s->n_seqs);
+    if (prefix_len > 0) lay(p.prefix, 1);
     p.join = prefix_len > 0 || longest > p.own.unit;
     p.bytes = p.join ? at : 0;
     return p;
