@@ -12,6 +12,7 @@ constexpr int kAhead = 8;       // pieces asked for at a time
 // which are of whole items.
 constexpr int64_t kManyRows = 2048;
 constexpr int kJoinRows = 16;   // of an item, to a block
+constexpr int64_t kJoinAcross = 1 << 20;        // blocks
 
 template <int E>
 struct Acc {                    // a row's result so far; a lane holds E dimensions
@@ -68,6 +69,7 @@ __device__ __forceinline__ bool add_side(Acc<E> &acc, const AttnSide &d, int b, 
 {
     const int lane = threadIdx.x & 63, per = 16 * d.tiles16;
     const int U = d.starts[d.s.n_seqs], W = runs_of(d.workers, U), along = units_along(len, d.starts[d.s.n_seqs + 1]);
+    if (U == 0) return false;       // row offsets that fall: there is nothing to join
     const int u0 = d.starts[b] + row_in_item / per * along;
     const int w0 = run_of(u0, W, U), w1 = run_of(u0 + along - 1, W, U);
     if (w0 == w1) {
@@ -95,10 +97,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
     constexpr int E = D / 64;
     __shared__ float part[WPR > 1 ? kJoinWaves : 1][D];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int x = (int)(blockIdx.x * (unsigned)(kJoinWaves / WPR)) + wave / WPR;
     const int heads = a.heads * a.per, n_tokens = a.side[0].s.n_tokens;
-    const int i = x / heads, hq = x % heads, h = hq / a.per;
-    if (i >= n_tokens) return;                      // all waves of a row together
+    const int64_t x64 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kJoinWaves / WPR) + wave / WPR;
+    if (x64 >= (int64_t)n_tokens * heads) return;   // all waves of a row together
+    const int x = (int)x64, i = x / heads, hq = x % heads, h = hq / a.per;
     const int b = __builtin_amdgcn_readfirstlane(find_seq(a.side[0].s, i));
     const Rows r = rows_of(a.side[0].s, b);
     if (i < r.begin || i >= r.end) return;          // a row of no sequence stays as it was
@@ -184,8 +186,11 @@ void join_rows(const JoinArgs &a, hipStream_t stream)
         if (ends > 0) join_items_kernel<T, D><<<dim3((unsigned)(ends * a.heads), (unsigned)((16 * a.side[0].tiles16 + kJoinRows - 1) / kJoinRows)), kJoinThreads, 0, stream>>>(a);
     } else if (rows <= 1024)
         join_kernel<T, D, kJoinWaves><<<dim3((unsigned)rows), kJoinThreads, 0, stream>>>(a);
-    else
-        join_kernel<T, D, 1><<<dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)), kJoinThreads, 0, stream>>>(a);
+    else {
+        // a dimension of a grid has less than 2^32 threads
+        const int64_t blocks = (rows + kJoinWaves - 1) / kJoinWaves, across = blocks < kJoinAcross ? blocks : kJoinAcross;
+        join_kernel<T, D, 1><<<dim3((unsigned)across, (unsigned)((blocks + across - 1) / across)), kJoinThreads, 0, stream>>>(a);
+    }
 }
 
 template <typename T>

@@ -245,6 +245,7 @@ struct Layout {
     int start;                  // of sequence `lane` and its rows and length, with up to 64
     Rows rows;
     int len;
+    bool falls;
     int32_t *starts, *scan;     // in LDS, with more: [n_seqs + 1], [WAVES]
     __device__ __forceinline__ bool few() const { return d.s.n_seqs <= 64; }
     __device__ __forceinline__ int units(const Rows &r, int len) const
@@ -266,21 +267,25 @@ struct Layout {
         }
         return __builtin_amdgcn_readfirstlane(all);
     }
-    // The units before the lane's sequences (`before`) and in all, and with more than 64 those
-    // of each of the thread's, to `starts`.
+    // The units before the lane's sequences (`before`) and in all (none if row offsets fall), and
+    // with more than 64 those of each of the thread's, to `starts`.
     __device__ __forceinline__ int count(int &before, bool keep)
     {
         if (few()) {
             const int u = (int)(threadIdx.x & 63) < d.s.n_seqs ? units(rows, len) : 0;
             const int upto = wave_sum(u);
             before = upto - u;
-            return __builtin_amdgcn_readlane(upto, 63);
+            return __any(falls) ? 0 : __builtin_amdgcn_readlane(upto, 63);
         }
         const int t = threadIdx.x, n = d.s.n_seqs;
         const int each = (n + 64 * WAVES - 1) / (64 * WAVES), b0 = min(t * each, n), b1 = min(b0 + each, n);
         int sum = 0;
-        for (int b = b0; b < b1; ++b) sum += units(rows_of(d.s, b), len_of(d.s, b));
-        const int all = block_sum(sum, before);
+        falls = false;
+        for (int b = b0; b < b1; ++b) {
+            sum += units(rows_of(d.s, b), len_of(d.s, b));
+            falls = falls || falls_at(d.s, b);
+        }
+        const int upto = block_sum(sum, before), all = __syncthreads_or(falls) ? 0 : upto;
         if (keep) {
             int at = before;
             for (int b = b0; b < b1; ++b) {
@@ -298,15 +303,17 @@ struct Layout {
         if (lane < d.s.n_seqs) {
             rows = rows_of(d.s, lane);
             len = len_of(d.s, lane);
+            falls = falls_at(d.s, lane);
         }
     }
 
     __device__ __forceinline__ Layout(const AttnSide &side, int per, int32_t *starts, int32_t *scan)
-        : d(side), per(per), unit(side.unit), start(0), rows{0, 0}, len(0), starts(starts), scan(scan)
+        : d(side), per(per), unit(side.unit), start(0), rows{0, 0}, len(0), falls(false), starts(starts), scan(scan)
     {
         if (few()) read();
         total = count(start, false);
-        if (total > d.workers && total <= kShortRun * d.workers) {
+        const int longest = d.s.fixed_len >= 0 ? d.s.fixed_len : d.s.max_pages << d.s.page_shift;
+        if (total > d.workers && total <= kShortRun * d.workers && unit < longest) {
             const int times = (total + d.workers - 1) / d.workers, first = unit;
             // two tries: rounding up by sequence may leave more units than runs
             for (int more = 0; more < 2; ++more) {
@@ -391,31 +398,37 @@ struct Wave {
     int lim[RT];                // what a row sees ends here
     int lim_low, lim_high;      // for all rows, for any
     f32x4 o[RT][D / 16];
-    u32x4 qb[BASE_FRAGS ? RT : 1];      // the sums as a B fragment
+    u32x4 qb[BASE_FRAGS ? RT : 1][kGroups > 4 ? 2 : 1];      // the sums as B fragments
     // m: scores are taken from it; above: how far one may lie above before m moves (none
     // while m has not been set)
     float m[RT], above[RT], l[RT], bsum[RT][kGroups];
     float step_lim, step_by;    // V's steps are below step_lim and multiplied by step_by
 };
 
-// The bases' part of the scores as one product of bfloat16 parts, exact but for the last:
-// slot e of the contraction's quad 0, 1 and 2 has the base of group e (its first part) and the
-// first, second and third part of the column's sum over that group, of quad 3 the second part
-// of the base (none of a bfloat16 one) and the first of the sum. What is left out is below
-// 2^-16 of the largest.
+// The bases' part of the scores as one product of bfloat16 parts: slot e of the contraction's
+// quads 0, 1 and 2 has the base of group e (its first part) and the first, second and third part
+// of the column's sum over that group, of quad 3 the second part of the base (none of a bfloat16
+// one) and the first of the sum; slot e + base_slots() of quad 3, the second of both. What is
+// left out is below 2^-23 of the product. Eight groups take two such products.
 template <int GROUPS>
-__device__ __forceinline__ u32x4 base_query(const float (&sum)[GROUPS], int quad)
+constexpr int base_products() { return GROUPS > 4 ? 2 : 1; }
+template <int GROUPS>
+constexpr int base_slots() { return GROUPS < 2 ? 2 : GROUPS / base_products<GROUPS>(); }
+template <int GROUPS>
+__device__ __forceinline__ u32x4 base_query(const float (&sum)[GROUPS], int product, int quad)
 {
-    static_assert(GROUPS <= 8, "a slot for each group");
+    constexpr int kSlots = base_slots<GROUPS>();
+    static_assert(kSlots <= 4, "two slots for each group");
     uint32_t bits[8] = {};
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-        float x = sum[g];
+    for (int g = 0; g < kSlots && g < GROUPS; ++g) {
+        float x = sum[product * kSlots + g];
         const uint32_t first = from_f32<Bf16>(x);
         x -= to_f32<Bf16>(first);
         const uint32_t second = from_f32<Bf16>(x);
         x -= to_f32<Bf16>(second);
         bits[g] = quad == 1 ? second : quad == 2 ? from_f32<Bf16>(x) : first;
+        bits[g + kSlots] = quad == 3 ? second : 0u;
     }
     u32x4 f;
 #pragma unroll
@@ -465,7 +478,9 @@ __device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnA
             w.qsum[t][g] = column_sum(sum) * a.scale;
             w.bsum[t][g] = 0.f;
         }
-        if constexpr (BASE_FRAGS) w.qb[t] = base_query<D / G>(w.qsum[t], quad);
+        if constexpr (BASE_FRAGS)
+#pragma unroll
+            for (int p = 0; p < base_products<D / G>(); ++p) w.qb[t][p] = base_query<D / G>(w.qsum[t], p, quad);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) w.o[t][j] = f32x4{0, 0, 0, 0};
         w.m[t] = 0.f;
@@ -492,7 +507,7 @@ struct Places {
 // grids of the missing ones {0, 0}. key_grid(half, k) gives {step * scale, base} of a lane's
 // place, value_grid {step, middle}; key(half, mm) and value(j) the A fragments. after_keys() is
 // called when no more keys are needed, before the values' grids and fragments are. With
-// BASE_FRAGS base(half) is the A fragment of the bases (base_query has the other), and what
+// BASE_FRAGS base(half, p) is the A fragment of the bases (base_query has the other), and what
 // key_grid says of them is not used.
 template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
           typename After, typename ValueGrid, typename Value>
@@ -512,11 +527,13 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
         for (int k = 0; k < kRegs; ++k) kgrid[k] = key_grid(half.value, k);
 #pragma unroll
         for (int t = 0; t < RT; ++t) from[t] = f32x4{-w.m[t], -w.m[t], -w.m[t], -w.m[t]};
-        if constexpr (BASE_FRAGS) {
-            const u32x4 bf = base(half.value);
+        if constexpr (BASE_FRAGS)
 #pragma unroll
-            for (int t = 0; t < RT; ++t) from[t] = mfma32<true>(bf, w.qb[t], from[t]);
-        }
+            for (int p = 0; p < base_products<kGroups>(); ++p) {
+                const u32x4 bf = base(half.value, p);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) from[t] = mfma32<true>(bf, w.qb[t][p], from[t]);
+            }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
@@ -594,6 +611,13 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
             vgrid[half][k] = value_grid(half, k);
             most = fmaxf(most, vgrid[half][k][0]);
         }
+    if (!open) {        // a group that held infinities or NaN, and a weight of 0
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k)
+                if (!(fabsf(vgrid[half][k][1]) < INFINITY)) vgrid[half][k][1] = 0.f;
+    }
     if (__any(most >= w.step_lim && most > 0.f)) {
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
@@ -909,7 +933,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
                         for (int k = 0; k < Places<D, G>::kRegs; ++k)
                             if (Places<D, G>::token(k) >= good[half]) kg[half][k] = vg[half][k] = 0;
                 },
-                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); }, [](int) { return u32x4{}; },
+                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); }, [](int, int) { return u32x4{}; },
                 [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
                 [&] {
                     page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
@@ -1077,13 +1101,14 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
                                      __builtin_amdgcn_readfirstlane(now.good[2 * pair + 1])};
                 attend_step<T>(
                     w, t, both, [] {}, [&](int half, int k) { return f32x2{now.key_step[2 * pair + half][k][lane], 0.f}; },
-                    [&](int half) {
-                        constexpr int kWords = D / G > 2 ? D / G / 2 : 1;
-                        const uint16_t *b = now.key_base[2 * pair + half][lane >= 48][lane & 15];
+                    [&](int half, int p) {
+                        // the same in the slots of the parts behind, which meet zeros but in quad 3
+                        constexpr int kWords = base_slots<D / G>() / 2;
+                        const uint16_t *b = now.key_base[2 * pair + half][lane >= 48][lane & 15] + 2 * kWords * p;
                         u32x4 f = {0, 0, 0, 0};
 #pragma unroll
-                        for (int e = 0; e < kWords; ++e) f[e] = reinterpret_cast<const uint32_t *>(b)[e];
-                        if (D / G == 1) f[0] &= 0xffffu;        // the other half is not written
+                        for (int e = 0; e < kWords; ++e) f[e] = f[e + kWords] = reinterpret_cast<const uint32_t *>(b)[e];
+                        if (D / G == 1) f[0] = f[1] = f[0] & 0xffffu;       // the other half is not written
                         return f;
                     },
                     [&](int half, int mm) { return now.key[2 * pair + half][mm][lane]; }, [] {},

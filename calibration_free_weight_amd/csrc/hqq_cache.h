@@ -49,6 +49,14 @@ HQQ_HD Rows rows_of(const SeqView &s, int32_t b)
     return r;
 }
 
+// Whether the rows of sequence b + 1 would begin before those of b: a call where any do attends
+// for none. (Else the sequences' rows are at most n_tokens together, and so is what is counted
+// from them.)
+HQQ_HD bool falls_at(const SeqView &s, int32_t b)
+{
+    return s.cu && clamp_i32(s.cu[b + 1], 0, s.n_tokens) < clamp_i32(s.cu[b], 0, s.n_tokens);
+}
+
 HQQ_HD int32_t len_of(const SeqView &s, int32_t b)
 {
     // max_pages << page_shift is below 2^31 (checked by the call)

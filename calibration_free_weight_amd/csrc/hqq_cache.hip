@@ -12,7 +12,7 @@
 namespace hqq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kRowThreads;
 
 // Whether row i belongs to a sequence, and where its token lies: page (or -1), token of it.
 struct Slot {
@@ -48,19 +48,29 @@ __device__ __forceinline__ Place place_of(int heads)
                  (int)threadIdx.x % kLanes};
 }
 
-// Smaller and larger of two (fminf would first quiet signalling numbers: an instruction each).
-__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
-__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
-__device__ __forceinline__ uint32_t larger_halves(uint32_t a, uint32_t b)
+// Smallest and largest of three, of binary32 numbers or of each half of three words: NaN if one is.
+__device__ __forceinline__ float smallest(float a, float b, float c)
 {
-    uint32_t r;
-    asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    float r;
+    asm("v_minimum3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
     return r;
 }
-__device__ __forceinline__ uint32_t smaller_halves(uint32_t a, uint32_t b)
+__device__ __forceinline__ float largest(float a, float b, float c)
+{
+    float r;
+    asm("v_maximum3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t smallest_halves(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t r;
-    asm("v_pk_min_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    asm("v_pk_minimum3_f16 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t largest_halves(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("v_pk_maximum3_f16 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
     return r;
 }
 
@@ -81,25 +91,26 @@ __device__ __forceinline__ uint32_t over_group(uint32_t x, F f)
     return x;
 }
 
-// The smallest and largest of a group, of which the lane has the values v (bits raw).
+// The smallest and largest of a group, of which the lane has the values v (bits raw); NaN if one
+// of the group is.
 template <typename T, int G>
 __device__ __forceinline__ void group_range(const uint4 raw, const float (&v)[8], float &lo, float &hi)
 {
     if constexpr (Types<T>::kBf16) {
-        lo = smaller(smaller(smaller(v[0], v[1]), smaller(v[2], v[3])), smaller(smaller(v[4], v[5]), smaller(v[6], v[7])));
-        hi = larger(larger(larger(v[0], v[1]), larger(v[2], v[3])), larger(larger(v[4], v[5]), larger(v[6], v[7])));
+        lo = smallest(smallest(smallest(v[0], v[1], v[2]), v[3], v[4]), v[5], smallest(v[6], v[7], v[7]));
+        hi = largest(largest(largest(v[0], v[1], v[2]), v[3], v[4]), v[5], largest(v[6], v[7], v[7]));
         lo = __uint_as_float(over_group<G>(__float_as_uint(lo), [](uint32_t a, uint32_t b) {
-            return __float_as_uint(smaller(__uint_as_float(a), __uint_as_float(b)));
+            return __float_as_uint(smallest(__uint_as_float(a), __uint_as_float(b), __uint_as_float(b)));
         }));
         hi = __uint_as_float(over_group<G>(__float_as_uint(hi), [](uint32_t a, uint32_t b) {
-            return __float_as_uint(larger(__uint_as_float(a), __uint_as_float(b)));
+            return __float_as_uint(largest(__uint_as_float(a), __uint_as_float(b), __uint_as_float(b)));
         }));
     } else {
         // two at a time; then the smallest, negated, and the largest in one word
-        const uint32_t h = larger_halves(larger_halves(raw.x, raw.y), larger_halves(raw.z, raw.w));
-        const uint32_t l = smaller_halves(smaller_halves(raw.x, raw.y), smaller_halves(raw.z, raw.w)) ^ 0x80008000u;
-        const uint32_t both = larger_halves(__builtin_amdgcn_perm(h, l, 0x05040100u), __builtin_amdgcn_perm(h, l, 0x07060302u));
-        const uint32_t all = over_group<G>(both, [](uint32_t a, uint32_t b) { return larger_halves(a, b); });
+        const uint32_t h = largest_halves(largest_halves(raw.x, raw.y, raw.z), raw.w, raw.w);
+        const uint32_t l = smallest_halves(smallest_halves(raw.x, raw.y, raw.z), raw.w, raw.w) ^ 0x80008000u;
+        const uint32_t x = __builtin_amdgcn_perm(h, l, 0x05040100u), y = __builtin_amdgcn_perm(h, l, 0x07060302u);
+        const uint32_t all = over_group<G>(largest_halves(x, y, y), [](uint32_t a, uint32_t b) { return largest_halves(a, b, b); });
         lo = -to_f32<T>(all & 0xffffu);
         hi = to_f32<T>(all >> 16);
     }
@@ -163,7 +174,9 @@ __device__ __forceinline__ uint32_t quantize8(const uint4 raw, float (&q)[8])
     if (!Types<T>::kBf16 && fmaf((float)kTop, step, lo) >= 65520.f)
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = fminf(q[e], (float)(kTop - 1));
-    return sb | (from_f32<T>(lo) << 16);
+    // A group that holds infinities or NaN reads back as NaN: step 0, which leaves what attention
+    // makes of the other groups alone.
+    return hi - lo < INFINITY ? sb | (from_f32<T>(lo) << 16) : Types<T>::kBf16 ? 0x7fc00000u : 0x7e000000u;
 }
 
 // Four codes as bytes, clamped to them (a number that is none becomes 0).
@@ -314,8 +327,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheView c, SeqVi
 template <typename T, int NB, int D, int G, int HEADS>
 void launch_heads(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p, hipStream_t stream)
 {
-    constexpr int kTokens = 8 * kThreads / D;
-    const dim3 grid((unsigned)(((int64_t)s.n_tokens + kTokens - 1) / kTokens * ((c.heads + HEADS - 1) / HEADS)));
+    const dim3 grid((unsigned)cache_rows_blocks(s.n_tokens, c.heads, D));
     if (write) cache_write_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
     else cache_read_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
 }
@@ -324,7 +336,7 @@ template <typename T, int NB, int D, int G>
 hipError_t launch(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p, hipStream_t stream)
 {
     // four heads to a wave, unless that leaves the GPU's 1024 units without a few waves each
-    if ((int64_t)s.n_tokens * c.heads * D >= int64_t(1) << 23) launch_heads<T, NB, D, G, 4>(write, c, s, p, stream);
+    if (four_heads(s.n_tokens, c.heads, D)) launch_heads<T, NB, D, G, 4>(write, c, s, p, stream);
     else launch_heads<T, NB, D, G, 1>(write, c, s, p, stream);
     return hipGetLastError();
 }

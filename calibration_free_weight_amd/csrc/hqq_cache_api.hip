@@ -101,6 +101,9 @@ hqq_status cache_rows(bool write, const hqq_cache *cache, const hqq_seqs *seqs, 
     st = check_rows(k, k_ts, k_hs, null, shape);
     if (st == HQQ_OK) st = check_rows(v, v_ts, v_hs, null, shape);
     if (st != HQQ_OK) return st;
+    // what the launch takes (a dimension of a grid has less than 2^32 threads)
+    if (hqq::cache_rows_blocks(seqs->n_tokens, cache->n_heads, cache->head_dim) >= (1 << 24))
+        return refuse("too many rows for one call", HQQ_ERR_UNSUPPORTED);
     auto rows = [](const void *p) { return static_cast<uint16_t *>(const_cast<void *>(p)); };
     const hqq::RowPtrs p{rows(k), rows(v), k_ts, k_hs, v_ts, v_hs};
     return done(hqq::launch_cache_rows(write, view_of(cache), view_of(cache, seqs), p, cache->head_dim,
@@ -109,6 +112,8 @@ hqq_status cache_rows(bool write, const hqq_cache *cache, const hqq_seqs *seqs, 
 }
 
 // ---- attention --------------------------------------------------------------------------------
+constexpr float kLog2e = 1.44269504088896341f;
+
 // How one side's work is cut, and where its partial results lie in the workspace.
 struct SidePlan {
     int tiles16, workers, unit;
@@ -203,8 +208,8 @@ hqq_status check_plan(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int6
     if (st != HQQ_OK) return st;
     if (n_q_heads < 1 || n_q_heads % c->n_heads != 0)
         return refuse("n_q_heads must be a positive multiple of the cache's n_heads");
-    if (s->n_tokens * n_q_heads > INT32_MAX || n_q_heads > (1 << 20))
-        return refuse("n_tokens * n_q_heads must be below 2^31");
+    if (n_q_heads > (1 << 20) || s->n_tokens * n_q_heads > (1 << 30))
+        return refuse("n_q_heads must be at most 2^20, and n_tokens * n_q_heads at most 2^30");
     if (prefix_len < 0 || prefix_len > (1 << 30)) return refuse("prefix_len must be in [0, 2^30]");
     *empty = s->n_seqs == 0 || s->n_tokens == 0;
     if (*empty) return HQQ_OK;
@@ -265,7 +270,7 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
         return refuse("prefix_len must be at most n_prefix_pages * page_size, and that at most 2^30");
     if (prefix_len > 0 && (!prefix_pages || !aligned(prefix_pages, 4)))
         return refuse("prefix_pages must be non-null and 4-byte aligned");
-    if (!std::isfinite(scale)) return refuse("scale must be finite");
+    if (!std::isfinite(scale * kLog2e)) return refuse("scale must be finite, and times log2(e) too");
     if (empty) return done(hipSuccess);
     st = check_rows(q, q_token_stride, q_head_stride, "q must be non-null",
                     "q must be 16-byte aligned, with strides that are multiples of 8 in [0, 2^36]");
@@ -295,7 +300,7 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     a.o_ts = out_token_stride;
     a.o_hs = out_head_stride;
     a.per = n_q_heads / cache->n_heads;
-    a.scale = scale * 1.44269504088896341f;
+    a.scale = scale * kLog2e;
     hqq::JoinArgs j{{a.side[0], {}}, 1, a.out, lse, a.o_ts, a.o_hs, a.per, cache->n_heads, cache->head_dim};
     hipError_t e = hipSuccess;
     if (shared) {

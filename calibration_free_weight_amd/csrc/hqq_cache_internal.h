@@ -80,6 +80,16 @@ __device__ __forceinline__ int find_seq(const SeqView &s, int i)
     return lo;
 }
 
+// A block of a write or read has 256 * 8 / head_dim tokens of four heads at a time, or of one
+// where the call has less than 2^23 numbers.
+constexpr int kRowThreads = 256;
+inline bool four_heads(int64_t n_tokens, int heads, int dim) { return n_tokens * heads * dim >= int64_t(1) << 23; }
+inline int64_t cache_rows_blocks(int64_t n_tokens, int heads, int dim)
+{
+    const int tokens = 8 * kRowThreads / dim, at_once = four_heads(n_tokens, heads, dim) ? 4 : 1;
+    return (n_tokens + tokens - 1) / tokens * ((heads + at_once - 1) / at_once);
+}
+
 // write: k and v rows into the cache; else back out of it. dim 64/128/256, nbits 4/8, g
 // 32/64/128 <= dim.
 hipError_t launch_cache_rows(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p,

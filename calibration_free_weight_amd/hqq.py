@@ -473,6 +473,8 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
         need = L.hqq_cache_attention_workspace(c, s, heads, prefix_len)
         if need:
             workspace = _scratch(need, dev, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad("workspace must be contiguous, on the cache's device")
     wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     st = _on(dev, L.hqq_cache_attention_prefix, c, s, pages, n_pages, prefix_len, qp, qt, qh, heads,
              dim ** -0.5 if scale is None else scale, op, ot, oh, None if lse is None else lse.data_ptr(),

@@ -293,8 +293,8 @@ hqq_status hqq_gemm_f16(const void *X, int64_t M, const void *Wr, int64_t N, int
  *   q    = min(rne((v - base) / step), top), decided on the exact quotient,
  * and read back as base + q * step, off by at most step / 2. (With binary16, where base +
  * top * step would round to infinity, q stops at top - 1 and the error at step.) Values must
- * be finite, and below 2^120 with bfloat16; a group that holds others reads back as
- * unspecified values, other groups are not affected.
+ * be finite, and below 2^120 with bfloat16; a group that holds infinities or NaN reads back as
+ * NaN, other groups are not affected.
  *
  * Pages. Tokens lie in pages of page_size; a sequence's pages are listed in a table, so that
  * sequences grow page by page and may share pages. Per page and head:
@@ -335,9 +335,9 @@ typedef struct hqq_cache {
  * kernel leave its buffers: lengths count as 0..max_pages*page_size, rows outside the tensors
  * do not exist, and a position whose table entry is not in [0, n_pages), or that is
  * negative, is not in the cache (writes drop it, reads give zeros, attention does not see
- * it). Rows behind cu_tokens[n_seqs] are not touched. cu_tokens must not decrease, and one
- * position of the cache must not be written twice by a call, or its contents are
- * unspecified. */
+ * it). Rows behind cu_tokens[n_seqs] are not touched. cu_tokens must not decrease (where it
+ * does, attention leaves all rows as they were), and one position of the cache must not be
+ * written twice by a call, or its contents are unspecified. */
 typedef struct hqq_seqs {
     const int32_t *table;    /* [n_seqs][max_pages]: pages of each sequence in order       */
     const int32_t *lens;     /* [n_seqs]: tokens of each sequence, the call's included     */
@@ -366,11 +366,14 @@ hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
  * reads key/value head h / (n_q_heads / n_heads). The row at position x of its sequence
  * sees positions 0..x (which must be in the cache already: write, then attend):
  *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * <q, k_t>),
- * with k_t, v_t = base + q * step unrounded, scores and sums in binary32, weights rounded to
- * 11 bits where they meet the codes of v, and out rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
- * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. workspace: device,
- * 256-byte aligned, at least hqq_cache_attention_workspace() bytes; calls that may run at the
- * same time need one each. Results do not depend on what it held. */
+ * with k_t, v_t = base + q * step unrounded, scores and sums in binary32 (the sums of
+ * |q| * 2^nbits must stay in its range), weights rounded to 11 bits where they meet the codes
+ * of v, and out rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
+ * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. What a row does not see
+ * does not change it, NaN included; a row that sees a group of NaN is unspecified, of v in that
+ * group's dimensions. n_tokens * n_q_heads is at most 2^30. out must not overlap q or itself.
+ * workspace: device, 256-byte aligned, at least hqq_cache_attention_workspace() bytes; calls
+ * that may run at the same time need one each. Results do not depend on what it held. */
 hqq_status hqq_cache_attention(const hqq_cache *cache, const hqq_seqs *seqs, const void *q,
                                int64_t q_token_stride, int64_t q_head_stride, int n_q_heads,
                                float scale, void *out, int64_t out_token_stride,

@@ -89,12 +89,18 @@ def test_bad_rows_and_plans_are_refused(H):
     def att(heads=4, scale=1.0, lse=None, ws=p, wb=big, pages=p, n=4, plen=10):
         return L.hqq_cache_attention_prefix(c, s, pages, n, plen, *good, heads, scale, *good, lse, ws, wb, None)
     for kw in (dict(heads=3), dict(heads=0), dict(heads=-2), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(scale=3e38), dict(heads=(1 << 20) + 2),
                dict(lse=p + 2), dict(ws=p + 16), dict(pages=None), dict(pages=p + 1), dict(plen=-1), dict(plen=65),
                dict(n=-1), dict(n=1 << 28)):
         assert att(**kw) == H.HQQ_ERR_ARG, kw
     need = L.hqq_cache_attention_workspace(c, s, 4, 10)
     assert need > 0
     assert att(ws=None) == H.HQQ_ERR_WORKSPACE and att(wb=need - 1) == H.HQQ_ERR_WORKSPACE
+    # more than a launch takes
+    wide, many = C.byref(cache(H, n_heads=64, head_dim=256)), C.byref(seqs(H, n_tokens=1 << 24))
+    for f in (L.hqq_cache_write, L.hqq_cache_read):
+        assert f(wide, many, p, 0, 0, p, 0, 0, None) == H.HQQ_ERR_UNSUPPORTED
+    assert L.hqq_cache_attention(c, many, p, 0, 0, 66, 1.0, *good, None, p, big, None) == H.HQQ_ERR_ARG
     # work counted beyond 32 bits
     s = C.byref(seqs(H, n_seqs=1, n_tokens=1 << 24, max_pages=1 << 26))
     assert L.hqq_cache_attention(c, s, *good, 64, 1.0, *good, None, p, big, None) == H.HQQ_ERR_UNSUPPORTED
@@ -134,6 +140,12 @@ int main()
             const int far = len - (x.end - x.begin);    // the smallest position a row can have
             need(far >= -n_tokens, "positions in 32 bits");
         }
+        // offsets that do not fall leave no more rows than there are; those that do are found
+        int64_t all = 0;
+        bool falls = false;
+        for (int b = 0; b < n; ++b) { all += rows_of(s, b).end - rows_of(s, b).begin; falls = falls || falls_at(s, b); }
+        need(falls || all <= n_tokens, "rows counted once");
+        need(!falls || !(sorted || uniform), "offsets that rise");
         for (int i = 0; i < n_tokens + 2; ++i) {
             const int b = seq_at(s, i);
             need(b >= 0 && b < n, "sequence of a row");

@@ -168,6 +168,7 @@ def test_values_that_are_not_finite_stay_in_their_group(H, dtype, nbits):
     keep = torch.ones_like(ref, dtype=torch.bool)
     keep[3, 1, 64:], keep[5, 0, :64], keep[6, 1, 64:] = False, False, False
     assert torch.equal(bk.cpu()[keep], ref[keep]) and torch.equal(bv.cpu()[keep.flip(0)], ref.flip(0)[keep.flip(0)])
+    assert torch.isnan(bk.cpu()[~keep]).all() and torch.isnan(bv.cpu()[~keep.flip(0)]).all()
 
 
 def test_pages_and_positions_that_are_not_there(H):
@@ -529,3 +530,143 @@ def test_empty_calls(H):
     lse = torch.empty(3, 4, dtype=torch.float32, device="cuda")
     out = H.cache_attention(cache, bare, i32([20]), torch.ones(3, 4, 64, dtype=F, device="cuda"), lse=lse)
     assert (out == 0).all() and (lse == -math.inf).all()
+
+
+# dtype, nbits, dim, group, page, kv heads, per, lens, new: many rows, more than 64 sequences, pieces
+MANY = [
+    (F, 4, 256, 32, 16, 1, 8, [300, 70], [40, 33]),
+    (B, 4, 256, 32, 32, 1, 16, [90], [50]),
+    (F, 8, 128, 32, 16, 2, 4, [700, 64, 1], [40, 40, 1]),
+    (F, 4, 64, 64, 16, 1, 8, [800, 33] + [20] * 70, [60, 9] + [9] * 70),
+    (B, 8, 128, 128, 64, 1, 1, [5] * 80 + [1200], [1] * 81),
+    (F, 4, 128, 64, 4096, 1, 2, [4099, 9], [130, 9]),
+    (B, 4, 128, 64, 16, 4, 4, [1300, 1000, 600], [1, 1, 1]),
+]
+
+
+@pytest.mark.parametrize("dtype,nbits,dim,group,page,kv,per,lens,new", MANY)
+def test_many_rows_bad_pages_and_far_bases(H, dtype, nbits, dim, group, page, kv, per, lens, new):
+    """Keys far from zero (their scores are mostly the bases' part), pages that are not there in
+    the middle of sequences, NaN in all that is not written; with a prefix of such pages too."""
+    gen = torch.Generator().manual_seed(dim + nbits + len(lens))
+    table, n_pages, free = layout(lens, page, gen, spare=8)
+    cache = poison(H.alloc_cache(n_pages, page, kv, dim, nbits, group, dtype))
+    cu = cumulated(lens)
+    far = values(cu[-1], kv, dim, dtype, gen) + 30 * torch.randn(kv, dim, generator=gen).to(dtype).cuda()
+    H.hqq_cache_write(cache, i32(table), i32(lens), far, values(cu[-1], kv, dim, dtype, gen), cu_tokens=i32(cu))
+    prefix = 3 * page + 5 if page < 1000 else 600
+    pages = free[:-(-prefix // page)]
+    H.hqq_cache_write(cache, i32([pages]), i32([prefix]), values(prefix, kv, dim, dtype, gen), values(prefix, kv, dim, dtype, gen))
+    for b in range(0, len(lens), 2):
+        for x in range(1, -(-lens[b] // page), 3):
+            table[b][x] = [-1, n_pages, 1 << 30][x % 3]
+    cu = cumulated(new)
+    q = (torch.rand(cu[-1], kv * per, dim, generator=gen) - 0.3).to(dtype).cuda()
+    every = torch.ones(cu[-1], dtype=torch.bool)
+    lse = torch.empty(cu[-1], kv * per, dtype=torch.float32, device="cuda")
+    held, scale = R.Held(cache), 0.25 / dim
+    out = H.cache_attention(cache, i32(table), i32(lens), q, cu_tokens=i32(cu), scale=scale, lse=lse)
+    R.check_attention(out, lse, R.attention(held, table, lens, cu, q, scale), every)
+    if len(pages) > 2:
+        pages[1] = -5
+    out = H.cache_attention_prefix(cache, i32(table), i32(lens), i32(pages), prefix, q, cu_tokens=i32(cu), scale=scale, lse=lse)
+    R.check_attention(out, lse, R.attention(held, table, lens, cu, q, scale, pages, prefix), every)
+
+
+@pytest.mark.parametrize("dtype,nbits,dim,group,per,new", [
+    (F, 4, 128, 64, 1, 7), (B, 8, 128, 32, 4, 8), (F, 8, 128, 128, 4, 30), (B, 4, 64, 32, 2, 60),
+    (F, 4, 256, 32, 1, 9), (B, 8, 256, 64, 8, 12)])
+def test_values_that_are_not_finite_are_not_seen_before_they_come(H, dtype, nbits, dim, group, per, new):
+    """Rows before a token with NaN or an infinity in its key or value give what they give
+    without it; rows from it on see NaN in the value's group at most, or in all with the key's."""
+    gen = torch.Generator().manual_seed(dim + new)
+    n = 250
+    table, n_pages, _ = layout([n], 16, gen)
+    k, v = values(n, 1, dim, dtype, gen), values(n, 1, dim, dtype, gen)
+    q = torch.randn(new, per, dim, generator=gen).to(dtype).cuda()
+    clean = poison(H.alloc_cache(n_pages, 16, 1, dim, nbits, group, dtype))
+    H.hqq_cache_write(clean, i32(table), i32([n]), k, v)
+    ref = R.attention(R.Held(clean), table, [n], None, q, dim ** -0.5)
+    at = n - 3                          # the last three rows see it
+    for bad in (math.nan, math.inf, -math.inf):
+        for which in (0, 1):
+            kv = [k.clone(), v.clone()]
+            kv[which][at, 0, 3] = bad
+            cache = poison(H.alloc_cache(n_pages, 16, 1, dim, nbits, group, dtype))
+            H.hqq_cache_write(cache, i32(table), i32([n]), *kv)
+            out = H.cache_attention(cache, i32(table), i32([n]), q)
+            before = torch.arange(new) < new - 3
+            R.check_attention(out, None, ref, before)
+            if which:                   # the value's other groups
+                R.check_attention(out[..., group:], None, tuple(x[..., group:] if x.dim() == 3 else x for x in ref), ~before)
+
+
+@pytest.mark.parametrize("n_seqs,per,new", [(3, 1, 1), (70, 1, 1), (3, 8, 40), (70, 8, 20)])
+def test_row_offsets_that_fall(H, n_seqs, per, new):
+    """Attention leaves all rows as they were."""
+    gen = torch.Generator().manual_seed(n_seqs)
+    lens = [600] + [40] * (n_seqs - 1)
+    cache, table, free = filled(H, F, 4, 64, 32, 16, 2, lens, gen, extra_pages=2)
+    cu = cumulated([new] * n_seqs)
+    q = torch.randn(cu[-1], 2 * per, 64, generator=gen).half().cuda()
+    cu[n_seqs // 2] = cu[-1]
+    for prefix in (0, 20):
+        out = torch.full_like(q, 5.0)
+        H.hqq_cache_attention_prefix(cache, i32(table), i32(lens), i32(free[:2]), prefix, q, out, cu_tokens=i32(cu))
+        assert (out == 5).all()
+
+
+def test_captured_prefix_steps(H):
+    """Many rows and a prefix in a graph, lengths and row offsets changing between replays."""
+    gen = torch.Generator().manual_seed(21)
+    page, dim, kv, per, cap, n = 16, 128, 2, 4, [200, 900, 30], 90
+    cache, table, free = filled(H, B, 4, dim, 64, page, kv, cap, gen, extra_pages=20)
+    pages, prefix = free[:20], 315
+    H.hqq_cache_write(cache, i32([pages]), i32([prefix]), values(prefix, kv, dim, B, gen), values(prefix, kv, dim, B, gen))
+    t, pp, lens, cu = i32(table), i32(pages), i32([200, 900, 30]), i32([0, 30, 60, 90])
+    q = values(n, kv * per, dim, B, gen)
+    out, lse = torch.empty_like(q), torch.empty(n, kv * per, dtype=torch.float32, device="cuda")
+    ws = torch.empty(H.hqq_cache_attention_workspace(cache, t, lens, n, kv * per, prefix), dtype=torch.uint8, device="cuda")
+
+    def step():
+        H.hqq_cache_attention_prefix(cache, t, lens, pp, prefix, q, out, lse=lse, cu_tokens=cu, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    held = R.Held(cache)
+    for ln, rows in (([200, 900, 30], [0, 30, 60, 90]), ([1, 33, 0], [0, 1, 89, 90]), ([150, 899, 30], [0, 0, 90, 90]),
+                     ([200, 640, 7], [5, 20, 20, 80])):
+        lens.copy_(i32(ln))
+        cu.copy_(i32(rows))
+        q.copy_(values(*q.shape, B, gen))
+        out.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        mine = torch.tensor([rows[0] <= i < rows[-1] for i in range(n)])
+        R.check_attention(out, lse, R.attention(held, table, ln, rows, q, dim ** -0.5, pages, prefix), mine)
+        assert (out.cpu()[~mine] == 3).all()
+        eager = torch.full_like(q, 3.0)
+        H.hqq_cache_attention_prefix(cache, t, lens, pp, prefix, q, eager, cu_tokens=cu)
+        assert torch.equal(eager, out)
+
+
+def test_rows_of_any_stride(H):
+    """One query row for all tokens (stride 0), heads before tokens, and a workspace elsewhere."""
+    gen = torch.Generator().manual_seed(22)
+    lens = [700, 130]
+    cache, table, _ = filled(H, F, 8, 64, 64, 32, 2, lens, gen)
+    t, ln = i32(table), i32(lens)
+    one = torch.randn(1, 6, 64, generator=gen).half().cuda()
+    q = one.expand(40, 6, 64)
+    out = torch.empty(6, 40, 64, dtype=F, device="cuda").transpose(0, 1)
+    H.hqq_cache_attention(cache, t, ln, q, out)
+    R.check_attention(out, None, R.attention(R.Held(cache), table, lens, None, q, 0.125), torch.ones(40, dtype=torch.bool))
+    need = H.hqq_cache_attention_workspace(cache, t, ln, 40, 6)
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(H.HQQError):
+            H.hqq_cache_attention(cache, t, ln, q, out, workspace=ws)
