@@ -55,6 +55,36 @@ __device__ __forceinline__ float row_lane(float x)
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + N, 0xf, 0xf, true));
 }
 
+// acc[r] += lane N[r] of each row of 16 lanes of k[r], times x[r]: the broadcast is part of the
+// instruction, which the compiler makes of a product alone. What it would keep apart for its own
+// instructions is kept apart here: two wait states behind whatever wrote k and x, and `settled`,
+// which reads the matrix products that x or acc come from and so comes after their last.
+template <int N0, int N1, int N2, int N3>
+__device__ __forceinline__ void add_row_lanes(float (&acc)[4], const float (&k)[4], const float (&x)[4], uint32_t settled)
+{
+    asm("s_nop 1\n"
+        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %1, %5, %9 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %2, %6, %10 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %3, %7, %11 row_newbcast:%16 row_mask:0xf bank_mask:0xf"
+        : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3])
+        : "v"(k[0]), "v"(k[1]), "v"(k[2]), "v"(k[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(settled),
+          "n"(N0), "n"(N1), "n"(N2), "n"(N3));
+}
+// The same into one number.
+template <int N0, int N1, int N2, int N3>
+__device__ __forceinline__ void add_row_lanes(float &acc, const float (&k)[4], const float (&x)[4])
+{
+    asm("s_nop 1\n"
+        "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n"
+        "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%12 row_mask:0xf bank_mask:0xf"
+        : "+v"(acc)
+        : "v"(k[0]), "v"(k[1]), "v"(k[2]), "v"(k[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]),
+          "n"(N0), "n"(N1), "n"(N2), "n"(N3));
+}
+
 // Two whole numbers 0..15 in neighbouring bytes (pair HI: bytes 2, 3) as two values of the
 // type. A byte 0..15 read as e4m3 is that number of 2^-9: subnormal up to 7, and with
 // exponent field 1 from 8 on, which has the same spacing.
@@ -546,22 +576,35 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
             }
         }
         if constexpr (half.value == 1) after_keys();
-        static_for<4>([&](auto r) {
-            constexpr int i = 4 * half.value + r.value;
+        uint32_t settled = 0;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) s[t][i] = from[t][r.value];
+        for (int t = 0; t < RT; ++t) {
+            settled |= __float_as_uint(from[t][3]);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) settled |= __float_as_uint(acc[t][g][3]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float sum[4] = {from[t][0], from[t][1], from[t][2], from[t][3]};
             static_for<kGroups>([&](auto g) {
-                constexpr int at = r.value * kGroups + g.value;
-                const float step = row_lane<at % 16>(kgrid[at / 16][0]);
+                constexpr int at0 = g.value, at1 = at0 + kGroups, at2 = at1 + kGroups, at3 = at2 + kGroups;
+                auto grids = [&](int e, float (&k)[4]) {
+                    k[0] = kgrid[at0 / 16][e], k[1] = kgrid[at1 / 16][e], k[2] = kgrid[at2 / 16][e], k[3] = kgrid[at3 / 16][e];
+                };
+                float k[4];
                 if constexpr (!BASE_FRAGS) {
-                    const float b = row_lane<at % 16>(kgrid[at / 16][1]);
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) s[t][i] = fmaf(b, w.qsum[t][g.value], s[t][i]);
+                    const float q = w.qsum[t][g.value], all[4] = {q, q, q, q};
+                    grids(1, k);
+                    add_row_lanes<at0 % 16, at1 % 16, at2 % 16, at3 % 16>(sum, k, all, settled);
                 }
-#pragma unroll
-                for (int t = 0; t < RT; ++t) s[t][i] = fmaf(step, acc[t][g.value][r.value], s[t][i]);
+                const f32x4 x = acc[t][g.value];
+                const float each[4] = {x[0], x[1], x[2], x[3]};
+                grids(0, k);
+                add_row_lanes<at0 % 16, at1 % 16, at2 % 16, at3 % 16>(sum, k, each, settled);
             });
-        });
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[t][4 * half.value + r] = sum[r];
+        }
     });
     if (!open) {
         int first = t0 + 4 * quad;
@@ -648,14 +691,14 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
         u32x4 pf[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            static_for<4>([&](auto i) {
-                constexpr int half = i.value / 2, r = i.value % 2 * 2;
-                constexpr int at = r * kGroups + g.value, at1 = at + kGroups;
-                const float x = s[t][2 * i.value], y = s[t][2 * i.value + 1];
-                w.bsum[t][g.value] = fmaf(row_lane<at % 16>(vgrid[half][at / 16][1]), x, w.bsum[t][g.value]);
-                w.bsum[t][g.value] = fmaf(row_lane<at1 % 16>(vgrid[half][at1 / 16][1]), y, w.bsum[t][g.value]);
-                pf[t][i.value] = round_pair(row_lane<at % 16>(vgrid[half][at / 16][0]) * x,
-                                            row_lane<at1 % 16>(vgrid[half][at1 / 16][0]) * y);
+            static_for<2>([&](auto half) {
+                constexpr int at0 = g.value, at1 = at0 + kGroups, at2 = at1 + kGroups, at3 = at2 + kGroups;
+                const f32x2(&v)[kRegs] = vgrid[half.value];
+                const float k[4] = {v[at0 / 16][1], v[at1 / 16][1], v[at2 / 16][1], v[at3 / 16][1]};
+                const float x[4] = {s[t][4 * half.value], s[t][4 * half.value + 1], s[t][4 * half.value + 2], s[t][4 * half.value + 3]};
+                add_row_lanes<at0 % 16, at1 % 16, at2 % 16, at3 % 16>(w.bsum[t][g.value], k, x);
+                pf[t][2 * half.value] = round_pair(row_lane<at0 % 16>(v[at0 / 16][0]) * x[0], row_lane<at1 % 16>(v[at1 / 16][0]) * x[1]);
+                pf[t][2 * half.value + 1] = round_pair(row_lane<at2 % 16>(v[at2 / 16][0]) * x[2], row_lane<at3 % 16>(v[at3 / 16][0]) * x[3]);
             });
         }
 #pragma unroll
