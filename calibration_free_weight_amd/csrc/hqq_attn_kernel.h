@@ -265,7 +265,8 @@ struct Item {
 // The units of a side, end to end. Up to 64 sequences each wave has them in its lanes, and
 // nothing waits for another; more are summed up in LDS. Where runs would be short, units are
 // made longer until there is one to a run: a run that ends one item and begins another pays
-// for its start and its end twice, which is as much as several steps.
+// for its start and its end twice, which is as much as several steps (16 sequences of 800 to 2900
+// tokens with 5 new ones each: 36 us, 40 with units of 128).
 constexpr int kShortRun = 6;    // units
 
 template <int ROWS, int WAVES>
@@ -896,7 +897,12 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
 
 // ---- few rows: the cache is read, and little else ------------------------------------------
 // Each wave takes 32 tokens of every 128 for all of the tile's rows, straight from memory into
-// its products: no barrier but at an item's end.
+// its products: no barrier but at an item's end. Codes and grids are read once and in whole lines;
+// a step's 400 instructions to widen and weigh them take about as long as its bytes (4 bits,
+// heads of 128), which is why grids are applied to sums and not to codes. 64 sequences of 4100 to
+// 8190 tokens, 8 heads of 128, 4 bits, 458 MB: 95 us, 4.8 TB/s (a copy reaches 5.1); 131071 tokens
+// of 8 bits, 277 MB: 45 us, 6.1 TB/s; 300 tokens of 32 heads: 9.6 us, four loads that wait for
+// each other (lengths, pages, codes, and the instructions themselves) and three steps.
 template <typename T, int NB, int D, int G, int RT>
 __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4 : 3) : 2) void attn_kernel(AttnArgs a)
 {
@@ -1005,7 +1011,15 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
 // (heads of up to 128), the next step's are made in the other half, so that one barrier a step
 // is enough; the codes of the step after that are on their way meanwhile. Eight waves of 16
 // rows rather than four of 32: four waves to a SIMD hide each other's waits better than two
-// that share a broadcast grid between twice the rows.
+// that share a broadcast grid between twice the rows (84 and 87 us for the second case below).
+//
+// It is bound by the instructions beside the products: a wave's step of 16 rows and 32 tokens of
+// heads of 128 in two groups has 18 products of 16 cycles and about 115 vector instructions of 4
+// (grids, exponentials, the rounding of weights), and its share of the widening 40 more. 2 x 500
+// rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 173 us, 414 TFLOP/s; 64 x 8 rows a head
+// over 16390 tokens, 8 heads: 83 us, 414 TFLOP/s, of them 16 before the first product and behind
+// the last, for 33 MB of pieces. Counters of the latter, before its last step: vector
+// instructions 70% of the time, LDS 36%, products 22%.
 constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;
 
 template <int D, int G>

@@ -137,8 +137,11 @@ __device__ __forceinline__ uint32_t step_bits(float lo, float hi, int top)
 }
 
 // ---- write ------------------------------------------------------------------------------------
-// Bound by the arithmetic as much as by memory: about 100 instructions for a lane's eight
-// values, of 24 bytes in and out with 4 bits. Codes are decided exactly: the quotient, by a
+// Bound by memory and the arithmetic together: 18060 tokens of 32 heads of 128 in 4 bits, 379 MB,
+// take 89 to 105 us (4.2 to 3.6 TB/s) where their bytes alone take 74 at a copy's rate, with about
+// 100 instructions for a lane's eight values of 24 bytes in and out. A token of 8 heads takes
+// 3.3 us, the launch and three loads that wait for each other.
+// Codes are decided exactly: the quotient, by a
 // product with the reciprocal's estimate, errs by at most 2^(nbits - 22), so only within twice
 // that of a half is it held against the midpoint, again without rounding: (2k + 1) * step has
 // at most 9 + 11 bits and lies next to twice the difference. With binary16 one value in some
@@ -250,6 +253,8 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheView c, SeqV
 }
 
 // ---- read -------------------------------------------------------------------------------------
+// Bound by memory: 65521 tokens of 8 heads of 128 in 8 bits, 407 MB, take 78 us (5.2 TB/s, a
+// copy's rate). All of a lane's loads are asked for before the first is used, whatever the page.
 template <typename T>
 __device__ __forceinline__ uint4 values8(const float (&q)[8], uint32_t meta)
 {
@@ -327,7 +332,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheView c, SeqVi
 template <typename T, int NB, int D, int G, int HEADS>
 void launch_heads(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)cache_rows_blocks(s.n_tokens, c.heads, D));
+    const dim3 grid((unsigned)cache_rows_blocks(write, s.n_tokens, c.heads, D));
     if (write) cache_write_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
     else cache_read_kernel<T, NB, D, G, HEADS><<<grid, kThreads, 0, stream>>>(c, s, p);
 }
@@ -335,8 +340,7 @@ void launch_heads(bool write, const CacheView &c, const SeqView &s, const RowPtr
 template <typename T, int NB, int D, int G>
 hipError_t launch(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p, hipStream_t stream)
 {
-    // four heads to a wave, unless that leaves the GPU's 1024 units without a few waves each
-    if (four_heads(s.n_tokens, c.heads, D)) launch_heads<T, NB, D, G, 4>(write, c, s, p, stream);
+    if (four_heads(write, s.n_tokens, c.heads, D)) launch_heads<T, NB, D, G, 4>(write, c, s, p, stream);
     else launch_heads<T, NB, D, G, 1>(write, c, s, p, stream);
     return hipGetLastError();
 }

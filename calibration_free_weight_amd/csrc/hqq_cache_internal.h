@@ -80,13 +80,20 @@ __device__ __forceinline__ int find_seq(const SeqView &s, int i)
     return lo;
 }
 
-// A block of a write or read has 256 * 8 / head_dim tokens of four heads at a time, or of one
-// where the call has less than 2^23 numbers.
+// A block of a write or read has 256 * 8 / head_dim tokens of four heads at a time, whose loads
+// are then under way together, or of one where four would leave the GPU's 1024 units without a
+// few waves each: from 2^23 numbers on for a write (8 heads of 128, 4 bits: 4096 tokens 9.4 us
+// with four and 8.1 with one, 16384 tokens both 25; 18060 tokens of 32 heads 89 and 110), 2^22
+// for a read (8 heads of 128, 8 bits: 2000 tokens 4.6 and 4.7, 6000 tokens 7.9 and 9.2, 65521
+// tokens 80 and 98; of 64, 4 bits: 4000 tokens 5.5 and 4.7, 12000 tokens 8.5 and 8.9).
 constexpr int kRowThreads = 256;
-inline bool four_heads(int64_t n_tokens, int heads, int dim) { return n_tokens * heads * dim >= int64_t(1) << 23; }
-inline int64_t cache_rows_blocks(int64_t n_tokens, int heads, int dim)
+inline bool four_heads(bool write, int64_t n_tokens, int heads, int dim)
 {
-    const int tokens = 8 * kRowThreads / dim, at_once = four_heads(n_tokens, heads, dim) ? 4 : 1;
+    return n_tokens * heads * dim >= int64_t(1) << (write ? 23 : 22);
+}
+inline int64_t cache_rows_blocks(bool write, int64_t n_tokens, int heads, int dim)
+{
+    const int tokens = 8 * kRowThreads / dim, at_once = four_heads(write, n_tokens, heads, dim) ? 4 : 1;
     return (n_tokens + tokens - 1) / tokens * ((heads + at_once - 1) / at_once);
 }
 
