@@ -1018,8 +1018,8 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
 // (grids, exponentials, the rounding of weights), and its share of the widening 40 more. 2 x 500
 // rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 173 us, 414 TFLOP/s; 64 x 8 rows a head
 // over 16390 tokens, 8 heads: 83 us, 414 TFLOP/s, of them 16 before the first product and behind
-// the last, for 33 MB of pieces. Counters of the latter, before its last step: vector
-// instructions 70% of the time, LDS 36%, products 22%.
+// the last, for 33 MB of pieces. Counters of the latter: vector instructions 66% of the time, LDS
+// 38%, products 23%; a wave waits 42% of its time for loads and for the block's other waves.
 constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;
 
 template <int D, int G>
