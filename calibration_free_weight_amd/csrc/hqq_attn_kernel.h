@@ -278,7 +278,7 @@ struct Layout {
     int len;
     bool falls;
     int32_t *starts, *scan;     // in LDS, with more: [n_seqs + 1], [WAVES]
-    __device__ __forceinline__ bool few() const { return d.s.n_seqs <= 64; }
+    __device__ __forceinline__ bool few() const { return __builtin_expect(d.s.n_seqs <= 64, 1); }
     __device__ __forceinline__ int units(const Rows &r, int len) const
     {
         return tiles_of((r.end - r.begin) * per, ROWS) * units_along(len, unit);
@@ -344,7 +344,7 @@ struct Layout {
         if (few()) read();
         total = count(start, false);
         const int longest = d.s.fixed_len >= 0 ? d.s.fixed_len : d.s.max_pages << d.s.page_shift;
-        if (total > d.workers && total <= kShortRun * d.workers && unit < longest) {
+        if (__builtin_expect(total > d.workers && total <= kShortRun * d.workers && unit < longest, 0)) {
             const int times = (total + d.workers - 1) / d.workers, first = unit;
             // two tries: rounding up by sequence may leave more units than runs
             for (int more = 0; more < 2; ++more) {
@@ -549,7 +549,7 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
     constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
     const int quad = (threadIdx.x & 63) >> 4;
     const bool open = t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
-    if (!open) close();
+    if (__builtin_expect(!open, 0)) close();
     float s[RT][8];
     static_for<2>([&](auto half) {
         f32x4 acc[RT][kGroups], from[RT];
@@ -607,7 +607,7 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
             for (int r = 0; r < 4; ++r) s[t][4 * half.value + r] = sum[r];
         }
     });
-    if (!open) {
+    if (__builtin_expect(!open, 0)) {
         int first = t0 + 4 * quad;
         asm volatile("" : "+v"(first));                     // a branch, not a choice in every step
 #pragma unroll
@@ -626,7 +626,7 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
                          larger3(s[t][5], s[t][6], s[t][7]), s[t][7]);
         grown = grown || top[t] > w.above[t];
     }
-    if (__any(grown)) {
+    if (__builtin_expect(__any(grown), 0)) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             top[t] = fmaxf(top[t], __shfl_xor(top[t], 16));
@@ -655,14 +655,14 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
             vgrid[half][k] = value_grid(half, k);
             most = fmaxf(most, vgrid[half][k][0]);
         }
-    if (!open) {        // a group that held infinities or NaN, and a weight of 0
+    if (__builtin_expect(!open, 0)) {       // a group that held infinities or NaN, and a weight of 0
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int k = 0; k < kRegs; ++k)
                 if (!(fabsf(vgrid[half][k][1]) < INFINITY)) vgrid[half][k][1] = 0.f;
     }
-    if (__any(most >= w.step_lim && most > 0.f)) {
+    if (__builtin_expect(__any(most >= w.step_lim && most > 0.f), 0)) {
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
         // the power of two at or below it
