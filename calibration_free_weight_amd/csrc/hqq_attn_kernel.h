@@ -1212,12 +1212,11 @@ hipError_t launch_many(const AttnArgs &a, hipStream_t stream)
 template <typename T, int NB, int D, int G>
 hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
-    // rows to a tile: 16 to 128, or to 64 for 256-wide heads (whose sums fill the registers)
+    // rows to a tile: 16, 32 or 128, and 16, 32 or 64 of 256-wide heads (whose sums fill the registers)
     const int n = a.side[0].tiles16;
     if (n == 1) return launch_few<T, NB, D, G, 1>(a, stream);
     if constexpr (D <= 128) {
         if (n == 2) return launch_few<T, NB, D, G, 2>(a, stream);
-        if (n == 4) return launch_many<T, NB, D, G, 2>(a, stream);
         if (n == 8) return launch_many<T, NB, D, G, 1>(a, stream);
     } else {
         if (n == 2) return launch_many<T, NB, D, G, 2>(a, stream);

@@ -126,18 +126,6 @@ struct Plan {
     size_t bytes;
 };
 
-// Query rows to a tile, in 16s: 16 where a sequence has no more, for its work is to read the
-// cache; else as many as its rows fill, up to 128 (64 for 256-wide heads, whose sums fill the
-// registers): the more rows, the fewer times codes are widened (512 rows over 16390 tokens, 8
-// heads of 128: 86 us in tiles of 128, 97 in tiles of 64).
-int tiles_for(int64_t rows, int dim)
-{
-    const int most = dim == 256 ? 4 : 8;
-    int t = 1;
-    while (t < most && 16 * t < rows) t *= 2;
-    return t;
-}
-
 // Blocks of a launch that a CU holds, by the registers that the kernels' sums and codes in
 // flight take (their launch bounds say the same). A launch has no more: with 1152 or 1536 blocks
 // rather than 1024 the last ones begin when the first are done, and take longer in all.
@@ -151,6 +139,40 @@ int resident(int tiles16, int dim, int nbits)
 // joining the pieces costs a launch (sequences of 100 to 500 tokens, 64 of them: 12.0 us whole,
 // 19.3 cut; one of 1000: 13.3 whole, 10.9 cut).
 constexpr int64_t kWhole = 512;
+
+// Query rows to a tile, in 16s, for `rows` rows of one head in n_seqs sequences of up to
+// `longest` tokens. More rows to a tile widen the codes fewer times, and take longer for a step:
+// where runs are short, smaller tiles on more of the GPU win. Measured in us with 8 heads of 128
+// in 4 bits, tiles of 16, 32 and 128 rows:
+//   500 rows x 4 over 500 tokens      18    19    31
+//   16 x 4 over 4000                  20    22    -
+//   8 x 64 x 4 over 2000              54    48    62
+//   500 x 4 over 4000                 89    80    82
+//   8 x 250 x 4 over 2000             189   156   128
+// and with 4 heads of 256, tiles of 16, 32 and 64 rows:
+//   16 x 5 x 4 over 800 to 2900       33    36    40
+//   64 x 5 x 4 over 4000              184   146   180
+//   500 x 4 over 500                  21    29    41
+//   8 x 250 x 4 over 2000             192   185   148
+// The limits are units of 128 tokens of 16 rows, to a run. (Tiles of 64 rows of heads of up to
+// 128 were between the others or behind both, and are not there.)
+int tiles_for(int64_t rows, int n_seqs, int64_t longest, const hqq_cache *c)
+{
+    const int64_t each = (rows + n_seqs - 1) / n_seqs, few = (each + 15) / 16;
+    if (few == 1) return 1;
+    const int64_t units = few * n_seqs * ((longest + hqq::kStep - 1) / hqq::kStep);
+    const int64_t blocks = 256 * resident(1, c->head_dim, c->nbits), runs = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
+    if (c->head_dim == 256) {
+        // the first limit is of one tile of 32 for a sequence: smaller ones read the cache twice
+        if (units <= (few == 2 ? 6 : 31) * runs) return 1;
+        return few == 2 ? 2 : 4;
+    }
+    // sequences that are not cut are spread the better the more tiles there are
+    if (units <= (longest <= kWhole ? 8 : 3) * runs) return 1;
+    if (units <= 30 * runs) return 2;
+    // what a step of a tile of 128 rows takes, to one of 32: 29 to 8
+    return (each + 127) / 128 * 29 < (each + 31) / 32 * 8 ? 8 : 2;
+}
 
 Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefix_len)
 {
@@ -187,9 +209,9 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         }
     };
     const int64_t longest = (int64_t)s->max_pages * c->page_size;
-    p.own = cut(tiles_for((rows + s->n_seqs - 1) / s->n_seqs, c->head_dim), s->n_seqs, longest);
+    p.own = cut(tiles_for(rows, s->n_seqs, longest, c), s->n_seqs, longest);
     if (prefix_len > 0) {
-        p.prefix = cut(tiles_for(rows, c->head_dim), 1, prefix_len);
+        p.prefix = cut(tiles_for(rows, 1, prefix_len, c), 1, prefix_len);
         // Short sequences behind a prefix go in its launch, in its larger tiles, while the GPU
         // holds the blocks of both: few steps in mostly empty tiles beside the prefix's cost
         // less than a launch of their own (25 sequences of a token, 16 heads of 256, a prefix of

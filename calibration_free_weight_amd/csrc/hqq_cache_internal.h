@@ -116,7 +116,7 @@ struct AttnSide {
     float *row_o, *row_ml;      // [heads][n_tokens * per][dim], [..][2], or null
     int32_t workers;            // most runs of a head's units
     int32_t unit;               // tokens, at least
-    int32_t tiles16;            // rows_per / 16: 1, 2, 4 or 8
+    int32_t tiles16;            // rows_per / 16: 1, 2 or 8, and 1, 2 or 4 with heads of 256
     int32_t causal;             // rows see their own position and what is before it, else all
 };
 

@@ -541,6 +541,17 @@ MANY = [
     (B, 8, 128, 128, 64, 1, 1, [5] * 80 + [1200], [1] * 81),
     (F, 4, 128, 64, 4096, 1, 2, [4099, 9], [130, 9]),
     (B, 4, 128, 64, 16, 4, 4, [1300, 1000, 600], [1, 1, 1]),
+    # enough heads that tiles of 128 rows are taken
+    (F, 4, 128, 64, 16, 128, 1, [1500, 300, 2000], [130, 100, 140]),
+    (B, 4, 64, 32, 32, 256, 2, [1300, 1200], [60, 60]),
+    (B, 8, 128, 32, 16, 128, 1, [900, 700, 900, 500], [120, 140, 97, 120]),
+    (F, 8, 64, 64, 16, 256, 1, [1000, 240], [200, 40]),
+    (F, 4, 128, 128, 64, 128, 1, [2000, 1990], [110, 128]),
+    (F, 8, 128, 32, 16, 32, 10, [990] * 5, [50] * 5),
+    # and for heads of 256, of 64 and 32
+    (F, 4, 256, 64, 16, 256, 1, [600, 560, 300], [100, 60, 130]),
+    (B, 8, 256, 128, 32, 256, 1, [700, 600], [20, 30]),
+    (F, 8, 256, 32, 16, 256, 2, [600, 580], [15, 12]),
 ]
 
 
@@ -549,12 +560,12 @@ def test_many_rows_bad_pages_and_far_bases(H, dtype, nbits, dim, group, page, kv
     """Keys far from zero (their scores are mostly the bases' part), pages that are not there in
     the middle of sequences, NaN in all that is not written; with a prefix of such pages too."""
     gen = torch.Generator().manual_seed(dim + nbits + len(lens))
-    table, n_pages, free = layout(lens, page, gen, spare=8)
+    table, n_pages, free = layout(lens, page, gen, spare=8 if kv < 128 else 100)
     cache = poison(H.alloc_cache(n_pages, page, kv, dim, nbits, group, dtype))
     cu = cumulated(lens)
     far = values(cu[-1], kv, dim, dtype, gen) + 30 * torch.randn(kv, dim, generator=gen).to(dtype).cuda()
     H.hqq_cache_write(cache, i32(table), i32(lens), far, values(cu[-1], kv, dim, dtype, gen), cu_tokens=i32(cu))
-    prefix = 3 * page + 5 if page < 1000 else 600
+    prefix = 600 if page > 1000 else 3 * page + 5 if kv < 128 else 1500
     pages = free[:-(-prefix // page)]
     H.hqq_cache_write(cache, i32([pages]), i32([prefix]), values(prefix, kv, dim, dtype, gen), values(prefix, kv, dim, dtype, gen))
     for b in range(0, len(lens), 2):
@@ -573,26 +584,26 @@ def test_many_rows_bad_pages_and_far_bases(H, dtype, nbits, dim, group, page, kv
     R.check_attention(out, lse, R.attention(held, table, lens, cu, q, scale, pages, prefix), every)
 
 
-@pytest.mark.parametrize("dtype,nbits,dim,group,per,new", [
-    (F, 4, 128, 64, 1, 7), (B, 8, 128, 32, 4, 8), (F, 8, 128, 128, 4, 30), (B, 4, 64, 32, 2, 60),
-    (F, 4, 256, 32, 1, 9), (B, 8, 256, 64, 8, 12)])
-def test_values_that_are_not_finite_are_not_seen_before_they_come(H, dtype, nbits, dim, group, per, new):
+@pytest.mark.parametrize("dtype,nbits,dim,group,heads,per,new,n", [
+    (F, 4, 128, 64, 1, 1, 7, 250), (B, 8, 128, 32, 1, 4, 8, 250), (F, 8, 128, 128, 1, 4, 30, 250), (B, 4, 64, 32, 1, 2, 60, 250),
+    (F, 4, 256, 32, 1, 1, 9, 250), (B, 8, 256, 64, 1, 8, 12, 250), (F, 4, 64, 32, 1024, 1, 128, 500),
+    (B, 8, 128, 64, 1024, 1, 128, 500), (F, 4, 256, 64, 1024, 1, 60, 1000)])
+def test_values_that_are_not_finite_are_not_seen_before_they_come(H, dtype, nbits, dim, group, heads, per, new, n):
     """Rows before a token with NaN or an infinity in its key or value give what they give
     without it; rows from it on see NaN in the value's group at most, or in all with the key's."""
     gen = torch.Generator().manual_seed(dim + new)
-    n = 250
     table, n_pages, _ = layout([n], 16, gen)
-    k, v = values(n, 1, dim, dtype, gen), values(n, 1, dim, dtype, gen)
-    q = torch.randn(new, per, dim, generator=gen).to(dtype).cuda()
-    clean = poison(H.alloc_cache(n_pages, 16, 1, dim, nbits, group, dtype))
+    k, v = values(n, heads, dim, dtype, gen), values(n, heads, dim, dtype, gen)
+    q = torch.randn(new, heads * per, dim, generator=gen).to(dtype).cuda()
+    clean = poison(H.alloc_cache(n_pages, 16, heads, dim, nbits, group, dtype))
     H.hqq_cache_write(clean, i32(table), i32([n]), k, v)
     ref = R.attention(R.Held(clean), table, [n], None, q, dim ** -0.5)
     at = n - 3                          # the last three rows see it
     for bad in (math.nan, math.inf, -math.inf):
         for which in (0, 1):
             kv = [k.clone(), v.clone()]
-            kv[which][at, 0, 3] = bad
-            cache = poison(H.alloc_cache(n_pages, 16, 1, dim, nbits, group, dtype))
+            kv[which][at, :, 3] = bad
+            cache = poison(H.alloc_cache(n_pages, 16, heads, dim, nbits, group, dtype))
             H.hqq_cache_write(cache, i32(table), i32([n]), *kv)
             out = H.cache_attention(cache, i32(table), i32([n]), q)
             before = torch.arange(new) < new - 3
