@@ -33,7 +33,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
-constexpr int kWaves = 4;                   // of a block for few rows
+constexpr int kWaves = 4;                   // of a block for tiles of few rows
 constexpr int kTile = 32;                   // tokens of a wave's step
 static_assert(kTile * kWaves == kStep, "a step is a tile for each wave");
 
@@ -266,7 +266,7 @@ struct Item {
 // nothing waits for another; more are summed up in LDS. Where runs would be short, units are
 // made longer until there is one to a run: a run that ends one item and begins another pays
 // for its start and its end twice, which is as much as several steps (16 sequences of 800 to 2900
-// tokens with 5 new ones each: 36 us, 40 with units of 128).
+// tokens with 5 new ones each, in tiles of 32 rows of heads of 256: 36 us, 40 with units of 128).
 constexpr int kShortRun = 6;    // units
 
 template <int ROWS, int WAVES>
@@ -895,12 +895,13 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
     return Place{second ? a.side[1] : a.side[0], (int)(block - run * a.c.heads), (int)run, block == 0};
 }
 
-// ---- few rows: the cache is read, and little else ------------------------------------------
+// ---- few rows, or little work: the cache is read, and little else ---------------------------
 // Each wave takes 32 tokens of every 128 for all of the tile's rows, straight from memory into
-// its products: no barrier but at an item's end. Codes and grids are read once and in whole lines;
+// its products: no barrier but at an item's end, and a step of a third of the latency of the form
+// below, which is why it takes many rows too while there is little work for each block. Codes and grids are read once and in whole lines;
 // a step's 400 instructions to widen and weigh them take about as long as its bytes (4 bits,
 // heads of 128), which is why grids are applied to sums and not to codes. 64 sequences of 4100 to
-// 8190 tokens, 8 heads of 128, 4 bits, 458 MB: 95 us, 4.8 TB/s (a copy reaches 5.1); 131071 tokens
+// 8190 tokens, 8 heads of 128, 4 bits, 455 MB: 96 us, 4.7 TB/s (a copy reaches 5.1); 131071 tokens
 // of 8 bits, 277 MB: 45 us, 6.1 TB/s; 300 tokens of 32 heads: 9.6 us, four loads that wait for
 // each other (lengths, pages, codes, and the instructions themselves) and three steps.
 template <typename T, int NB, int D, int G, int RT>
@@ -1004,7 +1005,7 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
     }
 }
 
-// ---- many rows: the arithmetic bounds it ------------------------------------------------------
+// ---- many rows over much: the arithmetic bounds it -------------------------------------------
 // TW waves share each 16 rows and take turns at tiles of 32 tokens; all waves of the block meet
 // the same 64 tokens a step. Together they widen the step's codes into fragments and open its
 // grids, in LDS: that is paid once for the block's rows. Where LDS has room for two steps
@@ -1016,8 +1017,8 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
 // It is bound by the instructions beside the products: a wave's step of 16 rows and 32 tokens of
 // heads of 128 in two groups has 18 products of 16 cycles and about 115 vector instructions of 4
 // (grids, exponentials, the rounding of weights), and its share of the widening 40 more. 2 x 500
-// rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 173 us, 414 TFLOP/s; 64 x 8 rows a head
-// over 16390 tokens, 8 heads: 83 us, 414 TFLOP/s, of them 16 before the first product and behind
+// rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 171 us, 418 TFLOP/s; 64 x 8 rows a head
+// over 16390 tokens, 8 heads: 81 us, 427 TFLOP/s, of them 16 before the first product and behind
 // the last, for 33 MB of pieces. Counters of the latter: vector instructions 66% of the time, LDS
 // 38%, products 23%; a wave waits 42% of its time for loads and for the block's other waves.
 constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;

@@ -457,7 +457,7 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
     s = _seqs_struct(table, lens, cu_tokens, n, dev)
     qp, qt, qh = _rows(q, shape, dev, dtype, "q")
     if out is None:
-        out = T.empty(shape, dtype=dtype, device=dev)
+        out = T.empty_like(q)
     op, ot, oh = _rows(out, shape, dev, dtype, "out")
     if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
                             not lse.is_contiguous()):
