@@ -27,12 +27,21 @@ struct Floats {
     float x[E];
 } __attribute__((aligned(4 * E)));
 
-// Adds up to 64 pieces: lane k has the maximum m and sum l of piece k, whose output is at
-// o + off(k) * D. Of the row's WPR waves each adds every WPR-th piece's output.
+// Adds up to 64 pieces (one at least): lane k has the maximum m and sum l of piece k, whose output
+// is at o + off(k) * D. Of the row's WPR waves each adds every WPR-th piece's output; the first
+// outputs are asked for before the maxima are looked at, which are on their way as well.
 template <int E, int WPR, typename Off>
 __device__ __forceinline__ void add_pieces(Acc<E> &acc, int n, float m, float l, const float *o, Off off)
 {
     const int lane = threadIdx.x & 63, mine = (threadIdx.x >> 6) % WPR;
+    Floats<E> x[kAhead];
+    const auto load = [&](int k0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            x[j] = *reinterpret_cast<const Floats<E> *>(o + off(min(k0 + j * WPR, n - 1)) * (64 * E) + lane * E);
+    };
+    load(mine);
+    __builtin_amdgcn_sched_barrier(0);
     float top = m;
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
@@ -48,19 +57,14 @@ __device__ __forceinline__ void add_pieces(Acc<E> &acc, int n, float m, float l,
 #pragma unroll
     for (int e = 0; e < E; ++e) acc.o[e] *= g;
     for (int k0 = mine; k0 < n; k0 += kAhead * WPR) {
-        Floats<E> x[kAhead];
-        float fk[kAhead];
+        if (k0 != mine) load(k0);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int k = min(k0 + j * WPR, n - 1);
-            x[j] = *reinterpret_cast<const Floats<E> *>(o + off(k) * (64 * E) + lane * E);
-            fk[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), k));
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
+            const float fk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), min(k0 + j * WPR, n - 1)));
             if (k0 + j * WPR < n)
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc.o[e] = fmaf(fk[j], x[j].x[e], acc.o[e]);
+                for (int e = 0; e < E; ++e) acc.o[e] = fmaf(fk, x[j].x[e], acc.o[e]);
+        }
     }
 }
 
@@ -94,7 +98,7 @@ __device__ __forceinline__ bool add_side(Acc<E> &acc, const AttnSide &d, int b, 
 // WPR waves per query row: they find the pieces of its item on each side by the rule that
 // dealt them out, and add them on the largest of their maxima, in order: out = sum_i 2^(m_i - m)
 // o_i / sum_i 2^(m_i - m) l_i with m = max m_i. Bound by the launch and the latency of its loads:
-// 5.6 us for 320 rows of 3 to 9 pieces, 13.4 us for 4096 rows of 17 (36 MB, 2.7 TB/s).
+// 5.7 us for 320 rows of 3 to 9 pieces, 12.4 us for 4096 rows of 17 (36 MB, 2.9 TB/s).
 template <typename T, int D, int WPR>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(JoinArgs a)
 {
