@@ -142,7 +142,8 @@ def attention(held, table, lens, cu, q, scale, prefix_pages=(), prefix_len=0):
     output's own rounding:
 
     A score is a sum of dim exact products of a 16-bit number and a code, scaled: its error is
-    at most (dim + 8) 2^-24 of the sum of magnitudes S, so a weight's relative error is twice
+    at most (dim + 8) 2^-24 of the sum of magnitudes S (2 of the 8 for bases that enter as
+    products of bfloat16 parts, which leave out 2^-23 of theirs), so a weight's relative error is twice
     scale*S*(dim + 8)*2^-24, once more for the sum that divides, plus 2^-18 for exp2 (its
     argument below 2^6 in magnitude where it matters, and a unit in the last place). Sums over
     n tokens add n 2^-24 at most. All of it weighs on A = sum of p (|base| + q step).
