@@ -234,6 +234,26 @@ __device__ __forceinline__ void static_for(F &&f)
     }
 }
 
+// Largest and smallest over the lanes whose number leaves the same rest by N (1 to 8): rotations
+// within rows of 16 lanes, then over the rows.
+template <int N>
+__device__ __forceinline__ void over_same_group(float &most, float &least)
+{
+    const auto with = [&](float a, float b) {
+        most = fmaxf(most, a);
+        least = fminf(least, b);
+    };
+    const auto turned = [](float x, auto by) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + by.value, 0xf, 0xf, true));
+    };
+    with(turned(most, Index<8>{}), turned(least, Index<8>{}));
+    if constexpr (N <= 4) with(turned(most, Index<4>{}), turned(least, Index<4>{}));
+    if constexpr (N <= 2) with(turned(most, Index<2>{}), turned(least, Index<2>{}));
+    if constexpr (N <= 1) with(turned(most, Index<1>{}), turned(least, Index<1>{}));
+    with(__shfl_xor(most, 16), __shfl_xor(least, 16));
+    with(__shfl_xor(most, 32), __shfl_xor(least, 32));
+}
+
 // Sum over the four lanes of a column (16 and 32 apart).
 __device__ __forceinline__ float column_sum(float x)
 {
@@ -415,9 +435,17 @@ struct Layout {
 
 // How far a score may lie above the maximum that weights are taken from: weights reach 2^6.
 constexpr float kSlack = 6.f;
-// V's steps are scaled to below 2^9 (by a power of two that follows the largest seen), so that
-// weight times step stays below 2^15 in binary16 and precise down to 2^-29 of that.
-constexpr int kStepBits = 8;
+// V's steps go into the products times a power of two of the wave and group that brings them to 1
+// or more and below 2^9: weight times step then stays below 2^15 in binary16, and a weight keeps 11
+// bits or is off by 2^-25 at most, where a row's largest is at least 1. Tokens that do not fit in
+// are left out (of the codes' part) and come behind the others, in attend_rest, where every row and
+// group has a power of two of its own: however large a token's values, it has no say in rows that do
+// not see it or hardly weigh it.
+constexpr uint32_t kStepLow = 0x3f800000u, kStepHigh = 0x44000000u;     // bits of 1 and 2^9
+// The sums of products are in units of 1/by: by is at least 2^-40, at which they hold whatever V
+// can, and lose of the smallest numbers less than 2^-104 (a step of bfloat16 is 2^-100 or more);
+// above that, a product of 2^60 units or more first lowers it to 2^-40.
+constexpr float kLeastBy = 0x1p-40f, kMostUnits = 0x1p60f;
 
 // What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16). BASE_FRAGS: the
 // bases' part of the scores is a product too, see base_query.
@@ -433,7 +461,8 @@ struct Wave {
     // m: scores are taken from it; above: how far one may lie above before m moves (none
     // while m has not been set)
     float m[RT], above[RT], l[RT], bsum[RT][kGroups];
-    float step_lim, step_by;    // V's steps are below step_lim and multiplied by step_by
+    float by;                   // V's steps of group lane % kGroups go in times this; 0 before there are any
+    bool rest;                  // some of V's steps did not fit
 };
 
 // The bases' part of the scores as one product of bfloat16 parts: slot e of the contraction's
@@ -518,7 +547,8 @@ __device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnA
         w.above[t] = -INFINITY;
         w.l[t] = 0.f;
     }
-    w.step_lim = w.step_by = 0.f;
+    w.by = 0.f;
+    w.rest = false;
 }
 
 // The lanes' places for the grids of 16 tokens: quad x holds those of tokens 4x..4x+3, lane c
@@ -533,24 +563,25 @@ struct Places {
     }
 };
 
-// One step: 32 tokens from t0 for the wave's rows, good[half] of each 16 there (or more; none
-// if negative). When some are not, or not for all rows, close() is called first, to make the
-// grids of the missing ones {0, 0}. key_grid(half, k) gives {step * scale, base} of a lane's
-// place, value_grid {step, middle}; key(half, mm) and value(j) the A fragments. after_keys() is
-// called when no more keys are needed, before the values' grids and fragments are. With
-// BASE_FRAGS base(half, p) is the A fragment of the bases (base_query has the other), and what
-// key_grid says of them is not used.
-template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
-          typename After, typename ValueGrid, typename Value>
-__device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
-                                            Base base, Key key, After after_keys, ValueGrid value_grid, Value value)
+// Whether all of a step's 32 tokens from t0 are there, for all of the wave's rows.
+template <int D, int G, int RT, bool BASE_FRAGS>
+__device__ __forceinline__ bool all_there(const Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2])
+{
+    return t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
+}
+
+// The scores of 32 tokens from t0 for the wave's rows, to base 2 and less m, good[half] of each 16
+// there (or more; none if negative), -infinity where a row does not see one. key_grid(half, k)
+// gives {step * scale, base} of a lane's place; key(half, mm) the A fragments. after_keys() is
+// called when no more keys are needed. With BASE_FRAGS base(half, p) is the A fragment of the bases
+// (base_query has the other), and what key_grid says of them is not used.
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename KeyGrid, typename Base, typename Key, typename After>
+__device__ __forceinline__ void scores(const Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], bool open,
+                                       KeyGrid key_grid, Base base, Key key, After after_keys, float (&s)[RT][8])
 {
     constexpr bool kBf16 = Types<T>::kBf16;
     constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
     const int quad = (threadIdx.x & 63) >> 4;
-    const bool open = t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
-    if (__builtin_expect(!open, 0)) close();
-    float s[RT][8];
     static_for<2>([&](auto half) {
         f32x4 acc[RT][kGroups], from[RT];
         f32x2 kgrid[kRegs];
@@ -618,6 +649,59 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
                 if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
             }
     }
+}
+
+__device__ __forceinline__ uint32_t misfit(float step) { return __float_as_uint(step) - kStepLow; }    // kMisfit or more
+constexpr uint32_t kMisfit = kStepHigh - kStepLow;
+
+// A `by` for V's steps of a step that are not all 0 and, times the one that there is, do not all
+// fit. 2^8 to 2^9 for the largest, if the smallest is 1 or more then: taken at first, and when it is
+// lower than what there is. At first, if they do not fit, that for the smallest: large ones are
+// rarer. The same steps one after another give the same, in attend_rest again. each_step(f) calls
+// f with a lane's steps, one after another.
+template <int GROUPS, typename Each>
+__device__ __forceinline__ float fitting(float by, Each each_step)
+{
+    float most = 0.f, least = INFINITY;
+    each_step([&](float step) {
+        most = fmaxf(most, step);
+        least = fminf(least, step > 0.f ? step : INFINITY);
+    });
+    over_same_group<GROUPS>(most, least);
+    const auto by_of = [](float step) {
+        return fmaxf(0x1p8f / __uint_as_float(__float_as_uint(fmaxf(step, 0x1p-100f)) & 0x7f800000u), kLeastBy);
+    };
+    const float fit = by_of(most);
+    const bool fits = least * fit >= 1.f && most * fit < 0x1p9f;
+    if (by == 0.f) return !(most > 0.f) ? 0.f : fits ? fit : by_of(least);
+    return fits && fit < by ? fit : by;
+}
+
+// Of group g and four tokens, whose grids are v and the row's weights p: the weights times the steps.
+template <int GROUPS, int REGS, typename Group>
+__device__ __forceinline__ void weigh(Group g, const f32x2 (&v)[REGS], const float *p, float (&x)[4])
+{
+    constexpr int at0 = g.value, at1 = at0 + GROUPS, at2 = at1 + GROUPS, at3 = at2 + GROUPS;
+    x[0] = row_lane<at0 % 16>(v[at0 / 16][0]) * p[0];
+    x[1] = row_lane<at1 % 16>(v[at1 / 16][0]) * p[1];
+    x[2] = row_lane<at2 % 16>(v[at2 / 16][0]) * p[2];
+    x[3] = row_lane<at3 % 16>(v[at3 / 16][0]) * p[3];
+}
+
+// One step: 32 tokens from t0, good[half] of each 16 there. When some are not, or not for all rows,
+// close() is called first, to make the grids of the missing ones {0, 0}. value_grid gives {step,
+// middle} of a lane's place and value(j) the A fragments, behind after_keys(); the others are as in
+// scores().
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
+          typename After, typename ValueGrid, typename Value>
+__device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
+                                            Base base, Key key, After after_keys, ValueGrid value_grid, Value value)
+{
+    constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
+    const bool open = all_there(w, t0, good);
+    if (__builtin_expect(!open, 0)) close();
+    float s[RT][8];
+    scores<T>(w, t0, good, open, key_grid, base, key, after_keys, s);
     float top[RT];
     bool grown = false;
 #pragma unroll
@@ -647,38 +731,54 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
     }
 
     f32x2 vgrid[2][kRegs];
-    float most = 0.f;
+    uint32_t off = 0;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int k = 0; k < kRegs; ++k) {
             vgrid[half][k] = value_grid(half, k);
-            most = fmaxf(most, vgrid[half][k][0]);
+            vgrid[half][k][0] *= w.by;
+            off = max(off, misfit(vgrid[half][k][0]));
         }
-    if (__builtin_expect(!open, 0)) {       // a group that held infinities or NaN, and a weight of 0
+    if (__builtin_expect(!open, 0)) {
+        off = 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int k = 0; k < kRegs; ++k)
+            for (int k = 0; k < kRegs; ++k) {
+                // a group that held infinities or NaN, and a weight of 0
                 if (!(fabsf(vgrid[half][k][1]) < INFINITY)) vgrid[half][k][1] = 0.f;
+                if (value_grid(half, k)[0] != 0.f) off = max(off, misfit(vgrid[half][k][0]));
+            }
     }
-    if (__builtin_expect(__any(most >= w.step_lim && most > 0.f), 0)) {
+    if (__builtin_expect(__any(off >= kMisfit), 0)) {       // steps of 0 too, which are no matter
+        const float was = w.by;
+        w.by = fitting<kGroups>(was, [&](auto f) {
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
-        // the power of two at or below it
-        const float p2 = __uint_as_float(__float_as_uint(most) & 0x7f800000u);
-        const float by = ldexpf(1.f / p2, kStepBits), f = w.step_by > 0.f ? by / w.step_by : 1.f;
-        w.step_lim = 2.f * p2;
-        w.step_by = by;
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+                for (int k = 0; k < kRegs; ++k) f(value_grid(half, k)[0]);
+        });
+        const float f = was > 0.f ? w.by / was : 1.f;
+        static_for<kGroups>([&](auto g) {
+            const float fg = row_lane<g.value>(f);
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) w.o[t][j] *= f;
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= fg;
+        });
+        bool some = false;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k) {
+                const float step = value_grid(half, k)[0] * w.by;
+                const bool out = misfit(step) >= kMisfit;
+                some = some || (out && step != 0.f);
+                vgrid[half][k][0] = out ? 0.f : step;
+            }
+        w.rest = w.rest || __any(some);
     }
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int k = 0; k < kRegs; ++k) vgrid[half][k][0] *= w.step_by;
 
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -696,10 +796,12 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
                 constexpr int at0 = g.value, at1 = at0 + kGroups, at2 = at1 + kGroups, at3 = at2 + kGroups;
                 const f32x2(&v)[kRegs] = vgrid[half.value];
                 const float k[4] = {v[at0 / 16][1], v[at1 / 16][1], v[at2 / 16][1], v[at3 / 16][1]};
-                const float x[4] = {s[t][4 * half.value], s[t][4 * half.value + 1], s[t][4 * half.value + 2], s[t][4 * half.value + 3]};
-                add_row_lanes<at0 % 16, at1 % 16, at2 % 16, at3 % 16>(w.bsum[t][g.value], k, x);
-                pf[t][2 * half.value] = round_pair(row_lane<at0 % 16>(v[at0 / 16][0]) * x[0], row_lane<at1 % 16>(v[at1 / 16][0]) * x[1]);
-                pf[t][2 * half.value + 1] = round_pair(row_lane<at2 % 16>(v[at2 / 16][0]) * x[2], row_lane<at3 % 16>(v[at3 / 16][0]) * x[3]);
+                const float p[4] = {s[t][4 * half.value], s[t][4 * half.value + 1], s[t][4 * half.value + 2], s[t][4 * half.value + 3]};
+                add_row_lanes<at0 % 16, at1 % 16, at2 % 16, at3 % 16>(w.bsum[t][g.value], k, p);
+                float x[4];
+                weigh<kGroups>(g, v, p, x);
+                pf[t][2 * half.value] = round_pair(x[0], x[1]);
+                pf[t][2 * half.value + 1] = round_pair(x[2], x[3]);
             });
         }
 #pragma unroll
@@ -709,6 +811,102 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
 #pragma unroll
             for (int t = 0; t < RT; ++t) w.o[t][j] = mfma32<false>(vf, pf[t], w.o[t][j]);
         }
+    });
+}
+
+// What attend_step left out of 32 tokens, behind all steps of the item: the codes' part of the
+// tokens whose steps of V did not fit, `by` being what it was before this step then (0 before the
+// first). A row's weights go in times the power of two that brings the largest of its products in
+// the group to 2^14, and its sums in units of the same meanwhile (of more where they hold 2^100 of
+// these). The arguments are those of attend_step.
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
+          typename ValueGrid, typename Value>
+__device__ __forceinline__ void attend_rest(Wave<D, G, RT, BASE_FRAGS> &w, float &by, int t0, const int (&good)[2], Close close,
+                                            KeyGrid key_grid, Base base, Key key, ValueGrid value_grid, Value value)
+{
+    constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
+    const bool open = all_there(w, t0, good);
+    if (!open) close();
+    f32x2 vgrid[2][kRegs];
+    bool out = false, some = false;
+    const auto each = [&](auto f) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int k = 0; k < kRegs; ++k) f(value_grid(half, k)[0], vgrid[half][k]);
+    };
+    each([&](float step, f32x2 &) { out = out || (step != 0.f && misfit(step * by) >= kMisfit); });
+    if (!__any(out)) return;
+    by = fitting<kGroups>(by, [&](auto f) { each([&](float step, f32x2 &) { f(step); }); });
+    each([&](float step, f32x2 &v) {
+        const bool left = step != 0.f && misfit(step * by) >= kMisfit;
+        some = some || left;
+        v = f32x2{left ? step : 0.f, 0.f};
+    });
+    if (!__any(some)) return;
+    float s[RT][8];
+    scores<T>(w, t0, good, open, key_grid, base, key, [] {}, s);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
+    static_for<kGroups>([&](auto g) {
+        u32x4 pf[RT];
+        float largest[RT], unit[RT], of_group = row_lane<g.value>(w.by);
+        bool many = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            largest[t] = 0x1p-100f;
+            static_for<2>([&](auto half) {
+                float x[4];
+                weigh<kGroups>(g, vgrid[half.value], s[t] + 4 * half.value, x);
+                largest[t] = larger3(larger3(largest[t], x[0], x[1]), x[2], x[3]);
+            });
+            largest[t] = fmaxf(largest[t], __shfl_xor(largest[t], 16));
+            largest[t] = fmaxf(largest[t], __shfl_xor(largest[t], 32));
+            many = many || largest[t] * of_group >= kMostUnits;
+        }
+        if (__any(many)) {
+            const float f = kLeastBy / of_group;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= f;
+            of_group = kLeastBy;
+            if ((threadIdx.x & 15) % kGroups == g.value) w.by = kLeastBy;
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float size = 0.f;
+#pragma unroll
+            for (int jj = 0; jj < G / 16; ++jj)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) size = fmaxf(size, fabsf(w.o[t][g.value * (G / 16) + jj][r]));
+            size = fmaxf(size, __shfl_xor(size, 16));
+            size = fmaxf(size, __shfl_xor(size, 32));
+            size = fmaxf(fmaxf(largest[t] * of_group * 0x1p-14f, size * 0x1p-100f), 0x1p-125f);
+            unit[t] = __uint_as_float(__float_as_uint(size) & 0x7f800000u);
+            const float to = of_group / unit[t], into = 1.f / unit[t];
+#pragma unroll
+            for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= into;
+            static_for<2>([&](auto half) {
+                float x[4];
+                weigh<kGroups>(g, vgrid[half.value], s[t] + 4 * half.value, x);
+                pf[t][2 * half.value] = round_pair(x[0] * to, x[1] * to);
+                pf[t][2 * half.value + 1] = round_pair(x[2] * to, x[3] * to);
+            });
+        }
+#pragma unroll
+        for (int jj = 0; jj < G / 16; ++jj) {
+            const int j = g.value * (G / 16) + jj;
+            const u32x4 vf = value(j);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) w.o[t][j] = mfma32<false>(vf, pf[t], w.o[t][j]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= unit[t];
     });
 }
 
@@ -740,7 +938,9 @@ __device__ __forceinline__ void finish(Wave<D, G, RT, BASE_FRAGS> &w, const Attn
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));        // its places are made here, not kept through the steps
     const int lane = thread & 63, col = lane & 15, quad = lane >> 4, wave = thread >> 6;
-    const float unstep = w.step_by > 0.f ? 1.f / w.step_by : 0.f;
+    const float unit = w.by > 0.f ? 1.f / w.by : 0.f;
+    float units[kGroups];
+    static_for<kGroups>([&](auto g) { units[g.value] = row_lane<g.value>(unit); });
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         w.l[t] = column_sum(w.l[t]);
@@ -765,7 +965,7 @@ __device__ __forceinline__ void finish(Wave<D, G, RT, BASE_FRAGS> &w, const Attn
 #pragma unroll
                     for (int jj = 0; jj < G / 16; ++jj)
                         part[(wave * 16 + col) * kStride + g * G - d0 + (4 * quad + i) * (G / 16) + jj] =
-                            fmaf(w.o[t][g * (G / 16) + jj][i], unstep, w.bsum[t][g]);
+                            fmaf(w.o[t][g * (G / 16) + jj][i], units[g], w.bsum[t][g]);
             __syncthreads();
             for (int y = thread; y < kRowWaves * 16 * kPart / 4; y += 64 * WAVES) {
                 const int r = y / (kPart / 4) % 16, first = y / (kPart / 4) / 16 * TW, e0 = d0 + y % (kPart / 4) * 4;
@@ -957,7 +1157,26 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
                 spot.grids(a.c.v_meta, at, vg[half]);
             }
         };
-        int t0 = (int)min((int64_t)x.u_in * layout.unit + wave * kTile, (int64_t)t_end);
+        const auto close = [&](const int (&good)[2]) {
+            asm volatile("");
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int k = 0; k < Places<D, G>::kRegs; ++k)
+                    if (Places<D, G>::token(k) >= good[half]) kg[half][k] = vg[half][k] = 0;
+        };
+        const auto key_grid = [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); };
+        const auto no_base = [](int, int) { return u32x4{}; };
+        const auto key = [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); };
+        const auto value_grid = [&](int half, int k) { return open_value_grid<T, NB>(vg[half][k]); };
+        const auto value = [&](int j) {
+            u32x4 f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = value_reg<NB, D>(vw[i / 2], i % 2, j, masks);
+            return f;
+        };
+        const int t_begin = (int)min((int64_t)x.u_in * layout.unit + wave * kTile, (int64_t)t_end);
+        int t0 = t_begin;
         if (t0 < t_end) {
             find(t0, page);
             load_keys(t0);
@@ -974,32 +1193,28 @@ __global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4
 #pragma unroll
             for (int half = 0; half < 2; ++half) good[half] = page[half] < 0 ? 0 : x.len - t0 - 16 * half;
             attend_step<T>(
-                w, t0, good,
-                [&] {
-                    asm volatile("");
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int k = 0; k < Places<D, G>::kRegs; ++k)
-                            if (Places<D, G>::token(k) >= good[half]) kg[half][k] = vg[half][k] = 0;
-                },
-                [&](int half, int k) { return open_key_grid<T>(kg[half][k], a.scale); }, [](int, int) { return u32x4{}; },
-                [&](int half, int mm) { return key_frag<Types<T>::kBf16, NB>(kw[half] + mm * (NB / 4)); },
+                w, t0, good, [&] { close(good); }, key_grid, no_base, key,
                 [&] {
                     page[0] = __builtin_amdgcn_readfirstlane(page_next[0]);
                     page[1] = __builtin_amdgcn_readfirstlane(page_next[1]);
                     load_keys(next);
                     __builtin_amdgcn_sched_barrier(0);
                 },
-                [&](int half, int k) { return open_value_grid<T, NB>(vg[half][k]); },
-                [&](int j) {
-                    u32x4 f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = value_reg<NB, D>(vw[i / 2], i % 2, j, masks);
-                    return f;
-                });
+                value_grid, value);
             load_values(next);
             __builtin_amdgcn_sched_barrier(0);
+        }
+        if (__builtin_expect(w.rest, 0)) {
+            float by = 0.f;
+            for (t0 = t_begin; t0 < t_end; t0 += kStep) {
+                int good[2];
+                find(t0, page);
+                load_keys(t0);
+                load_values(t0);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) good[half] = page[half] < 0 ? 0 : x.len - t0 - 16 * half;
+                attend_rest<T>(w, by, t0, good, [&] { close(good); }, key_grid, no_base, key, value_grid, value);
+            }
         }
         finish<T, D, G, RT, kWaves, kWaves>(w, a, d, x, h, place.run, ml, part);
     }
@@ -1059,6 +1274,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
     float *ml = reinterpret_cast<float *>(shared4 + wide_bytes<D, G>() / 16);
     int32_t *starts = reinterpret_cast<int32_t *>(ml + kWide * 16 * 2);
     int32_t *scan = starts + (((unsigned)d.s.n_seqs + 4) & ~3u);
+    int32_t *rest = scan + 8;                   // some wave's
     Layout<kRows, kWide> layout(d, a.per, starts, scan);
     if (place.first && d.starts) layout.put(d.starts);
     const int W = runs_of(d.workers, layout.total);
@@ -1122,7 +1338,34 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
             }
             if (lane == 0 && piece == 0) to.good[sub] = good;
         };
-        int t0 = (int)min((int64_t)x.u_in * layout.unit, (int64_t)t_end), page = 0, buffer = 0;
+        // the wave's pairs of 16 tokens of a step, to do(t, good, ...) with what attend_step takes of them
+        const auto turns = [&](const WideStep<D, G> &now, int t0, auto attend) {
+#pragma unroll 1
+            for (int turn = 0; turn < kTurns; ++turn) {
+                const int pair = wave % TW + turn, t = t0 + 32 * pair;
+                if (t >= min(w.lim_high, t_end)) continue;
+                const int both[2] = {__builtin_amdgcn_readfirstlane(now.good[2 * pair]),
+                                     __builtin_amdgcn_readfirstlane(now.good[2 * pair + 1])};
+                attend(
+                    t, both, [&](int half, int k) { return f32x2{now.key_step[2 * pair + half][k][lane], 0.f}; },
+                    [&](int half, int p) {
+                        // the same in the slots of the parts behind, which meet zeros but in quad 3
+                        constexpr int kWords = base_slots<D / G>() / 2;
+                        const uint16_t *b = now.key_base[2 * pair + half][lane >= 48][lane & 15] + 2 * kWords * p;
+                        u32x4 f = {0, 0, 0, 0};
+#pragma unroll
+                        for (int e = 0; e < kWords; ++e) f[e] = f[e + kWords] = reinterpret_cast<const uint32_t *>(b)[e];
+                        if (D / G == 1) f[0] = f[1] = f[0] & 0xffffu;       // the other half is not written
+                        return f;
+                    },
+                    [&](int half, int mm) { return now.key[2 * pair + half][mm][lane]; }, [] {},
+                    [&](int half, int k) { return now.value_grid[2 * pair + half][k][lane]; },
+                    [&](int j) { return now.value[pair][j][lane]; });
+            }
+        };
+        const int t_begin = (int)min((int64_t)x.u_in * layout.unit, (int64_t)t_end);
+        int t0 = t_begin, page = 0, buffer = 0;
+        if (threadIdx.x == 0) *rest = 0;        // before the first barrier, and behind the last item's last
         // a step that there is not is fetched like the last one, and not used
         auto within = [&](int t) { return t < t_end ? t : t0; };
         if (t0 < t_end) fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
@@ -1150,42 +1393,34 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_w
             fetch(next + 16 * sub, __builtin_amdgcn_readfirstlane(page));
             page = page_of_step(within(t0 + (kAhead + 1) * kWideStep));
             __builtin_amdgcn_sched_barrier(0);
-            const WideStep<D, G> &now = steps[buffer];
-#pragma unroll 1
-            for (int turn = 0; turn < kTurns; ++turn) {
-                const int pair = wave % TW + turn, t = t0 + 32 * pair;
-                if (t >= min(w.lim_high, t_end)) continue;
-                const int both[2] = {__builtin_amdgcn_readfirstlane(now.good[2 * pair]),
-                                     __builtin_amdgcn_readfirstlane(now.good[2 * pair + 1])};
-                attend_step<T>(
-                    w, t, both, [] {}, [&](int half, int k) { return f32x2{now.key_step[2 * pair + half][k][lane], 0.f}; },
-                    [&](int half, int p) {
-                        // the same in the slots of the parts behind, which meet zeros but in quad 3
-                        constexpr int kWords = base_slots<D / G>() / 2;
-                        const uint16_t *b = now.key_base[2 * pair + half][lane >= 48][lane & 15] + 2 * kWords * p;
-                        u32x4 f = {0, 0, 0, 0};
-#pragma unroll
-                        for (int e = 0; e < kWords; ++e) f[e] = f[e + kWords] = reinterpret_cast<const uint32_t *>(b)[e];
-                        if (D / G == 1) f[0] = f[1] = f[0] & 0xffffu;       // the other half is not written
-                        return f;
-                    },
-                    [&](int half, int mm) { return now.key[2 * pair + half][mm][lane]; }, [] {},
-                    [&](int half, int k) { return now.value_grid[2 * pair + half][k][lane]; },
-                    [&](int j) { return now.value[pair][j][lane]; });
-            }
+            turns(steps[buffer], t0, [&](int t, const int (&good)[2], auto... parts) { attend_step<T>(w, t, good, [] {}, parts...); });
             if constexpr (kBuffers == 2) buffer ^= 1;
         }
+        if (lane == 0 && w.rest) *rest = 1;
         __syncthreads();                        // `part` lies over the steps
+        if (__builtin_expect(*rest, 0)) {
+            float by = 0.f;
+            for (t0 = t_begin; t0 < t_end; t0 += kWideStep) {
+                __syncthreads();
+                fetch(t0 + 16 * sub, __builtin_amdgcn_readfirstlane(page_of_step(t0)));
+                widen(steps[0]);
+                __syncthreads();
+                turns(steps[0], t0, [&](int t, const int (&good)[2], auto key_grid, auto base, auto key, auto, auto value_grid, auto value) {
+                    attend_rest<T>(w, by, t, good, [] {}, key_grid, base, key, value_grid, value);
+                });
+            }
+            __syncthreads();
+        }
         finish<T, D, G, 1, TW, kWide>(w, a, d, x, h, place.run, ml, part);
     }
 }
 
 // Bytes of LDS beside what the waves work in: the units before each sequence's and their scan,
-// at most 16 KB.
+// at most 16 KB, and a flag.
 inline size_t starts_bytes(const AttnArgs &a)
 {
     const int n = a.sides == 2 ? max(a.side[0].s.n_seqs, a.side[1].s.n_seqs) : a.side[0].s.n_seqs;
-    return 4 * (((size_t)n + 4) & ~size_t(3)) + 4 * 8;
+    return 4 * (((size_t)n + 4) & ~size_t(3)) + 4 * 8 + 16;
 }
 inline dim3 grid_of(const AttnArgs &a)
 {

@@ -367,8 +367,10 @@ hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
  * sees positions 0..x (which must be in the cache already: write, then attend):
  *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * <q, k_t>),
  * with k_t, v_t = base + q * step unrounded, scores and sums in binary32 (the sums of
- * |q| * 2^nbits must stay in its range), weights rounded to 11 bits where they meet the codes
- * of v, and out rounded once to the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
+ * |q| * 2^nbits and of 64 * |v_t| must stay in its range), weights rounded where they meet the
+ * codes of v, to 11 bits or by 2^-25 of the row's largest weight, whichever is more (those
+ * below 2^-119 of it may be lost, and of sums less than 2^-100), and out rounded once to the
+ * type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
  * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. What a row does not see
  * does not change it, NaN included; a row that sees a group of NaN is unspecified, of v in that
  * group's dimensions. n_tokens * n_q_heads is at most 2^30. out must not overlap q or itself.
