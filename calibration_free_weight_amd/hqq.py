@@ -325,7 +325,9 @@ def hqq_unpack(packed, n_codes, nbits, codes, stream=None) -> None:
 # page_size, head_dim/group_size, 2] of the type of the rows, page_size, n_heads, head_dim,
 # nbits, group_size. table: int32 [n_seqs, max_pages]; lens: int32 [n_seqs]; cu_tokens: int32
 # [n_seqs + 1] or None. Rows are [n_tokens, heads, head_dim] with contiguous dimensions. The
-# calls run on the current stream of the cache's device unless `stream` is given.
+# calls run on the current stream of the cache's device unless `stream` is given; what they allocate
+# then belongs to that stream, as if allocated under it (wait for it before other streams use it, and
+# record_stream before they outlive it).
 # hqq_cache and hqq_seqs as bytes (a third of the time that a ctypes structure takes to make)
 _pack_cache = struct.Struct("@4Pq6i").pack
 _pack_seqs = struct.Struct("@3P2iq").pack
@@ -438,13 +440,14 @@ def hqq_cache_attention_workspace(cache, table, lens, n_tokens, n_q_heads, prefi
     return n
 
 
-def _scratch(n, dev, stream):
-    """Scratch memory of a call, from the allocator's pool of the stream that it runs on."""
+def _on_stream(dev, stream, make):
+    """make(), with what it allocates from the allocator's pool of the stream that a call runs on:
+    memory of another stream's pool may have work of that stream before it."""
     T = _torch
-    if stream is None or int(stream) == T._C._cuda_getCurrentRawStream(dev):
-        return T.empty(n, dtype=T.uint8, device=dev)
+    if stream is None or dev < 0 or int(stream) == T._C._cuda_getCurrentRawStream(dev):
+        return make()
     with T.cuda.stream(T.cuda.ExternalStream(int(stream), device=dev)):
-        return T.empty(n, dtype=T.uint8, device=dev)
+        return make()
 
 
 def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream):
@@ -457,7 +460,7 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
     s = _seqs_struct(table, lens, cu_tokens, n, dev)
     qp, qt, qh = _rows(q, shape, dev, dtype, "q")
     if out is None:
-        out = T.empty_like(q)
+        out = _on_stream(dev, stream, lambda: T.empty_like(q))
     op, ot, oh = _rows(out, shape, dev, dtype, "out")
     if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
                             not lse.is_contiguous()):
@@ -472,7 +475,7 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
     if workspace is None:
         need = L.hqq_cache_attention_workspace(c, s, heads, prefix_len)
         if need:
-            workspace = _scratch(need, dev, stream)
+            workspace = _on_stream(dev, stream, lambda: T.empty(need, dtype=T.uint8, device=dev))
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise _bad("workspace must be contiguous, on the cache's device")
     wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -517,7 +520,8 @@ def cache_read(cache, table, lens, n_tokens, cu_tokens=None, stream=None):
     """Allocate and fill (k, v) for the last tokens of the sequences, n_tokens in all."""
     T = _torch or _th()
     km = cache["k_meta"]
-    both = T.empty((2, n_tokens, cache["n_heads"], cache["head_dim"]), dtype=km.dtype, device=km.device)
+    both = _on_stream(km.get_device(), stream, lambda: T.empty(
+        (2, n_tokens, cache["n_heads"], cache["head_dim"]), dtype=km.dtype, device=km.device))
     k, v = both.unbind(0)
     hqq_cache_read(cache, table, lens, k, v, cu_tokens, stream)
     return k, v
