@@ -460,7 +460,7 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
     s = _seqs_struct(table, lens, cu_tokens, n, dev)
     qp, qt, qh = _rows(q, shape, dev, dtype, "q")
     if out is None:
-        out = _on_stream(dev, stream, lambda: T.empty_like(q))
+        out = _on_stream(dev, stream, lambda: T.empty(shape, dtype=dtype, device=q.device))
     op, ot, oh = _rows(out, shape, dev, dtype, "out")
     if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
                             not lse.is_contiguous()):
@@ -528,13 +528,13 @@ def cache_read(cache, table, lens, n_tokens, cu_tokens=None, stream=None):
 
 
 def cache_attention(cache, table, lens, q, cu_tokens=None, scale=None, lse=None, stream=None):
-    """Allocate the output and call hqq_cache_attention."""
+    """Allocate the output (contiguous) and call hqq_cache_attention."""
     return _attention(cache, table, lens, None, 0, q, None, lse, scale, cu_tokens, None, stream)
 
 
 def cache_attention_prefix(cache, table, lens, prefix_pages, prefix_len, q, cu_tokens=None, scale=None,
                            lse=None, stream=None):
-    """Allocate the output and call hqq_cache_attention_prefix."""
+    """Allocate the output (contiguous) and call hqq_cache_attention_prefix."""
     return _attention(cache, table, lens, prefix_pages, prefix_len, q, None, lse, scale, cu_tokens, None, stream)
 
 

@@ -51,3 +51,15 @@ def test_what_a_call_allocates_belongs_to_its_stream(H, call):
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(torch.stack(got) if call == "read" else got, want)
+
+
+def test_outputs_are_contiguous_whatever_the_queries(H):
+    cache, table, lens, q = small(H)
+    want = H.cache_attention(cache, table, lens, q)
+    wide = torch.zeros(q.shape[0], q.shape[1] + 3, q.shape[2], dtype=q.dtype, device="cuda")
+    wide[:, 1:-2] = q
+    for x in (q.transpose(0, 1).contiguous().transpose(0, 1), wide[:, 1:-2]):       # heads first; a part of more
+        out = H.cache_attention(cache, table, lens, x)
+        assert out.is_contiguous() and torch.equal(out.view(q.shape[0], -1), want.view(q.shape[0], -1))
+        out = H.cache_attention_prefix(cache, table, lens, table[0], 0, x)
+        assert out.is_contiguous() and torch.equal(out, want)
