@@ -669,7 +669,8 @@ __device__ __forceinline__ float fitting(float by, Each each_step)
     });
     over_same_group<GROUPS>(most, least);
     const auto by_of = [](float step) {
-        return fmaxf(0x1p8f / __uint_as_float(__float_as_uint(fmaxf(step, 0x1p-100f)) & 0x7f800000u), kLeastBy);
+        // 2^8 over the power of two at or below the step, by exponents
+        return fmaxf(__uint_as_float(0x83000000u - (__float_as_uint(fmaxf(step, 0x1p-100f)) & 0x7f800000u)), kLeastBy);
     };
     const float fit = by_of(most);
     const bool fits = least * fit >= 1.f && most * fit < 0x1p9f;
@@ -760,13 +761,14 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
                 for (int k = 0; k < kRegs; ++k) f(value_grid(half, k)[0]);
         });
         const float f = was > 0.f ? w.by / was : 1.f;
-        static_for<kGroups>([&](auto g) {
-            const float fg = row_lane<g.value>(f);
+        if (__any(f < 1.f))
+            static_for<kGroups>([&](auto g) {
+                const float fg = row_lane<g.value>(f);
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+                for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= fg;
-        });
+                    for (int jj = 0; jj < G / 16; ++jj) w.o[t][g.value * (G / 16) + jj] *= fg;
+            });
         bool some = false;
 #pragma unroll
         for (int half = 0; half < 2; ++half)
