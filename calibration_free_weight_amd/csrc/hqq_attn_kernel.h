@@ -1107,7 +1107,7 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
 // of 8 bits, 277 MB: 45 us, 6.1 TB/s; 300 tokens of 32 heads: 9.6 us, four loads that wait for
 // each other (lengths, pages, codes, and the instructions themselves) and three steps.
 template <typename T, int NB, int D, int G, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT *D <= 128 ? (NB == 4 || D == 64 ? 4 : 3) : 2) void attn_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * kWaves, blocks_per_cu(RT, D, NB) * kWaves / 4) void attn_kernel(AttnArgs a)       // waves to a SIMD
 {
     constexpr int kRows = 16 * RT;
     extern __shared__ int32_t shared[];
@@ -1262,7 +1262,7 @@ constexpr size_t wide_bytes()       // of the steps, or of what joins the waves 
 }
 
 template <typename T, int NB, int D, int G, int TW>
-__global__ __launch_bounds__(64 * wide_waves<D>(), D <= 128 ? 4 : 2) void attn_wide_kernel(AttnArgs a)
+__global__ __launch_bounds__(64 * wide_waves<D>(), blocks_per_cu(wide_waves<D>() / TW, D, NB) * wide_waves<D>() / 4) void attn_wide_kernel(AttnArgs a)
 {
     constexpr int kWide = wide_waves<D>(), kRows = 16 * (kWide / TW), kTurns = 2 / TW, kBuffers = wide_buffers<D>();
     constexpr int kRegs = Places<D, G>::kRegs, kParts = kWide / kWideTiles;

@@ -126,15 +126,6 @@ struct Plan {
     size_t bytes;
 };
 
-// Blocks of a launch that a CU holds, by the registers that the kernels' sums and codes in
-// flight take (their launch bounds say the same). A launch has no more: with 1152 or 1536 blocks
-// rather than 1024 the last ones begin when the first are done, and take longer in all.
-int resident(int tiles16, int dim, int nbits)
-{
-    if (tiles16 > 1 || dim == 256) return 2;
-    return nbits == 8 && dim == 128 ? 3 : 4;
-}
-
 // The longest side that one block takes alone: cutting it saves four steps at most, and
 // joining the pieces costs a launch (sequences of 100 to 500 tokens, 64 of them: 12.0 us whole,
 // 19.3 cut; one of 1000: 13.3 whole, 10.9 cut).
@@ -161,7 +152,7 @@ int tiles_for(int64_t rows, int n_seqs, int64_t longest, const hqq_cache *c)
     const int64_t each = (rows + n_seqs - 1) / n_seqs, few = (each + 15) / 16;
     if (few == 1) return 1;
     const int64_t units = few * n_seqs * ((longest + hqq::kStep - 1) / hqq::kStep);
-    const int64_t blocks = 256 * resident(1, c->head_dim, c->nbits), runs = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
+    const int64_t blocks = 256 * hqq::blocks_per_cu(1, c->head_dim, c->nbits), runs = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
     if (c->head_dim == 256) {
         // the first limit is of one tile of 32 for a sequence: smaller ones read the cache twice
         if (units <= (few == 2 ? 6 : 31) * runs) return 1;
@@ -192,7 +183,7 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         x.unit = (int)(longest <= kWhole ? (longest + step) / step * step : step);
         // no more than the 256 CUs hold at once (a block more would take as long again), nor than
         // the units that there can be
-        const int64_t blocks = 256 * resident(x.tiles16, c->head_dim, c->nbits);
+        const int64_t blocks = 256 * hqq::blocks_per_cu(x.tiles16, c->head_dim, c->nbits);
         const int64_t units = (rows / (16 * x.tiles16) + n_seqs) * hqq::units_along((int32_t)longest, x.unit);
         const int64_t each = blocks / c->n_heads > 0 ? blocks / c->n_heads : 1;
         x.workers = (int)(each < units ? each : units);
@@ -218,7 +209,7 @@ Plan plan_of(const hqq_cache *c, const hqq_seqs *s, int n_q_heads, int64_t prefi
         // 1544: 28 us so, 37 with two).
         const SidePlan with = cut(p.prefix.tiles16, s->n_seqs, longest);
         const int64_t both = (int64_t)(with.workers + p.prefix.workers) * c->n_heads;
-        if (longest <= kWhole && both <= 256 * resident(with.tiles16, c->head_dim, c->nbits)) p.own = with;
+        if (longest <= kWhole && both <= 256 * hqq::blocks_per_cu(with.tiles16, c->head_dim, c->nbits)) p.own = with;
     }
     lay(p.own, s->n_seqs);
     if (prefix_len > 0) lay(p.prefix, 1);

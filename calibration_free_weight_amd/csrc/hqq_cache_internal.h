@@ -146,6 +146,16 @@ struct AttnShape {
     bool bf16;
 };
 
+// Blocks of a launch that a CU holds, by the registers that the kernels' sums and codes in flight
+// take: their launch bounds are made of this, and no more blocks are launched. (With 1152 or 1536
+// rather than 1024 the last ones begin when the first are done, and take longer in all. Heads of 64
+// in tiles of 32 rows would fit four times, with some registers in memory: 64 heads, 200 rows over
+// 2000 tokens, 4 bits 94 us and 98.5, but 32 heads of 80 rows over 1000 tokens 39.6 and 33.)
+constexpr int blocks_per_cu(int tiles16, int dim, int nbits)
+{
+    return tiles16 > 1 || dim == 256 ? 2 : nbits == 8 && dim == 128 ? 3 : 4;
+}
+
 hipError_t launch_attn(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
 hipError_t launch_join(const JoinArgs &a, bool bf16, hipStream_t stream);
 
