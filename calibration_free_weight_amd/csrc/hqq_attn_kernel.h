@@ -58,7 +58,8 @@ __device__ __forceinline__ float row_lane(float x)
 // acc[r] += lane N[r] of each row of 16 lanes of k[r], times x[r]: the broadcast is part of the
 // instruction, which the compiler makes of a product alone. What it would keep apart for its own
 // instructions is kept apart here: two wait states behind whatever wrote k and x, and `settled`,
-// which reads the matrix products that x or acc come from and so comes after their last.
+// which reads the matrix products that x or acc come from and so comes after their last. (acc is
+// written before all of k and x are read.)
 template <int N0, int N1, int N2, int N3>
 __device__ __forceinline__ void add_row_lanes(float (&acc)[4], const float (&k)[4], const float (&x)[4], uint32_t settled)
 {
@@ -67,7 +68,7 @@ __device__ __forceinline__ void add_row_lanes(float (&acc)[4], const float (&k)[
         "v_fmac_f32_dpp %1, %5, %9 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %2, %6, %10 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %3, %7, %11 row_newbcast:%16 row_mask:0xf bank_mask:0xf"
-        : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3])
+        : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "+&v"(acc[3])
         : "v"(k[0]), "v"(k[1]), "v"(k[2]), "v"(k[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(settled),
           "n"(N0), "n"(N1), "n"(N2), "n"(N3));
 }
@@ -80,7 +81,7 @@ __device__ __forceinline__ void add_row_lanes(float &acc, const float (&k)[4], c
         "v_fmac_f32_dpp %0, %2, %6 row_newbcast:%10 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %0, %3, %7 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n"
         "v_fmac_f32_dpp %0, %4, %8 row_newbcast:%12 row_mask:0xf bank_mask:0xf"
-        : "+v"(acc)
+        : "+&v"(acc)
         : "v"(k[0]), "v"(k[1]), "v"(k[2]), "v"(k[3]), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]),
           "n"(N0), "n"(N1), "n"(N2), "n"(N3));
 }
