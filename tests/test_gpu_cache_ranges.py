@@ -58,6 +58,12 @@ def sizes(scene, dtype, n, dim, group):
     elif scene == "one far behind":
         x *= 2.0 ** -13 if half else 2.0 ** -60
         x[-1] = 7000.0 if half else 2.0 ** 90
+    elif scene == "ends of the range":
+        x *= 2.0 ** -14 if half else 2.0 ** -84
+        x[-1] = 7000.0 if half else 2.0 ** 112
+    elif scene == "a step far larger":      # all tokens of some steps, which the first of many rows do not see
+        x *= 2.0 ** -14 if half else 2.0 ** -84
+        x[-40:] = 7000.0 if half else 2.0 ** 100
     elif scene == "groups apart":
         x[:, :group] = 2.0 ** 10 if half else 2.0 ** 50
         x[:, group:] = 2.0 ** -11 if half else 2.0 ** -30
@@ -72,7 +78,7 @@ def sizes(scene, dtype, n, dim, group):
     return x
 
 
-@pytest.mark.parametrize("scene", ["one behind", "one far behind", "groups apart", "rising and falling", "mixed", "hardly weighed"])
+@pytest.mark.parametrize("scene", ["one behind", "one far behind", "ends of the range", "a step far larger", "groups apart", "rising and falling", "mixed", "hardly weighed"])
 @pytest.mark.parametrize("dtype,nbits,dim,group,heads,per,n,new,width", FORMS)
 def test_values_of_very_different_size(H, scene, dtype, nbits, dim, group, heads, per, n, new, width):
     gen = torch.Generator().manual_seed(dim + nbits + len(scene))
