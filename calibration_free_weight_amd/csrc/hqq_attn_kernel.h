@@ -822,6 +822,10 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
 // first). A row's weights go in times the power of two that brings the largest of its products in
 // the group to 2^14, and its sums in units of the same meanwhile (of more where they hold 2^100 of
 // these). The arguments are those of attend_step.
+// Kept out of the step, where the same cost the usual path 8 to 18% (its sums were copied, or other
+// values went to memory). Such tokens take about twice a step: 64 sequences of 4100 to 8190 tokens,
+// 8 heads of 128, 4 bits 106 us without any, 114 with one token in 1000 and 199 with every third
+// far below the others; 2 x 500 rows over 3500 to 4000 tokens, 40 heads 170, 232 and 472.
 template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
           typename ValueGrid, typename Value>
 __device__ __forceinline__ void attend_rest(Wave<D, G, RT, BASE_FRAGS> &w, float &by, int t0, const int (&good)[2], Close close,
@@ -1104,9 +1108,10 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
 // below, which is why it takes many rows too while there is little work for each block. Codes and grids are read once and in whole lines;
 // a step's 400 instructions to widen and weigh them take about as long as its bytes (4 bits,
 // heads of 128), which is why grids are applied to sums and not to codes. 64 sequences of 4100 to
-// 8190 tokens, 8 heads of 128, 4 bits, 455 MB: 96 us, 4.7 TB/s (a copy reaches 5.1); 131071 tokens
-// of 8 bits, 277 MB: 45 us, 6.1 TB/s; 300 tokens of 32 heads: 9.6 us, four loads that wait for
-// each other (lengths, pages, codes, and the instructions themselves) and three steps.
+// 8190 tokens, 8 heads of 128, 4 bits, 455 MB: 98 us, 4.6 TB/s (a copy reaches 5.1); 131071 tokens
+// of 8 bits, 277 MB: 45 us, 6.2 TB/s; 300 tokens of 32 heads: 9.8 us, four loads that wait for
+// each other (lengths, pages, codes, and the instructions themselves) and three steps one after
+// another.
 template <typename T, int NB, int D, int G, int RT>
 __global__ __launch_bounds__(64 * kWaves, blocks_per_cu(RT, D, NB) * kWaves / 4) void attn_kernel(AttnArgs a)       // waves to a SIMD
 {
@@ -1235,10 +1240,10 @@ __global__ __launch_bounds__(64 * kWaves, blocks_per_cu(RT, D, NB) * kWaves / 4)
 // It is bound by the instructions beside the products: a wave's step of 16 rows and 32 tokens of
 // heads of 128 in two groups has 18 products of 16 cycles and about 115 vector instructions of 4
 // (grids, exponentials, the rounding of weights), and its share of the widening 40 more. 2 x 500
-// rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 171 us, 418 TFLOP/s; 64 x 8 rows a head
-// over 16390 tokens, 8 heads: 81 us, 427 TFLOP/s, of them 16 before the first product and behind
-// the last, for 33 MB of pieces. Counters of the latter: vector instructions 66% of the time, LDS
-// 38%, products 23%; a wave waits 42% of its time for loads and for the block's other waves.
+// rows over 3500 to 4000 tokens, 40 heads of 128, 4 bits: 177 us, 405 TFLOP/s; 64 x 8 rows a head
+// over 16390 tokens, 8 heads: 81 us, 422 TFLOP/s, of them 16 before the first product and behind
+// the last, for 33 MB of pieces. Counters of the latter: vector instructions 67% of the time, LDS
+// 38%, products 23%; a wave waits 41% of its time for loads and for the block's other waves.
 constexpr int kWideStep = 64, kWideTiles = kWideStep / 16;
 
 template <int D, int G>

@@ -137,10 +137,12 @@ __device__ __forceinline__ uint32_t step_bits(float lo, float hi, int top)
 }
 
 // ---- write ------------------------------------------------------------------------------------
-// Bound by memory and the arithmetic together: 18060 tokens of 32 heads of 128 in 4 bits, 379 MB,
-// take 89 to 105 us (4.2 to 3.6 TB/s) where their bytes alone take 74 at a copy's rate, with about
-// 100 instructions for a lane's eight values of 24 bytes in and out. A token of 8 heads takes
-// 3.3 us, the launch and three loads that wait for each other.
+// Bound by neither memory nor arithmetic alone: 18060 tokens of 32 heads of 128 in 4 bits, 379 MB,
+// take 105 us (3.6 TB/s; 89 when the same inputs were written just before) where their bytes take 74
+// at a copy's rate, with about 100 instructions for a lane's eight values of 24 bytes in and out:
+// vector instructions are issued 72% of the time, and a wave waits 45% of its own. A token of 8
+// heads takes 3.4 us, the launch and a chain of loads (its sequence's row offsets, length and page;
+// with many sequences two looks at the offsets first).
 // Codes are decided exactly: the quotient, by a
 // product with the reciprocal's estimate, errs by at most 2^(nbits - 22), so only within twice
 // that of a half is it held against the midpoint, again without rounding: (2k + 1) * step has
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheView c, SeqV
 }
 
 // ---- read -------------------------------------------------------------------------------------
-// Bound by memory: 65521 tokens of 8 heads of 128 in 8 bits, 407 MB, take 78 us (5.2 TB/s, a
+// Bound by memory: 65521 tokens of 8 heads of 128 in 8 bits, 407 MB, take 80 us (5.1 TB/s, a
 // copy's rate). All of a lane's loads are asked for before the first is used, whatever the page.
 template <typename T>
 __device__ __forceinline__ uint4 values8(const float (&q)[8], uint32_t meta)

@@ -146,7 +146,9 @@ constexpr int64_t kWhole = 512;
 //   500 x 4 over 500                  21    29    41
 //   8 x 250 x 4 over 2000             192   185   148
 // The limits are units of 128 tokens of 16 rows, to a run. (Tiles of 64 rows of heads of up to
-// 128 were between the others or behind both, and are not there.)
+// 128 were between the others or behind both, and are not there.) One tile for all: rows are the
+// sequences' average and `longest` is the table's width, for lengths are not known here. A chunk
+// among single rows, or short sequences under a wide table, get what their average would.
 int tiles_for(int64_t rows, int n_seqs, int64_t longest, const hqq_cache *c)
 {
     const int64_t each = (rows + n_seqs - 1) / n_seqs, few = (each + 15) / 16;

@@ -354,8 +354,8 @@ hqq_status hqq_cache_write(const hqq_cache *cache, const hqq_seqs *seqs, const v
                            int64_t k_token_stride, int64_t k_head_stride, const void *v,
                            int64_t v_token_stride, int64_t v_head_stride, void *stream);
 
-/* Read tokens back, the mirror of hqq_cache_write: k and v get base + q * step rounded once
- * to the type, zeros for tokens that are not in the cache. With n_b = lens[b] the whole
+/* Read tokens back, the mirror of hqq_cache_write: k and v get base + q * step, rounded to
+ * binary32 and then to the type, zeros for tokens that are not in the cache. With n_b = lens[b] the whole
  * sequence is read. The heads of a token must not overlap, nor the tokens. */
 hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
                           int64_t k_token_stride, int64_t k_head_stride, void *v,
@@ -369,8 +369,8 @@ hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k,
  * with k_t, v_t = base + q * step unrounded, scores and sums in binary32 (the sums of
  * |q| * 2^nbits and of 64 * |v_t| must stay in its range), weights rounded where they meet the
  * codes of v, to 11 bits or by 2^-25 of the row's largest weight, whichever is more (those
- * below 2^-119 of it may be lost, and of sums less than 2^-100), and out rounded once to the
- * type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
+ * below 2^-119 of it may be lost, and of sums less than 2^-100), and out rounded from binary32 to
+ * the type; lse (binary32 [n_tokens, n_q_heads], nullable) gets
  * log(sum_t w_t). A row that sees nothing gives zeros and -infinity. What a row does not see
  * does not change it, NaN included; a row that sees a group of NaN is unspecified, of v in that
  * group's dimensions. n_tokens * n_q_heads is at most 2^30. out must not overlap q or itself.
