@@ -1406,7 +1406,7 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), blocks_per_cu(wide_waves<D>()
         }
         if (lane == 0 && w.rest) *rest = 1;
         __syncthreads();                        // `part` lies over the steps
-        if (__builtin_expect(*rest, 0)) {
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(*rest), 0)) {
             float by = 0.f;
             for (t0 = t_begin; t0 < t_end; t0 += kWideStep) {
                 __syncthreads();

@@ -160,3 +160,59 @@ def test_sequences_of_very_different_size(H, dtype, nbits, heads, per, n_seqs, l
     out = H.cache_attention(cache, i32(table), i32(lens), q, cu_tokens=cu(new), lse=lse)
     ref = CB.attention(R.Held(cache), table, lens, cu(new).tolist(), q, dim ** -0.5)
     CB.check(out, lse, ref, torch.ones(sum(new), dtype=torch.bool))
+
+
+@pytest.mark.parametrize("scene", ["usual", "hardly weighed", "mixed"])
+@pytest.mark.parametrize("heads,new,width", [(2, 7, 256), (256, 100, 1024), (256, 128, 2048)])
+def test_queries_that_are_not_finite_leave_other_rows_alone(H, scene, heads, new, width):
+    gen = torch.Generator().manual_seed(new + len(scene))
+    dim, n = 64, 200
+    k = torch.randn(n, heads, dim, generator=gen, dtype=torch.float64) * 0.5
+    v = torch.randn(n, heads, dim, generator=gen, dtype=torch.float64) * sizes(scene, B, n, dim, 32)[:, None]
+    q = torch.randn(new, heads, dim, generator=gen) * 0.5
+    if scene == "hardly weighed":
+        q[..., 0], k[5, :, 0] = 4.0, -120.0
+    cache, table = held_cache(H, B, 4, 32, 16, width, k, v, gen)
+    bad = {0: float("nan"), 3: float("inf"), 5: float("-inf")}
+    ref = CB.attention(R.Held(cache), table, [n], None, q.to(B), 0.125)
+    for i, x in bad.items():
+        q[i, :, 7] = x
+    out = H.cache_attention(cache, i32(table), i32([n]), q.to(B).cuda())
+    CB.check(out, None, ref, torch.tensor([i not in bad for i in range(new)]))
+
+
+@pytest.mark.parametrize("heads,new,width", [(2, 7, 704), (256, 128, 2048)])
+def test_captured_calls_on_values_that_change_their_size(H, heads, new, width):
+    """A graph replayed over values of usual and of very different sizes in turn."""
+    gen = torch.Generator().manual_seed(new)
+    dim, n = 64, 200
+    made = []
+    for scene in ("usual", "mixed", "usual", "one behind"):
+        k = torch.randn(n, heads, dim, generator=gen, dtype=torch.float64) * 0.5
+        v = torch.randn(n, heads, dim, generator=gen, dtype=torch.float64) * sizes(scene, B, n, dim, 32)[:, None]
+        made.append(held_cache(H, B, 8, 32, 16, width, k, v, torch.Generator().manual_seed(1)))
+    cache, table = {**made[0][0]}, made[0][1]
+    for x in ("k_codes", "v_codes", "k_meta", "v_meta"):
+        cache[x] = cache[x].clone()
+    t, lens = i32(table), i32([n])
+    q = (torch.randn(new, heads, dim, generator=gen) * 0.5).to(B).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(H.hqq_cache_attention_workspace(cache, t, lens, new, heads), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        H.hqq_cache_attention(cache, t, lens, q, out, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        H.hqq_cache_attention(cache, t, lens, q, out, workspace=ws)
+    for other, same_table in made + made[:2]:
+        assert same_table == table
+        for x in ("k_codes", "v_codes", "k_meta", "v_meta"):
+            cache[x].copy_(other[x])
+        out.fill_(3)
+        g.replay()
+        torch.cuda.synchronize()
+        ref = CB.attention(R.Held(cache), table, [n], None, q, dim ** -0.5)
+        CB.check(out, None, ref, torch.ones(new, dtype=torch.bool))
+        assert torch.equal(H.cache_attention(cache, t, lens, q), out)
