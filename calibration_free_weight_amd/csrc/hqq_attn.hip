@@ -215,6 +215,10 @@ hipError_t join_typed(const JoinArgs &a, hipStream_t stream)
 
 hipError_t launch_attn(const AttnArgs &a, const AttnShape &x, hipStream_t stream)
 {
+    if (a.tree) {
+        if (x.bf16) return x.nbits == 4 ? launch_attn_tree_bf16_4(a, x, stream) : launch_attn_tree_bf16_8(a, x, stream);
+        return x.nbits == 4 ? launch_attn_tree_f16_4(a, x, stream) : launch_attn_tree_f16_8(a, x, stream);
+    }
     if (x.bf16) return x.nbits == 4 ? launch_attn_bf16_4(a, x, stream) : launch_attn_bf16_8(a, x, stream);
     return x.nbits == 4 ? launch_attn_f16_4(a, x, stream) : launch_attn_f16_8(a, x, stream);
 }

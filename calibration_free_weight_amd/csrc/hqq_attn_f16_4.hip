@@ -5,7 +5,7 @@ namespace hqq {
 
 hipError_t launch_attn_f16_4(const AttnArgs &a, const AttnShape &x, hipStream_t stream)
 {
-    return by_dim<F16, 4>(a, x, stream);
+    return by_dim<F16, 4, false>(a, x, stream);
 }
 
 }  // namespace hqq

@@ -449,14 +449,18 @@ constexpr uint32_t kStepLow = 0x3f800000u, kStepHigh = 0x44000000u;     // bits 
 constexpr float kLeastBy = 0x1p-40f, kMostUnits = 0x1p60f;
 
 // What a wave keeps of its 16 * RT query rows (a lane: of its column of each 16). BASE_FRAGS: the
-// bases' part of the scores is a product too, see base_query.
-template <int D, int G, int RT, bool BASE_FRAGS>
+// bases' part of the scores is a product too, see base_query. TREE: rows see what was there before
+// the call's tokens, and of these the ones that their masks name.
+template <int D, int G, int RT, bool BASE_FRAGS, bool TREE>
 struct Wave {
     static constexpr int kGroups = D / G;
     u32x4 qf[RT][D / 32];       // queries, as B fragments
     float qsum[RT][kGroups];    // their sums over each group, scaled
-    int lim[RT];                // what a row sees ends here
+    int lim[RT];                // what a row sees ends here; with TREE its row of the call, that of the masks
     int lim_low, lim_high;      // for all rows, for any
+    int first;                  // with TREE, the position of the first of the call's tokens
+    const uint32_t *tree;       // and the masks, with the 32-bit words of one
+    int tree_words;
     f32x4 o[RT][D / 16];
     u32x4 qb[BASE_FRAGS ? RT : 1][kGroups > 4 ? 2 : 1];      // the sums as B fragments
     // m: scores are taken from it; above: how far one may lie above before m moves (none
@@ -497,8 +501,8 @@ __device__ __forceinline__ u32x4 base_query(const float (&sum)[GROUPS], int prod
     return f;
 }
 
-template <typename T, int D, int G, int RT, bool BASE_FRAGS>
-__device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, bool TREE>
+__device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS, TREE> &w, const AttnArgs &a, bool causal, const Item &x, int h, int row0)
 {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
@@ -507,8 +511,16 @@ __device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnA
     // what the first and the last of the wave's rows see
     const int before = causal ? x.len - (x.rows.end - x.rows.begin) + 1 : x.len;
     const int last = min(row0 + 16 * RT, x.n_rows) - 1;
-    w.lim_low = row0 <= last ? before + (causal ? (int)((unsigned)row0 / per) : 0) : 0;
-    w.lim_high = row0 <= last ? before + (causal ? (int)((unsigned)last / per) : 0) : 0;
+    if constexpr (TREE) {
+        w.first = x.len - (x.rows.end - x.rows.begin);
+        w.lim_low = row0 <= last ? w.first : 0;
+        w.lim_high = row0 <= last ? x.len : 0;
+        w.tree = reinterpret_cast<const uint32_t *>(a.tree);
+        w.tree_words = 2 * a.tree_words;
+    } else {
+        w.lim_low = row0 <= last ? before + (causal ? (int)((unsigned)row0 / per) : 0) : 0;
+        w.lim_high = row0 <= last ? before + (causal ? (int)((unsigned)last / per) : 0) : 0;
+    }
     uint4 raw[RT][D / 32];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -516,7 +528,7 @@ __device__ __forceinline__ void begin(Wave<D, G, RT, BASE_FRAGS> &w, const AttnA
         const bool have = row < x.n_rows;
         const int tok = have ? (int)((unsigned)row / per) : 0, hq = h * a.per + (have ? row - tok * a.per : 0);
         const uint16_t *q = a.q + (x.rows.begin + tok) * a.q_ts + hq * a.q_hs + 8 * quad;
-        w.lim[t] = !have ? 0 : before + (causal ? tok : 0);
+        w.lim[t] = TREE ? x.rows.begin + tok : !have ? 0 : before + (causal ? tok : 0);
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
             raw[t][m] = uint4{0, 0, 0, 0};
@@ -565,10 +577,21 @@ struct Places {
 };
 
 // Whether all of a step's 32 tokens from t0 are there, for all of the wave's rows.
-template <int D, int G, int RT, bool BASE_FRAGS>
-__device__ __forceinline__ bool all_there(const Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2])
+template <int D, int G, int RT, bool BASE_FRAGS, bool TREE>
+__device__ __forceinline__ bool all_there(const Wave<D, G, RT, BASE_FRAGS, TREE> &w, int t0, const int (&good)[2])
 {
     return t0 + kTile <= w.lim_low && good[0] >= 16 && good[1] >= 16;
+}
+
+// Which of the four tokens from position `at` the lane's row of 16 rows t sees, in the low bits: all
+// before the call's own, those of its mask's bits, none behind its words.
+template <int D, int G, int RT, bool BASE_FRAGS>
+__device__ __forceinline__ uint32_t four_seen(const Wave<D, G, RT, BASE_FRAGS, true> &w, int t, int at)
+{
+    const int bit = at - w.first, k = bit >> 5;
+    const uint32_t *mask = w.tree + (int64_t)w.lim[t] * w.tree_words;
+    const auto word = [&](int k) { return k < 0 ? ~0u : k < w.tree_words ? mask[k] : 0u; };
+    return (uint32_t)(((uint64_t)word(k + 1) << 32 | word(k)) >> (bit & 31));
 }
 
 // The scores of 32 tokens from t0 for the wave's rows, to base 2 and less m, good[half] of each 16
@@ -576,8 +599,8 @@ __device__ __forceinline__ bool all_there(const Wave<D, G, RT, BASE_FRAGS> &w, i
 // gives {step * scale, base} of a lane's place; key(half, mm) the A fragments. after_keys() is
 // called when no more keys are needed. With BASE_FRAGS base(half, p) is the A fragment of the bases
 // (base_query has the other), and what key_grid says of them is not used.
-template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename KeyGrid, typename Base, typename Key, typename After>
-__device__ __forceinline__ void scores(const Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], bool open,
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, bool TREE, typename KeyGrid, typename Base, typename Key, typename After>
+__device__ __forceinline__ void scores(const Wave<D, G, RT, BASE_FRAGS, TREE> &w, int t0, const int (&good)[2], bool open,
                                        KeyGrid key_grid, Base base, Key key, After after_keys, float (&s)[RT][8])
 {
     constexpr bool kBf16 = Types<T>::kBf16;
@@ -647,7 +670,12 @@ __device__ __forceinline__ void scores(const Wave<D, G, RT, BASE_FRAGS> &w, int 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int at = first + 16 * (i >> 2) + (i & 3);
-                if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
+                if constexpr (TREE) {
+                    const uint32_t seen = i < 4 ? four_seen(w, t, first) : four_seen(w, t, first + 16);
+                    if (at >= t0 + 16 * (i >> 2) + good[i >> 2] || !(seen >> (i & 3) & 1)) s[t][i] = -INFINITY;
+                } else {
+                    if (at >= min(w.lim[t], t0 + 16 * (i >> 2) + good[i >> 2])) s[t][i] = -INFINITY;
+                }
             }
     }
 }
@@ -694,9 +722,9 @@ __device__ __forceinline__ void weigh(Group g, const f32x2 (&v)[REGS], const flo
 // close() is called first, to make the grids of the missing ones {0, 0}. value_grid gives {step,
 // middle} of a lane's place and value(j) the A fragments, behind after_keys(); the others are as in
 // scores().
-template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, bool TREE, typename Close, typename KeyGrid, typename Base, typename Key,
           typename After, typename ValueGrid, typename Value>
-__device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
+__device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS, TREE> &w, int t0, const int (&good)[2], Close close, KeyGrid key_grid,
                                             Base base, Key key, After after_keys, ValueGrid value_grid, Value value)
 {
     constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
@@ -826,9 +854,9 @@ __device__ __forceinline__ void attend_step(Wave<D, G, RT, BASE_FRAGS> &w, int t
 // values went to memory). Such tokens take about twice a step: 64 sequences of 4100 to 8190 tokens,
 // 8 heads of 128, 4 bits 106 us without any, 114 with one token in 1000 and 199 with every third
 // far below the others; 2 x 500 rows over 3500 to 4000 tokens, 40 heads 170, 232 and 472.
-template <typename T, int D, int G, int RT, bool BASE_FRAGS, typename Close, typename KeyGrid, typename Base, typename Key,
+template <typename T, int D, int G, int RT, bool BASE_FRAGS, bool TREE, typename Close, typename KeyGrid, typename Base, typename Key,
           typename ValueGrid, typename Value>
-__device__ __forceinline__ void attend_rest(Wave<D, G, RT, BASE_FRAGS> &w, float &by, int t0, const int (&good)[2], Close close,
+__device__ __forceinline__ void attend_rest(Wave<D, G, RT, BASE_FRAGS, TREE> &w, float &by, int t0, const int (&good)[2], Close close,
                                             KeyGrid key_grid, Base base, Key key, ValueGrid value_grid, Value value)
 {
     constexpr int kGroups = D / G, kRegs = Places<D, G>::kRegs;
@@ -936,8 +964,8 @@ constexpr int kPartPad = 4;
 // maxima, and writes it: waves TW * r .. TW * r + TW - 1 have rows 16 * RT * r .. of the item.
 // ml: [WAVES][16 * RT][2]; part: [WAVES][16][part_dims + kPartPad]. Blocks come and leave in
 // step.
-template <typename T, int D, int G, int RT, int TW, int WAVES, bool BASE_FRAGS>
-__device__ __forceinline__ void finish(Wave<D, G, RT, BASE_FRAGS> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
+template <typename T, int D, int G, int RT, int TW, int WAVES, bool BASE_FRAGS, bool TREE>
+__device__ __forceinline__ void finish(Wave<D, G, RT, BASE_FRAGS, TREE> &w, const AttnArgs &a, const AttnSide &d, const Item &x, int h, int run,
                                        float *ml, float *part)
 {
     constexpr int kGroups = D / G, kPart = part_dims(D), kStride = kPart + kPartPad;
@@ -1112,7 +1140,7 @@ __device__ __forceinline__ Place place_of(const AttnArgs &a)
 // of 8 bits, 277 MB: 45 us, 6.2 TB/s; 300 tokens of 32 heads: 9.8 us, four loads that wait for
 // each other (lengths, pages, codes, and the instructions themselves) and three steps one after
 // another.
-template <typename T, int NB, int D, int G, int RT>
+template <typename T, int NB, int D, int G, int RT, bool TREE>
 __global__ __launch_bounds__(64 * kWaves, blocks_per_cu(RT, D, NB) * kWaves / 4) void attn_kernel(AttnArgs a)       // waves to a SIMD
 {
     constexpr int kRows = 16 * RT;
@@ -1136,10 +1164,10 @@ __global__ __launch_bounds__(64 * kWaves, blocks_per_cu(RT, D, NB) * kWaves / 4)
     for (int u = first_unit(place.run, W, layout.total); u < u_end;) {
         const Item x = layout.item(u, u_end);
         u += x.count;
-        Wave<D, G, RT, false> w;
+        Wave<D, G, RT, false, TREE> w;
         // what the last of the item's rows sees
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
-        const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
+        const int seen = d.causal && !TREE ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * layout.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[2][Spot<NB, D, G>::kKeyBytes / 4], vw[2][Spot<NB, D, G>::kValBytes];
@@ -1267,7 +1295,7 @@ constexpr size_t wide_bytes()       // of the steps, or of what joins the waves 
     return ((steps > part ? steps : part) + 15) & ~size_t(15);
 }
 
-template <typename T, int NB, int D, int G, int TW>
+template <typename T, int NB, int D, int G, int TW, bool TREE>
 __global__ __launch_bounds__(64 * wide_waves<D>(), blocks_per_cu(wide_waves<D>() / TW, D, NB) * wide_waves<D>() / 4) void attn_wide_kernel(AttnArgs a)
 {
     constexpr int kWide = wide_waves<D>(), kRows = 16 * (kWide / TW), kTurns = 2 / TW, kBuffers = wide_buffers<D>();
@@ -1296,10 +1324,10 @@ __global__ __launch_bounds__(64 * wide_waves<D>(), blocks_per_cu(wide_waves<D>()
     for (int u = first_unit(place.run, W, layout.total); u < u_end; layout.again()) {
         const Item x = layout.item(u, u_end);
         u += x.count;
-        Wave<D, G, 1, true> w;
+        Wave<D, G, 1, true, TREE> w;
         // what the block's rows see: the same for its waves, which go in step
         const int last = (int)((unsigned)(min(x.row0 + kRows, x.n_rows) - 1) / (unsigned)a.per);
-        const int seen = d.causal ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
+        const int seen = d.causal && !TREE ? x.len - (x.rows.end - x.rows.begin) + last + 1 : x.len;
         const int t_end = (int)min((int64_t)(x.u_in + x.count) * layout.unit, (int64_t)seen);
         const int32_t *table = d.s.table + (int64_t)x.b * d.s.max_pages;
         uint32_t kw[Spot<NB, D, G>::kKeyBytes / 4 / kParts], vw[Spot<NB, D, G>::kValBytes], kg[kRegs], vg[kRegs];
@@ -1436,55 +1464,55 @@ inline dim3 grid_of(const AttnArgs &a)
     return dim3((unsigned)(runs * a.c.heads));
 }
 
-template <typename T, int NB, int D, int G, int RT>
+template <typename T, int NB, int D, int G, int RT, bool TREE>
 hipError_t launch_few(const AttnArgs &a, hipStream_t stream)
 {
     const size_t lds = starts_bytes(a) + 4 * kWaves * 16 * RT * 2 + 4 * (size_t)kWaves * 16 * (part_dims(D) + kPartPad);
-    attn_kernel<T, NB, D, G, RT><<<grid_of(a), 64 * kWaves, lds, stream>>>(a);
+    attn_kernel<T, NB, D, G, RT, TREE><<<grid_of(a), 64 * kWaves, lds, stream>>>(a);
     return hipGetLastError();
 }
 
-template <typename T, int NB, int D, int G, int TW>
+template <typename T, int NB, int D, int G, int TW, bool TREE>
 hipError_t launch_many(const AttnArgs &a, hipStream_t stream)
 {
     const int waves = wide_waves<D>();
     const size_t lds = wide_bytes<D, G>() + 4 * waves * 16 * 2 + starts_bytes(a);
-    attn_wide_kernel<T, NB, D, G, TW><<<grid_of(a), 64 * waves, lds, stream>>>(a);
+    attn_wide_kernel<T, NB, D, G, TW, TREE><<<grid_of(a), 64 * waves, lds, stream>>>(a);
     return hipGetLastError();
 }
 
-template <typename T, int NB, int D, int G>
+template <typename T, int NB, int D, int G, bool TREE>
 hipError_t by_tiles(const AttnArgs &a, hipStream_t stream)
 {
     // rows to a tile: 16, 32 or 128, and 16, 32 or 64 of 256-wide heads (whose sums fill the registers)
     const int n = a.side[0].tiles16;
-    if (n == 1) return launch_few<T, NB, D, G, 1>(a, stream);
+    if (n == 1) return launch_few<T, NB, D, G, 1, TREE>(a, stream);
     if constexpr (D <= 128) {
-        if (n == 2) return launch_few<T, NB, D, G, 2>(a, stream);
-        if (n == 8) return launch_many<T, NB, D, G, 1>(a, stream);
+        if (n == 2) return launch_few<T, NB, D, G, 2, TREE>(a, stream);
+        if (n == 8) return launch_many<T, NB, D, G, 1, TREE>(a, stream);
     } else {
-        if (n == 2) return launch_many<T, NB, D, G, 2>(a, stream);
-        if (n == 4) return launch_many<T, NB, D, G, 1>(a, stream);
+        if (n == 2) return launch_many<T, NB, D, G, 2, TREE>(a, stream);
+        if (n == 4) return launch_many<T, NB, D, G, 1, TREE>(a, stream);
     }
     return hipErrorInvalidValue;
 }
 
-template <typename T, int NB, int D>
+template <typename T, int NB, int D, bool TREE>
 hipError_t by_group(const AttnArgs &a, int g, hipStream_t stream)
 {
-    if (g == 32) return by_tiles<T, NB, D, 32>(a, stream);
-    if (g == 64) return by_tiles<T, NB, D, 64>(a, stream);
+    if (g == 32) return by_tiles<T, NB, D, 32, TREE>(a, stream);
+    if (g == 64) return by_tiles<T, NB, D, 64, TREE>(a, stream);
     if constexpr (D >= 128)
-        if (g == 128) return by_tiles<T, NB, D, 128>(a, stream);
+        if (g == 128) return by_tiles<T, NB, D, 128, TREE>(a, stream);
     return hipErrorInvalidValue;
 }
 
-template <typename T, int NB>
+template <typename T, int NB, bool TREE>
 hipError_t by_dim(const AttnArgs &a, const AttnShape &x, hipStream_t stream)
 {
-    if (x.dim == 64) return by_group<T, NB, 64>(a, x.g, stream);
-    if (x.dim == 128) return by_group<T, NB, 128>(a, x.g, stream);
-    return by_group<T, NB, 256>(a, x.g, stream);
+    if (x.dim == 64) return by_group<T, NB, 64, TREE>(a, x.g, stream);
+    if (x.dim == 128) return by_group<T, NB, 128, TREE>(a, x.g, stream);
+    return by_group<T, NB, 256, TREE>(a, x.g, stream);
 }
 
 }  // namespace

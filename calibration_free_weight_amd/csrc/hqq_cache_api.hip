@@ -1,5 +1,6 @@
 // hqq_cache_api.hip -- the C entry points of the quantized key/value cache: argument checks,
 // the workspace plan of attention, and the launch sequences.
+#include <algorithm>
 #include <cmath>
 
 #include "hqq.h"
@@ -109,6 +110,15 @@ hqq_status cache_rows(bool write, const hqq_cache *cache, const hqq_seqs *seqs, 
     return done(hqq::launch_cache_rows(write, view_of(cache), view_of(cache, seqs), p, cache->head_dim,
                                        cache->nbits, cache->group_size, cache->dtype == HQQ_BF16,
                                        static_cast<hipStream_t>(stream)));
+}
+
+constexpr int kMaxCaches = 1024;
+
+// What the caches of a call must have in common.
+bool alike(const hqq_cache &a, const hqq_cache &b)
+{
+    return a.n_pages == b.n_pages && a.page_size == b.page_size && a.n_heads == b.n_heads && a.head_dim == b.head_dim &&
+           a.nbits == b.nbits && a.group_size == b.group_size && a.dtype == b.dtype;
 }
 
 // ---- attention --------------------------------------------------------------------------------
@@ -250,37 +260,12 @@ hqq::AttnSide side_at(const hqq::SeqView &s, const SidePlan &p, char *ws, bool t
                          p.workers, p.unit, p.tiles16, causal};
 }
 
-}  // namespace
-
-extern "C" {
-
-hqq_status hqq_cache_write(const hqq_cache *cache, const hqq_seqs *seqs, const void *k, int64_t k_token_stride,
-                           int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
-                           void *stream)
-{
-    return cache_rows(true, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
-}
-
-hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k, int64_t k_token_stride,
-                          int64_t k_head_stride, void *v, int64_t v_token_stride, int64_t v_head_stride,
-                          void *stream)
-{
-    return cache_rows(false, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
-}
-
-size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs, int n_q_heads, int64_t prefix_len)
-{
-    bool empty;
-    if (check_plan(cache, seqs, n_q_heads, prefix_len, &empty) != HQQ_OK) return 0;
-    hqq::report_error(HQQ_OK, "");
-    return empty ? 0 : plan_of(cache, seqs, n_q_heads, prefix_len).bytes;
-}
-
-hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *seqs, const int32_t *prefix_pages,
-                                      int n_prefix_pages, int64_t prefix_len, const void *q, int64_t q_token_stride,
-                                      int64_t q_head_stride, int n_q_heads, float scale, void *out,
-                                      int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
-                                      size_t workspace_bytes, void *stream)
+// The three attention calls: a prefix of prefix_len tokens, or masks of the call's own tokens, or
+// neither.
+hqq_status attention(const hqq_cache *cache, const hqq_seqs *seqs, const int32_t *prefix_pages, int n_prefix_pages,
+                     int64_t prefix_len, const uint64_t *tree, int tree_words, const void *q, int64_t q_token_stride,
+                     int64_t q_head_stride, int n_q_heads, float scale, void *out, int64_t out_token_stride,
+                     int64_t out_head_stride, float *lse, void *workspace, size_t workspace_bytes, void *stream)
 {
     bool empty;
     hqq_status st = check_plan(cache, seqs, n_q_heads, prefix_len, &empty);
@@ -321,6 +306,8 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     a.o_hs = out_head_stride;
     a.per = n_q_heads / cache->n_heads;
     a.scale = scale * kLog2e;
+    a.tree = tree;
+    a.tree_words = tree_words;
     hqq::JoinArgs j{{a.side[0], {}}, 1, a.out, lse, a.o_ts, a.o_hs, a.per, cache->n_heads, cache->head_dim};
     hipError_t e = hipSuccess;
     if (shared) {
@@ -343,13 +330,100 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
     return done(e);
 }
 
+}  // namespace
+
+extern "C" {
+
+hqq_status hqq_cache_write(const hqq_cache *cache, const hqq_seqs *seqs, const void *k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                           void *stream)
+{
+    return cache_rows(true, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
+}
+
+hqq_status hqq_cache_read(const hqq_cache *cache, const hqq_seqs *seqs, void *k, int64_t k_token_stride,
+                          int64_t k_head_stride, void *v, int64_t v_token_stride, int64_t v_head_stride,
+                          void *stream)
+{
+    return cache_rows(false, cache, seqs, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, stream);
+}
+
+hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs *seqs, const int32_t *kept,
+                          int max_kept, int32_t *lens_out, void *stream)
+{
+    if (n_caches < 1 || n_caches > kMaxCaches || !caches) return refuse("caches must be 1 to 1024 caches");
+    const void *codes[kMaxCaches];
+    for (int i = 0; i < n_caches; ++i) {
+        const hqq_status st = check_cache(caches + i);
+        if (st != HQQ_OK) return st;
+        if (!alike(caches[0], caches[i])) return refuse("the caches of a call must have the same sizes and type");
+        codes[i] = caches[i].k_codes;
+    }
+    // moved twice, a token would go on to where the first move found another
+    std::sort(codes, codes + n_caches);
+    if (std::adjacent_find(codes, codes + n_caches) != codes + n_caches) return refuse("the caches of a call must differ");
+    const hqq_status st = check_seqs(caches, seqs);
+    if (st != HQQ_OK) return st;
+    if (max_kept < 0 || max_kept > (1 << 24)) return refuse("max_kept must be in [0, 2^24]");
+    if (seqs->n_seqs == 0) return done(hipSuccess);
+    if (max_kept > 0 && (!kept || !aligned(kept, 4))) return refuse("kept must be non-null and 4-byte aligned");
+    if (!seqs->lens || !aligned(seqs->lens, 4) || !aligned(seqs->cu_tokens, 4) || !aligned(lens_out, 4))
+        return refuse("lens must be non-null, and lens, cu_tokens and lens_out 4-byte aligned");
+    if (lens_out == seqs->lens) return refuse("lens_out must not be lens");
+    hqq::KeepArgs a{view_of(caches, seqs), kept, lens_out, max_kept, caches->n_heads, caches->head_dim / caches->group_size, {}};
+    hipError_t e = hipSuccess;
+    for (int first = 0; first < n_caches && e == hipSuccess; first += hqq::kKeepLayers) {
+        const int n = n_caches - first < hqq::kKeepLayers ? n_caches - first : hqq::kKeepLayers;
+        for (int i = 0; i < n; ++i) {
+            const hqq_cache &c = caches[first + i];
+            void *const part[4] = {c.k_codes, c.v_codes, c.k_meta, c.v_meta};
+            for (int k = 0; k < 4; ++k) a.layers[i].part[k] = static_cast<uint8_t *>(part[k]);
+        }
+        e = hqq::launch_keep(a, n, caches->head_dim, caches->nbits, static_cast<hipStream_t>(stream));
+        a.lens_out = nullptr;       // the first launch has written them
+    }
+    return done(e);
+}
+
+size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs, int n_q_heads, int64_t prefix_len)
+{
+    bool empty;
+    if (check_plan(cache, seqs, n_q_heads, prefix_len, &empty) != HQQ_OK) return 0;
+    hqq::report_error(HQQ_OK, "");
+    return empty ? 0 : plan_of(cache, seqs, n_q_heads, prefix_len).bytes;
+}
+
+hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *seqs, const int32_t *prefix_pages,
+                                      int n_prefix_pages, int64_t prefix_len, const void *q, int64_t q_token_stride,
+                                      int64_t q_head_stride, int n_q_heads, float scale, void *out,
+                                      int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
+                                      size_t workspace_bytes, void *stream)
+{
+    return attention(cache, seqs, prefix_pages, n_prefix_pages, prefix_len, nullptr, 0, q, q_token_stride, q_head_stride,
+                     n_q_heads, scale, out, out_token_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
+}
+
 hqq_status hqq_cache_attention(const hqq_cache *cache, const hqq_seqs *seqs, const void *q, int64_t q_token_stride,
                                int64_t q_head_stride, int n_q_heads, float scale, void *out,
                                int64_t out_token_stride, int64_t out_head_stride, float *lse, void *workspace,
                                size_t workspace_bytes, void *stream)
 {
-    return hqq_cache_attention_prefix(cache, seqs, nullptr, 0, 0, q, q_token_stride, q_head_stride, n_q_heads, scale,
-                                      out, out_token_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
+    return attention(cache, seqs, nullptr, 0, 0, nullptr, 0, q, q_token_stride, q_head_stride, n_q_heads, scale, out,
+                     out_token_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
+}
+
+hqq_status hqq_cache_attention_tree(const hqq_cache *cache, const hqq_seqs *seqs, const uint64_t *tree, int tree_words,
+                                    const void *q, int64_t q_token_stride, int64_t q_head_stride, int n_q_heads,
+                                    float scale, void *out, int64_t out_token_stride, int64_t out_head_stride,
+                                    float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    bool empty;
+    const hqq_status st = check_plan(cache, seqs, n_q_heads, 0, &empty);
+    if (st != HQQ_OK) return st;
+    if (tree_words < 1 || tree_words > 256) return refuse("tree_words must be in [1, 256]");
+    if (!empty && (!tree || !aligned(tree, 8))) return refuse("tree must be non-null and 8-byte aligned");
+    return attention(cache, seqs, nullptr, 0, 0, tree, tree_words, q, q_token_stride, q_head_stride, n_q_heads, scale,
+                     out, out_token_stride, out_head_stride, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -102,6 +102,20 @@ inline int64_t cache_rows_blocks(bool write, int64_t n_tokens, int heads, int di
 hipError_t launch_cache_rows(bool write, const CacheView &c, const SeqView &s, const RowPtrs &p,
                              int dim, int nbits, int g, bool bf16, hipStream_t stream);
 
+// ---- accepted tokens kept -----------------------------------------------------------------------
+constexpr int kKeepLayers = 64;             // of a launch: 2 KB of arguments
+struct KeepArgs {
+    SeqView s;
+    const int32_t *kept;        // [n_seqs][max_kept]
+    int32_t *lens_out;          // nullable
+    int32_t max_kept, heads, groups;
+    struct {
+        uint8_t *part[4];       // codes of keys and of values, grids of keys and of values
+    } layers[kKeepLayers];
+};
+
+hipError_t launch_keep(const KeepArgs &a, int n_layers, int dim, int nbits, hipStream_t stream);
+
 // ---- attention ---------------------------------------------------------------------------------
 // What the rows of a call attend to comes from one or two sides: the sequences, and a prefix
 // that all share (one sequence with all rows of the call). A run leaves at most two pieces of
@@ -130,6 +144,8 @@ struct AttnArgs {
     int64_t q_ts, q_hs, o_ts, o_hs;
     int32_t per;                // query heads to a key/value head
     float scale;                // times log2(e)
+    const uint64_t *tree;       // masks of the call's rows, tree_words each, or null
+    int32_t tree_words;
 };
 
 struct JoinArgs {
@@ -164,5 +180,9 @@ hipError_t launch_attn_f16_4(const AttnArgs &a, const AttnShape &x, hipStream_t 
 hipError_t launch_attn_f16_8(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
 hipError_t launch_attn_bf16_4(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
 hipError_t launch_attn_bf16_8(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
+hipError_t launch_attn_tree_f16_4(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
+hipError_t launch_attn_tree_f16_8(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
+hipError_t launch_attn_tree_bf16_4(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
+hipError_t launch_attn_tree_bf16_8(const AttnArgs &a, const AttnShape &x, hipStream_t stream);
 
 }  // namespace hqq

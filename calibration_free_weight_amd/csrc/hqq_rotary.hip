@@ -1,0 +1,260 @@
+// hqq_rotary.hip -- rotary positions: pairs of dimensions of queries and keys turned by their
+// token's position (gfx950), and the frequencies that they are turned by.
+//
+// (a, b) -> (a cos x - b sin x, b cos x + a sin x), x = 2 pi * position * freq. Frequencies are
+// turns in 64 bits behind the point, so that the product's low 64 bits are the part of a turn
+// that is left, whatever the position: nothing is lost at far positions, and no range is reduced.
+// Of it 32 bits are kept: 2^-33 turns, 7e-10 radians.
+#include <cmath>
+
+#include "hqq.h"
+#include "hqq_cache_internal.h"
+#include "hqq_internal.h"
+
+namespace hqq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kFewUnits = 1 << 19;
+constexpr int kMaxPairs = 2048;         // of a block's tokens: 16 KB of cosines and sines
+
+struct Tensor {
+    const uint16_t *in;
+    uint16_t *out;
+    int64_t in_ts, in_hs, out_ts, out_hs;
+    int32_t heads;
+};
+
+struct RotaryArgs {
+    Tensor x[2];
+    const uint64_t *freqs;
+    const int32_t *positions;
+    float scale;
+    int32_t n_tokens, pairs;    // rotary_dim / 2
+    int32_t per_head, units;    // units of a head, of a token
+    int32_t tokens, parts;      // tokens to a block; blocks to a token
+    int32_t rest0, dim;         // dimensions from rest0 to dim are copied
+};
+
+// Cosine and sine of a part of a turn, 2^-32 turns a step: the nearest quarter turn is taken off,
+// the rest is within pi/4, where the Taylor sums below are off by 2^-26.
+__device__ __forceinline__ float2 cos_sin(uint32_t part, float scale)
+{
+    const uint32_t quarter = (part + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(part - (quarter << 30)) * (6.283185307179586f * 0x1p-32f), y = x * x;
+    float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(y, s, 1.f / 120.f);
+    s = fmaf(y, s, -1.f / 6.f);
+    s = fmaf(x * y, s, x);
+    float c = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(y, c, -1.f / 720.f);
+    c = fmaf(y, c, 1.f / 24.f);
+    c = fmaf(y, c, -0.5f);
+    c = fmaf(y, c, 1.f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return float2{((quarter + 1) & 2 ? -a : a) * scale, (quarter & 2 ? -b : b) * scale};
+}
+
+template <typename T>
+__device__ __forceinline__ void turn(float a, float b, const float2 cs, uint32_t &first, uint32_t &second)
+{
+    first = from_f32<T>(fmaf(a, cs.x, -(b * cs.y)));
+    second = from_f32<T>(fmaf(b, cs.x, a * cs.y));
+}
+
+// Eight pairs of a head, of 16 dimensions; pairs of neighbours, or of the two halves.
+template <typename T, bool NEIGHBOURS>
+__device__ __forceinline__ void turn8(uint4 &lo, uint4 &hi, const float2 *cs)
+{
+    float a[8], b[8];
+    unpack8<T>(lo, a);
+    unpack8<T>(hi, b);
+    uint32_t x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (NEIGHBOURS) {
+            const float *p = e < 4 ? a + 2 * e : b + 2 * e - 8;
+            uint32_t *to = e < 4 ? x + 2 * e : y + 2 * e - 8;
+            turn<T>(p[0], p[1], cs[e], to[0], to[1]);
+        } else {
+            turn<T>(a[e], b[e], cs[e], x[e], y[e]);
+        }
+    }
+    lo = uint4{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
+    hi = uint4{y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16};
+}
+
+// A unit is eight pairs, or with !WIDE one; or as many dimensions that are copied. A block makes
+// the cosines and sines of its tokens once, for all heads, while its first units are on their way.
+template <typename T, bool NEIGHBOURS, bool WIDE>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
+{
+    extern __shared__ float2 cs[];      // [tokens][pairs]
+    const int t0 = (int)(blockIdx.x / (unsigned)a.parts) * a.tokens, part = (int)(blockIdx.x % (unsigned)a.parts);
+    const int tokens = min(a.tokens, a.n_tokens - t0);
+    for (int j = threadIdx.x; j < tokens * a.pairs; j += kThreads) {
+        const unsigned t = (unsigned)j / (unsigned)a.pairs, i = j - t * a.pairs;
+        const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + t] * a.freqs[i];
+        cs[j] = cos_sin((uint32_t)((turns + 0x80000000u) >> 32), a.scale);
+    }
+    __syncthreads();
+    const int turning = WIDE ? a.pairs / 8 : a.pairs;       // units of a head
+    for (int j = part * kThreads + threadIdx.x; j < tokens * a.units; j += a.parts * kThreads) {
+        const unsigned t = (unsigned)j / (unsigned)a.units, of_token = j - t * a.units;
+        unsigned h = of_token / (unsigned)a.per_head;
+        const int u = of_token - h * a.per_head;
+        const bool second = h >= (unsigned)a.x[0].heads;
+        const Tensor &x = a.x[second];
+        if (second) h -= a.x[0].heads;
+        const uint16_t *in = x.in + (t0 + (int64_t)t) * x.in_ts + h * x.in_hs;
+        uint16_t *out = x.out + (t0 + (int64_t)t) * x.out_ts + h * x.out_hs;
+        const float2 *c = cs + t * a.pairs;
+        if constexpr (WIDE) {
+            if (u < turning) {
+                const int d0 = NEIGHBOURS ? 16 * u : 8 * u, d1 = NEIGHBOURS ? d0 + 8 : d0 + a.pairs;
+                uint4 lo = *reinterpret_cast<const uint4 *>(in + d0), hi = *reinterpret_cast<const uint4 *>(in + d1);
+                turn8<T, NEIGHBOURS>(lo, hi, c + 8 * u);
+                *reinterpret_cast<uint4 *>(out + d0) = lo;
+                *reinterpret_cast<uint4 *>(out + d1) = hi;
+            } else {
+                const int d = a.rest0 + 8 * (u - turning);
+                *reinterpret_cast<uint4 *>(out + d) = *reinterpret_cast<const uint4 *>(in + d);
+            }
+        } else {
+            if (u < turning) {
+                const int d0 = NEIGHBOURS ? 2 * u : u, d1 = NEIGHBOURS ? d0 + 1 : d0 + a.pairs;
+                uint32_t p, q;
+                turn<T>(to_f32<T>(in[d0]), to_f32<T>(in[d1]), c[u], p, q);
+                out[d0] = (uint16_t)p;
+                out[d1] = (uint16_t)q;
+            } else {
+                const int d = a.rest0 + (u - turning);
+                out[d] = in[d];
+            }
+        }
+    }
+}
+
+template <typename T, bool NEIGHBOURS>
+void launch(const RotaryArgs &a, bool wide, unsigned blocks, hipStream_t stream)
+{
+    const size_t lds = (size_t)a.tokens * a.pairs * sizeof(float2);
+    if (wide) rotary_kernel<T, NEIGHBOURS, true><<<blocks, kThreads, lds, stream>>>(a);
+    else rotary_kernel<T, NEIGHBOURS, false><<<blocks, kThreads, lds, stream>>>(a);
+}
+
+hqq_status refuse(const char *msg)
+{
+    report_error(HQQ_ERR_ARG, msg);
+    return HQQ_ERR_ARG;
+}
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+}  // namespace hqq
+
+extern "C" {
+
+hqq_status hqq_rotary_frequencies(int rotary_dim, double theta, double factor, int64_t original_len, double low,
+                                  double high, uint64_t *freqs)
+{
+    using namespace hqq;
+    if (rotary_dim < 2 || rotary_dim > 1024 || rotary_dim % 2) return refuse("rotary_dim must be even, in [2, 1024]");
+    if (!(theta >= 1.0) || !std::isfinite(theta)) return refuse("theta must be finite, at least 1");
+    if (!(factor >= 1.0) || !std::isfinite(factor)) return refuse("factor must be finite, at least 1");
+    if (original_len < 0) return refuse("original_len must not be negative");
+    if (original_len > 0 && (!(low >= 0.0) || !(high > low) || !std::isfinite(high)))
+        return refuse("low and high must be finite, with 0 <= low < high");
+    if (!freqs) return refuse("freqs must be non-null");
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        const long double turns = std::pow((long double)theta, -2.0L * i / rotary_dim) / 6.283185307179586476925286766559L;
+        long double s = 0.0L;
+        if (original_len > 0) {
+            s = (original_len * turns - low) / ((long double)high - low);
+            s = s < 0.0L ? 0.0L : s > 1.0L ? 1.0L : s;
+        }
+        freqs[i] = (uint64_t)std::ldexp(turns * ((1.0L - s) / factor + s), 64);
+    }
+    report_error(HQQ_OK, "");
+    return HQQ_OK;
+}
+
+hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, float scale, const int32_t *positions,
+                      int64_t n_tokens, int head_dim, int dtype, const hqq_rotary_rows *rows, int n_rows, void *stream)
+{
+    using namespace hqq;
+    if (rotary_dim < 2 || rotary_dim % 2 || head_dim > 1024 || rotary_dim > head_dim)
+        return refuse("rotary_dim must be even, 2 at least and head_dim at most, and head_dim 1024 at most");
+    if (dtype != HQQ_F16 && dtype != HQQ_BF16) return refuse("dtype must be HQQ_F16 or HQQ_BF16");
+    if (interleaved != 0 && interleaved != 1) return refuse("interleaved must be 0 or 1");
+    if (!std::isfinite(scale)) return refuse("scale must be finite");
+    if (n_tokens < 0 || n_tokens > (1 << 24)) return refuse("n_tokens must be in [0, 2^24]");
+    if (n_rows < 0 || n_rows > 2 || (n_rows > 0 && !rows)) return refuse("rows must be one or two tensors");
+    RotaryArgs a{};
+    bool wide = rotary_dim % 16 == 0 && head_dim % 8 == 0, rest = false;
+    int heads = 0;
+    for (int i = 0; i < n_rows; ++i) {
+        const hqq_rotary_rows &r = rows[i];
+        if (r.n_heads < 0 || r.n_heads > 4096) return refuse("rows: n_heads must be in [0, 4096]");
+        if (r.n_heads == 0 || n_tokens == 0) continue;
+        if (!r.in || !r.out) return refuse("rows: in and out must be non-null");
+        if (!aligned(r.in, 2) || !aligned(r.out, 2)) return refuse("rows: in and out must be 2-byte aligned");
+        const int64_t strides[] = {r.in_token_stride, r.in_head_stride, r.out_token_stride, r.out_head_stride};
+        for (int64_t s : strides) {
+            if (s < 0 || s > (int64_t(1) << 36)) return refuse("rows: strides must be in [0, 2^36]");
+            wide = wide && s % 8 == 0;
+        }
+        wide = wide && aligned(r.in, 16) && aligned(r.out, 16);
+        if (r.in == r.out) {
+            if (strides[0] != strides[2] || strides[1] != strides[3])
+                return refuse("rows: in place, the strides of in and out must be the same");
+        } else {
+            rest = true;
+        }
+        a.x[heads > 0] = Tensor{static_cast<const uint16_t *>(r.in), static_cast<uint16_t *>(r.out),
+                                strides[0], strides[1], strides[2], strides[3], r.n_heads};
+        heads += r.n_heads;
+    }
+    if (heads == 0 || n_tokens == 0) {
+        report_error(HQQ_OK, "");
+        return HQQ_OK;
+    }
+    if (!freqs || !positions || !aligned(freqs, 8) || !aligned(positions, 4))
+        return refuse("freqs and positions must be non-null, 8- and 4-byte aligned");
+    const int turning = rotary_dim / (wide ? 16 : 2);
+    a.freqs = freqs;
+    a.positions = positions;
+    a.scale = scale;
+    a.n_tokens = (int32_t)n_tokens;
+    a.pairs = rotary_dim / 2;
+    a.per_head = turning + (rest ? (head_dim - rotary_dim) / (wide ? 8 : 1) : 0);
+    a.units = a.per_head * heads;
+    a.rest0 = rotary_dim;
+    a.dim = head_dim;
+    // A unit to a thread, four where there are many; with fewer than a block's in a token, several tokens.
+    const int most = n_tokens * a.units <= kFewUnits ? kThreads : 4 * kThreads;
+    a.tokens = most / a.units < kMaxPairs / a.pairs ? most / a.units : kMaxPairs / a.pairs;
+    if (a.tokens < 1) a.tokens = 1;
+    if (a.tokens > a.n_tokens) a.tokens = a.n_tokens;
+    a.parts = a.tokens > 1 ? 1 : (a.units + most - 1) / most;
+    const int64_t blocks = (n_tokens + a.tokens - 1) / a.tokens * a.parts;
+    if (blocks >= (1 << 24)) {
+        report_error(HQQ_ERR_UNSUPPORTED, "too many rows for one call");
+        return HQQ_ERR_UNSUPPORTED;
+    }
+    const hipStream_t str = static_cast<hipStream_t>(stream);
+    if (dtype == HQQ_BF16) {
+        if (interleaved) launch<Bf16, true>(a, wide, (unsigned)blocks, str);
+        else launch<Bf16, false>(a, wide, (unsigned)blocks, str);
+    } else {
+        if (interleaved) launch<F16, true>(a, wide, (unsigned)blocks, str);
+        else launch<F16, false>(a, wide, (unsigned)blocks, str);
+    }
+    const hipError_t e = hipGetLastError();
+    const hqq_status st = e == hipSuccess ? HQQ_OK : HQQ_ERR_DEVICE;
+    report_error(st, e == hipSuccess ? "" : hipGetErrorString(e));
+    return st;
+}
+
+}  // extern "C"

@@ -25,7 +25,9 @@ EXPORTS = ("hqq_packed_bytes", "hqq_workspace_bytes", "hqq_quantize", "hqq_quant
            "hqq_dequantize_scales", "hqq_pack", "hqq_unpack", "hqq_status_string",
            "hqq_last_error", "hqq_batch_check", "hqq_debug_solver", "hqq_quantize_noalloc",
            "hqq_gemm_multi", "hqq_cache_write", "hqq_cache_read", "hqq_cache_attention",
-           "hqq_cache_attention_prefix", "hqq_cache_attention_workspace")
+           "hqq_cache_attention_prefix", "hqq_cache_attention_workspace",
+           "hqq_cache_attention_tree", "hqq_cache_keep", "hqq_rotary_frequencies", "hqq_rotary",
+           "hqq_prompt_attention")
 
 
 class HQQError(RuntimeError):
@@ -59,6 +61,12 @@ class hqq_cache(C.Structure):
 class hqq_seqs(C.Structure):
     _fields_ = [("table", C.c_void_p), ("lens", C.c_void_p), ("cu_tokens", C.c_void_p),
                 ("n_seqs", C.c_int), ("max_pages", C.c_int), ("n_tokens", C.c_int64)]
+
+
+class hqq_rotary_rows(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("in_token_stride", C.c_int64), ("in_head_stride", C.c_int64),
+                ("out", C.c_void_p), ("out_token_stride", C.c_int64), ("out_head_stride", C.c_int64),
+                ("n_heads", C.c_int)]
 
 
 _L = None
@@ -124,6 +132,17 @@ def lib():
                                                  i64, i64, vp, vp, st, vp]
         L.hqq_cache_attention_workspace.restype = st
         L.hqq_cache_attention_workspace.argtypes = [cp, sp, i32, i64]
+        L.hqq_cache_attention_tree.restype = i32
+        L.hqq_cache_attention_tree.argtypes = [cp, sp, vp, i32, vp, i64, i64, i32, f32, vp, i64, i64, vp, vp, st, vp]
+        L.hqq_cache_keep.restype = i32
+        L.hqq_cache_keep.argtypes = [cp, i32, sp, vp, i32, vp, vp]
+        L.hqq_rotary_frequencies.restype = i32
+        L.hqq_rotary_frequencies.argtypes = [i32, C.c_double, C.c_double, i64, C.c_double, C.c_double, vp]
+        L.hqq_rotary.restype = i32
+        L.hqq_rotary.argtypes = [vp, i32, i32, f32, vp, i64, i32, i32, vp, i32, vp]
+        L.hqq_prompt_attention.restype = i32
+        L.hqq_prompt_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i32, i32, i32, i32, vp,
+                                           i32, f32, vp, i64, i64, vp, vp]
         L.hqq_status_string.restype = C.c_char_p
         L.hqq_status_string.argtypes = [i32]
         L.hqq_last_error.restype = C.c_char_p
@@ -450,7 +469,8 @@ def _on_stream(dev, stream, make):
         return make()
 
 
-def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream):
+def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream,
+               tree=None):
     T = _torch or _th()
     c, dev, dtype = _cache_struct(cache)
     shape = q.shape
@@ -471,6 +491,9 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
                 not prefix_pages.is_contiguous():
             raise _bad("prefix_pages must be a contiguous int32 vector on the cache's device")
         pages, n_pages = prefix_pages.data_ptr(), prefix_pages.shape[0]
+    if tree is not None and (tree.dim() != 2 or tree.shape[0] != n or tree.dtype != T.int64 or
+                             tree.get_device() != dev or not tree.is_contiguous()):
+        raise _bad("tree must be a contiguous int64 [n_tokens, words] on the cache's device")
     L = _L or lib()
     if workspace is None:
         need = L.hqq_cache_attention_workspace(c, s, heads, prefix_len)
@@ -479,9 +502,12 @@ def _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale,
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise _bad("workspace must be contiguous, on the cache's device")
     wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    st = _on(dev, L.hqq_cache_attention_prefix, c, s, pages, n_pages, prefix_len, qp, qt, qh, heads,
-             dim ** -0.5 if scale is None else scale, op, ot, oh, None if lse is None else lse.data_ptr(),
-             wp, wb, _stream_of(dev, stream))
+    rest = (qp, qt, qh, heads, dim ** -0.5 if scale is None else scale, op, ot, oh,
+            None if lse is None else lse.data_ptr(), wp, wb, _stream_of(dev, stream))
+    if tree is not None:
+        st = _on(dev, L.hqq_cache_attention_tree, c, s, tree.data_ptr(), tree.shape[1], *rest)
+    else:
+        st = _on(dev, L.hqq_cache_attention_prefix, c, s, pages, n_pages, prefix_len, *rest)
     if st:
         _check(st)
     return out
@@ -500,6 +526,43 @@ def hqq_cache_attention_prefix(cache, table, lens, prefix_pages, prefix_len, q, 
     """hqq_cache_attention for sequences that share a prefix of prefix_len tokens, held once in
     prefix_pages (int32 [n]); table and lens are those of what follows it."""
     _attention(cache, table, lens, prefix_pages, prefix_len, q, out, lse, scale, cu_tokens, workspace, stream)
+
+
+def hqq_cache_attention_tree(cache, table, lens, tree, q, out, lse=None, scale=None, cu_tokens=None,
+                             workspace=None, stream=None) -> None:
+    """hqq_cache_attention for drafted trees: a row sees what came before the call's tokens and, of
+    these, the ones whose bits are set in its row of tree (int64 [n_tokens, words], bit j % 64 of
+    word j // 64 for its sequence's row j)."""
+    if tree is None:
+        raise _bad("tree must be a contiguous int64 [n_tokens, words] on the cache's device")
+    _attention(cache, table, lens, None, 0, q, out, lse, scale, cu_tokens, workspace, stream, tree)
+
+
+def hqq_cache_keep(caches, table, lens, kept, n_tokens, lens_out=None, cu_tokens=None, stream=None) -> None:
+    """Move the accepted tokens of the last call (its n_tokens rows are the last tokens of their
+    sequences) behind what was there before it, in `caches`, one cache or the list of all layers'.
+    kept: int32 [n_seqs, max_kept], for each sequence the accepted rows by their number, ascending,
+    with -1 behind the last. lens_out (int32 [n_seqs], not lens) gets the new lengths."""
+    T = _torch or _th()
+    caches = [caches] if isinstance(caches, dict) else list(caches)
+    if not caches:
+        raise _bad("caches must be one cache or more")
+    structs, devs, types = zip(*(_cache_struct(c) for c in caches))
+    dev = devs[0]
+    if any(d != dev for d in devs):
+        raise _bad("the caches must be on one GPU")
+    s = _seqs_struct(table, lens, cu_tokens, n_tokens, dev)
+    n = table.shape[0]
+    if kept.dim() != 2 or kept.shape[0] != n or kept.dtype != T.int32 or kept.get_device() != dev or \
+            not kept.is_contiguous():
+        raise _bad("kept must be a contiguous int32 [n_seqs, max_kept] on the caches' device")
+    if lens_out is not None and (lens_out.shape != (n,) or lens_out.dtype != T.int32 or
+                                 lens_out.get_device() != dev or not lens_out.is_contiguous()):
+        raise _bad("lens_out must be a contiguous int32 [n_seqs] on the caches' device")
+    st = _on(dev, lib().hqq_cache_keep, b"".join(structs), len(structs), s, kept.data_ptr(), kept.shape[1],
+             None if lens_out is None else lens_out.data_ptr(), _stream_of(dev, stream))
+    if st:
+        _check(st)
 
 
 def alloc_cache(n_pages, page_size, n_heads, head_dim, nbits=4, group_size=64, dtype=None, device="cuda"):
@@ -536,6 +599,126 @@ def cache_attention_prefix(cache, table, lens, prefix_pages, prefix_len, q, cu_t
                            lse=None, stream=None):
     """Allocate the output (contiguous) and call hqq_cache_attention_prefix."""
     return _attention(cache, table, lens, prefix_pages, prefix_len, q, None, lse, scale, cu_tokens, None, stream)
+
+
+def cache_attention_tree(cache, table, lens, tree, q, cu_tokens=None, scale=None, lse=None, stream=None):
+    """Allocate the output (contiguous) and call hqq_cache_attention_tree."""
+    if tree is None:
+        raise _bad("tree must be a contiguous int64 [n_tokens, words] on the cache's device")
+    return _attention(cache, table, lens, None, 0, q, None, lse, scale, cu_tokens, None, stream, tree)
+
+
+def cache_keep(caches, table, lens, kept, n_tokens, cu_tokens=None, stream=None):
+    """hqq_cache_keep; returns the new lengths."""
+    T = _torch or _th()
+    out = _on_stream(lens.get_device(), stream, lambda: T.empty_like(lens))
+    hqq_cache_keep(caches, table, lens, kept, n_tokens, out, cu_tokens, stream)
+    return out
+
+
+# ---- rotary positions, and attention of prompts ----------------------------------------------
+# Rows are [n_tokens, heads, head_dim] with contiguous dimensions and any strides between tokens and
+# heads (those of attention: multiples of 8), float16 or bfloat16. Streams and what calls allocate
+# are as with the cache.
+def rotary_frequencies(rotary_dim, theta=10000.0, factor=1.0, original_len=0, low=1.0, high=4.0, device="cuda"):
+    """The frequencies of hqq_rotary, int64 [rotary_dim/2] (turns per position, 64 bits behind the
+    point): theta ** (-2 i / rotary_dim) radians; slowed by `factor` for long contexts, where
+    original_len is given only in the dimensions that turn less than `high` times over it (in full
+    those that turn `low` times at most)."""
+    T = _torch or _th()
+    n = max(int(rotary_dim) // 2, 0)
+    host = T.empty(max(n, 1), dtype=T.int64)
+    _check(lib().hqq_rotary_frequencies(rotary_dim, theta, factor, original_len, low, high, host.data_ptr()))
+    return host.to(device)
+
+
+def _turnable(x, n, dev, dtype, name, dim):
+    if x.dim() != 3 or x.shape[0] != n or x.shape[2] != dim or x.dtype != dtype or x.get_device() != dev:
+        raise _bad(f"{name} must be [n_tokens, heads, head_dim] of q's tokens, dimensions, type and device")
+    return _rows(x, x.shape, dev, dtype, name)
+
+
+_pack_rotary = struct.Struct("@P2qP2qi4x").pack
+
+
+def hqq_rotary(freqs, positions, q, k=None, q_out=None, k_out=None, interleaved=False, scale=1.0, stream=None) -> None:
+    """Turn q and k [n_tokens, heads, head_dim] by positions (int32 [n_tokens]) into q_out and k_out,
+    or in place where these are None. freqs (rotary_frequencies) tells by its length how many
+    dimensions are turned; interleaved: pairs are neighbours, else of the two halves."""
+    T = _torch or _th()
+    dev, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
+        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
+    n, _, dim = q.shape
+    if freqs.dim() != 1 or freqs.dtype != T.int64 or freqs.get_device() != dev or not freqs.is_contiguous():
+        raise _bad("freqs must be a contiguous int64 vector on q's device")
+    if positions.shape != (n,) or positions.dtype != T.int32 or positions.get_device() != dev or \
+            not positions.is_contiguous():
+        raise _bad("positions must be a contiguous int32 [n_tokens] on q's device")
+    if k is None and k_out is not None:
+        raise _bad("k_out without k")
+    rows = b""
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            continue
+        at = _turnable(x, n, dev, dtype, name, dim)
+        to = at if out is None else _turnable(out, n, dev, dtype, name + "_out", dim)
+        if out is not None and out.shape != x.shape:
+            raise _bad(f"{name}_out must have the heads of {name}")
+        rows += _pack_rotary(*at, *to, x.shape[1])
+    st = _on(dev, (_L or lib()).hqq_rotary, freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)), scale,
+             positions.data_ptr(), n, dim, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, rows, 1 if k is None else 2,
+             _stream_of(dev, stream))
+    if st:
+        _check(st)
+
+
+def rotary(freqs, positions, q, k=None, interleaved=False, scale=1.0, stream=None):
+    """Allocate the outputs (contiguous) and call hqq_rotary; returns q's, or with k both."""
+    T = _torch or _th()
+    dev = q.get_device()
+    new = lambda x: _on_stream(dev, stream, lambda: T.empty(x.shape, dtype=x.dtype, device=x.device))
+    q_out, k_out = new(q), None if k is None else new(k)
+    hqq_rotary(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream)
+    return q_out if k is None else (q_out, k_out)
+
+
+def hqq_prompt_attention(q, k, v, out, cu_tokens=None, n_seqs=1, lse=None, scale=None, stream=None) -> None:
+    """out = causal attention of packed sequences over themselves: q and out [n_tokens, n_q_heads,
+    head_dim], k and v [n_tokens, n_kv_heads, head_dim]. cu_tokens (int32 [n_seqs + 1]): where the
+    sequences begin and end; without it they are n_seqs of the same length. scale: head_dim ** -0.5
+    unless given."""
+    T = _torch or _th()
+    dev, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
+        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
+    n, heads, dim = shape = q.shape
+    kv = k.shape
+    if len(kv) != 3 or kv[0] != n or kv[2] != dim:
+        raise _bad("k must be [n_tokens, n_kv_heads, head_dim] of q's tokens and dimensions")
+    at = (*_rows(q, shape, dev, dtype, "q"), *_rows(k, kv, dev, dtype, "k"), *_rows(v, kv, dev, dtype, "v"))
+    cu = None
+    if cu_tokens is not None:
+        if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1 or cu_tokens.dtype != T.int32 or \
+                cu_tokens.get_device() != dev or not cu_tokens.is_contiguous():
+            raise _bad("cu_tokens must be a contiguous int32 [n_seqs + 1] on q's device")
+        cu, n_seqs = cu_tokens.data_ptr(), cu_tokens.shape[0] - 1
+    if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
+                            not lse.is_contiguous()):
+        raise _bad("lse must be a contiguous float32 [n_tokens, n_q_heads] on q's device")
+    st = _on(dev, (_L or lib()).hqq_prompt_attention, *at, n, heads, kv[1], dim,
+             HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, cu, n_seqs, dim ** -0.5 if scale is None else scale,
+             *_rows(out, shape, dev, dtype, "out"), None if lse is None else lse.data_ptr(), _stream_of(dev, stream))
+    if st:
+        _check(st)
+
+
+def prompt_attention(q, k, v, cu_tokens=None, n_seqs=1, scale=None, lse=None, stream=None):
+    """Allocate the output (contiguous) and call hqq_prompt_attention."""
+    T = _torch or _th()
+    out = _on_stream(q.get_device(), stream, lambda: T.empty(q.shape, dtype=q.dtype, device=q.device))
+    hqq_prompt_attention(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream)
+    return out
 
 
 # ---- allocation helpers (PyTorch device memory for the outputs) -----------------------------

@@ -279,6 +279,77 @@ hqq_status hqq_gemm_multi(const void *X, int64_t M, int64_t K, const hqq_gemm_we
 hqq_status hqq_gemm_f16(const void *X, int64_t M, const void *Wr, int64_t N, int64_t K, void *Y,
                         void *stream);
 
+typedef enum hqq_dtype {
+    HQQ_F16 = 0,             /* IEEE binary16                                             */
+    HQQ_BF16 = 1             /* bfloat16                                                  */
+} hqq_dtype;
+
+/* ---- Rotary positions ---------------------------------------------------------------------------
+ * Queries and keys of a served model are turned by their position before they go into the cache
+ * and its attention: of a head's first rotary_dim dimensions, pair i is (i, i + rotary_dim/2), or
+ * with `interleaved` (2i, 2i + 1), and becomes
+ *   (a, b) -> scale * (a cos x - b sin x, b cos x + a sin x),  x = 2 pi * position * freqs[i] / 2^64;
+ * the other dimensions stay. freqs are turns per position in 64 bits behind the point, so far
+ * positions lose nothing: x is off by 10^-9 whatever the position, cosine and sine by 2^-23; products
+ * are in binary32, rounded once to the type. Negated positions turn back (with scale 1, that is
+ * also the gradient's way). */
+
+/* Fill freqs (HOST array, rotary_dim/2 numbers; copy it to the device for hqq_rotary) with
+ *   f_i = theta^(-2i/rotary_dim) radians per position, in turns * 2^64,
+ * and for contexts longer than a model was first trained on, f_i * ((1 - s)/factor + s), where
+ *   s = (t - low)/(high - low) within 0 and 1, t = original_len * f_i / (2 pi):
+ * dimensions that turn `high` times or more over original_len stay, those that turn `low` times or
+ * less are slowed by `factor`. original_len 0: all are slowed by factor (low and high are not
+ * used). rotary_dim: even, 2..1024; theta and factor: finite, at least 1. Host only. */
+hqq_status hqq_rotary_frequencies(int rotary_dim, double theta, double factor, int64_t original_len,
+                                  double low, double high, uint64_t *freqs);
+
+/* One tensor of hqq_rotary: [n_tokens, n_heads, head_dim], strides in elements, dimensions
+ * contiguous. out may be in, with the same strides (the other dimensions are then not touched);
+ * else it must overlap no input or output of the call. */
+typedef struct hqq_rotary_rows {
+    const void *in;
+    int64_t in_token_stride, in_head_stride;
+    void *out;
+    int64_t out_token_stride, out_head_stride;
+    int n_heads;             /* 0..4096; 0: nothing to do                                  */
+} hqq_rotary_rows;
+
+/* Turn one or two tensors (queries and keys) in one launch. freqs: device, uint64
+ * [rotary_dim/2]; positions: device, int32 [n_tokens], any values. rotary_dim is even, at most
+ * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24. Any strides and
+ * 2-byte alignment will do; 16-byte pointers, strides that are multiples of 8 and rotary_dim a
+ * multiple of 16 (head_dim of 8) take the fast path. Nothing is allocated. */
+hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, float scale,
+                      const int32_t *positions, int64_t n_tokens, int head_dim, int dtype,
+                      const hqq_rotary_rows *rows, int n_rows, void *stream);
+
+/* ---- Attention of prompts ------------------------------------------------------------------------
+ * Causal attention of packed sequences over themselves, with keys and values as they are (what
+ * hqq_cache_write then stores for the tokens to come). q and out: [n_tokens, n_q_heads, head_dim],
+ * k and v: [n_tokens, n_kv_heads, head_dim], of type dtype, with strides in elements between tokens
+ * and heads (multiples of 8; dimensions contiguous; pointers 16-byte aligned), e.g. slices of one
+ * fused projection's output; head_dim 64, 128 or 256; n_q_heads a multiple of n_kv_heads, query
+ * head h reads key/value head h / (n_q_heads / n_kv_heads). Sequence b has rows cu_tokens[b] ..
+ * cu_tokens[b+1]-1 (device, int32 [n_seqs + 1]), or n_tokens/n_seqs rows each when cu_tokens is
+ * NULL. Row i of a sequence sees its rows 0..i:
+ *   out_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale * <q_i, k_j>),
+ * with scores, sums and the softmax's statistics in binary32, weights rounded to the type where they
+ * meet the values, and out rounded from binary32; lse (binary32 [n_tokens, n_q_heads], nullable)
+ * gets log(sum_j w_ij). What a row does not see does not change it, infinities and NaN included; a
+ * row that sees them in k or q, or whose scores leave binary32's range, is unspecified, one that
+ * sees them in v in that dimension. Offsets outside 0..n_tokens count as the nearest of these, and
+ * where they fall all rows stay as they were; rows of no sequence always do. n_seqs: 0..4096;
+ * n_tokens: 0..2^24; n_kv_heads: 1..1024; n_tokens * n_q_heads at most 2^30. out must not overlap
+ * q, k, v or itself. No workspace is needed, nothing is allocated. */
+hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                int64_t n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                                int dtype, const int32_t *cu_tokens, int n_seqs, float scale,
+                                void *out, int64_t out_token_stride, int64_t out_head_stride,
+                                float *lse, void *stream);
+
 /* ---- The quantized key/value cache of one attention layer ------------------------------------
  * The pages quantize a model's weights [SK "HQQLinear layer"]; while the model answers, the
  * other large tensors it reads per token are the keys and values of what came before. These
@@ -308,11 +379,6 @@ hqq_status hqq_gemm_f16(const void *X, int64_t M, const void *Wr, int64_t N, int
  *   k_meta, v_meta: per token, head_dim/group_size pairs {step, base} of type `dtype`.
  * This order is what the matrix instructions of hqq_cache_attention read with wide loads and
  * no exchange between lanes. */
-typedef enum hqq_dtype {
-    HQQ_F16 = 0,             /* IEEE binary16                                             */
-    HQQ_BF16 = 1             /* bfloat16                                                  */
-} hqq_dtype;
-
 typedef struct hqq_cache {
     void *k_codes, *v_codes; /* [n_pages][n_heads][page_size*head_dim*nbits/8] bytes, each */
     void *k_meta, *v_meta;   /* [n_pages][n_heads][page_size][head_dim/group_size][2]      */
@@ -395,11 +461,37 @@ hqq_status hqq_cache_attention_prefix(const hqq_cache *cache, const hqq_seqs *se
                                       int64_t out_head_stride, float *lse, void *workspace,
                                       size_t workspace_bytes, void *stream);
 
-/* Workspace bytes of the two attention calls for these sizes (prefix_len 0 for the first);
+/* hqq_cache_attention for drafted tokens that form trees (several continuations to be checked at
+ * once): with n_b rows of sequence b in the call, a row sees the positions before them, 0 ..
+ * lens[b] - n_b - 1, and of the call's own tokens those that its mask names: bit j % 64 of
+ * tree[row * tree_words + j / 64] stands for row cu_tokens[b] + j. (A row names its ancestors and,
+ * as a rule, itself; the order is any.) Bits from n_b on are not looked at, tokens from
+ * 64 * tree_words on are not seen. tree: device, uint64 [n_tokens, tree_words], 8-byte aligned;
+ * tree_words: 1..256. Everything else, the workspace too, is hqq_cache_attention's. */
+hqq_status hqq_cache_attention_tree(const hqq_cache *cache, const hqq_seqs *seqs,
+                                    const uint64_t *tree, int tree_words, const void *q,
+                                    int64_t q_token_stride, int64_t q_head_stride, int n_q_heads,
+                                    float scale, void *out, int64_t out_token_stride,
+                                    int64_t out_head_stride, float *lse, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the attention calls for these sizes (prefix_len 0 but for the one with a prefix);
  * a function of the sizes alone. 0 if none is needed (workspace may then be NULL), and if the
  * arguments are invalid: the call then says why. */
 size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seqs,
                                      int n_q_heads, int64_t prefix_len);
+
+/* Keep the accepted ones of the call's tokens, in the caches of all layers (host array of
+ * n_caches, 1..1024, all different, with the same sizes, type and table). kept (device, int32
+ * [n_seqs, max_kept]) lists for each sequence the accepted rows by their number among its n_b
+ * rows, ascending; a list ends with its row of kept, or before the first entry that is negative,
+ * n_b or more, or not above the one before it. With m_b entries, token kept[b][i] moves to position
+ * lens[b] - n_b + i: codes and grids are copied as they are. lens_out (device, int32 [n_seqs],
+ * nullable, not lens) gets lens[b] - n_b + m_b, 0 at least. Positions from there on hold nothing of
+ * meaning afterwards. Where either place is not in the cache, that token does not move. Pages that
+ * hold the moved places must belong to one sequence alone. One launch for up to 64 caches. */
+hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs *seqs,
+                          const int32_t *kept, int max_kept, int32_t *lens_out, void *stream);
 
 /* The bit-packing of the quantized weight W_q [SK "HQQLinear layer": W_q holds the packed
  * codes; bit widths 8/4/3/2/1 from its introduction], standalone: pack n_codes uint8 codes

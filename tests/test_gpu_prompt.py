@@ -1,0 +1,229 @@
+"""Causal attention of packed prompts on the GPU, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F, B = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def H():
+    from calibration_free_weight_amd import hqq
+    return hqq
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cumulated(counts):
+    cu = [0]
+    for c in counts:
+        cu.append(cu[-1] + c)
+    return cu
+
+
+def reference(q, k, v, bounds, scale):
+    """(out, lse, bound, bound of lse) in float64; rows of no sequence are NaN. A binary32 evaluation:
+
+    A score is a sum of dim exact products, in any order: off by (dim + 4) 2^-24 of the sum of
+    magnitudes S, scale's own rounding and two more in the exponent's argument included, and by 2^-23 of
+    the largest score for what is taken off. A weight is off by twice that, relative, and 2^-21 for exp2,
+    and once more for the sum that divides; sums over n weights and products add n 2^-23. Where it meets
+    the values, a weight is rounded to the type: half a step, and with binary16 2^-25 at least, where
+    the largest weight is 1 or more."""
+    n, hq, dim = q.shape
+    hk = k.shape[1]
+    per, half = hq // hk, R.HALF_STEP[q.dtype]
+    out = torch.full((n, hq, dim), math.nan, dtype=torch.float64)
+    lse = torch.full((n, hq), math.nan, dtype=torch.float64)
+    bound, blse = torch.zeros_like(out), torch.zeros_like(lse)
+    for lo, hi in bounds:
+        if hi == lo:
+            continue
+        t = hi - lo
+        x = q[lo:hi].cpu().double().reshape(t, hk, per, dim).permute(1, 2, 0, 3)
+        y, z = (a[lo:hi].cpu().double().transpose(0, 1) for a in (k, v))
+        seen = torch.ones(t, t, dtype=torch.bool).tril()
+        s = (torch.matmul(x, y.transpose(1, 2)[:, None]) * scale).masked_fill(~seen, -math.inf)
+        mag = (torch.matmul(x.abs(), y.abs().transpose(1, 2)[:, None]) * abs(scale)).masked_fill(~seen, 0.0)
+        m = s.amax(-1, keepdim=True)
+        w = torch.exp(s - m)
+        tot = w.sum(-1, keepdim=True)
+        p = w / tot
+        big = s.masked_fill(~seen, 0.0).abs().amax(-1, keepdim=True)
+        r = 2 * (mag * (dim + 4) * 2.0 ** -24 + big * 2.0 ** -23) + 2.0 ** -21
+        total = (p * r).sum(-1, keepdim=True) + t * 2.0 ** -23
+        e = torch.matmul(p * (r + total + half) + (2.0 ** -25 / tot * seen if q.dtype == F else 0.0), z.abs()[:, None])
+        e = e + t * 2.0 ** -23 * torch.matmul(p, z.abs()[:, None])
+        put = lambda a: a.permute(2, 0, 1, *range(3, a.dim())).reshape(t, hq, *a.shape[3:])
+        out[lo:hi], bound[lo:hi] = put(torch.matmul(p, z[:, None])), put(e)
+        lse[lo:hi] = put((m + torch.log(tot)).squeeze(-1))
+        blse[lo:hi] = put((r.masked_fill(~seen, 0.0).amax(-1) + total.squeeze(-1) + m.squeeze(-1).abs() * 2.0 ** -22))
+    return out, lse, bound, blse
+
+
+def check(got, got_lse, ref, mine=None):
+    out, lse, bound, blse = ref
+    mine = ~torch.isnan(lse[:, 0]) if mine is None else mine
+    x, y, e = got.cpu().double()[mine], out[mine], bound[mine]
+    assert torch.isfinite(x).all(), "outputs are not finite"
+    tol = e + R.HALF_STEP[got.dtype] * (y.abs() + e) + (2.0 ** -25 if got.dtype == F else 2.0 ** -130)
+    bad = (x - y).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((x - y).abs() / tol).max()):.3g} of the tolerance"
+    if got_lse is not None:
+        d = (got_lse.cpu().double()[mine] - lse[mine]).abs()
+        assert (d <= blse[mine]).all(), f"lse off by {float(d.max()):.3g}"
+
+
+def inputs(n, hq, hk, dim, dtype, gen, size=1.0):
+    """q, k and v as parts of one projection's output, with a mean per channel."""
+    x = torch.randn(n, hq + 2 * hk, dim, generator=gen) * size + torch.randn(hq + 2 * hk, dim, generator=gen) * 0.5
+    x = x.to(dtype).cuda()
+    return x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+
+
+PROMPTS = [
+    # dtype, dim, kv heads, per, lengths
+    (F, 128, 2, 1, [1]),
+    (B, 128, 1, 1, [37]),
+    (F, 128, 2, 1, [128, 129, 127, 64, 65, 63]),
+    (B, 128, 2, 4, [200, 1, 0, 33, 2]),
+    (F, 64, 3, 5, [99, 100, 31, 32, 300]),
+    (B, 64, 1, 7, [513, 18]),
+    (F, 256, 1, 2, [140, 31, 32, 33]),
+    (B, 256, 2, 3, [70, 0, 0, 5]),
+    (F, 128, 1, 16, [77, 8]),
+    (B, 64, 1, 40, [65, 3]),
+    (F, 64, 1, 200, [9]),
+    (B, 128, 2, 8, [1000]),
+    (F, 256, 1, 1, [700]),
+    (F, 64, 1, 1, [1500, 1]),
+    (B, 128, 1, 1, [3] * 300),
+    (F, 64, 1, 2, [1, 0, 2] * 500),
+]
+
+
+@pytest.mark.parametrize("dtype,dim,hk,per,lens", PROMPTS)
+def test_prompt_attention(H, dtype, dim, hk, per, lens):
+    gen = torch.Generator().manual_seed(dim + sum(lens) + per)
+    cu = cumulated(lens)
+    n, hq = cu[-1], hk * per
+    q, k, v = inputs(n + 2, hq, hk, dim, dtype, gen)
+    obuf = torch.full((n + 2, hq + 2, dim), 11.0, dtype=dtype, device="cuda")
+    lse = torch.full((n + 2, hq), 13.0, dtype=torch.float32, device="cuda")
+    H.hqq_prompt_attention(q, k, v, obuf[:, 1:-1], cu_tokens=i32(cu), lse=lse)
+    ref = reference(q, k, v, list(zip(cu, cu[1:])), dim ** -0.5)
+    check(obuf[:, 1:-1], lse, ref)
+    assert (obuf[n:] == 11).all() and (obuf[:, 0] == 11).all() and (obuf[:, -1] == 11).all() and (lse[n:] == 13).all()
+    if len(set(lens)) == 1:                         # the same without row offsets
+        got = H.prompt_attention(q[:n], k[:n], v[:n], n_seqs=len(lens))
+        assert got.is_contiguous() and torch.equal(got, obuf[:n, 1:-1])
+
+
+@pytest.mark.parametrize("dtype,dim", [(F, 128), (B, 64), (B, 256)])
+@pytest.mark.parametrize("scale", [1.0, -0.3, 0.0, 1e-30])
+def test_scales_and_scores_far_apart(H, dtype, dim, scale):
+    gen = torch.Generator().manual_seed(dim)
+    q, k, v = inputs(150, 4, 2, dim, dtype, gen, 3.0)
+    lse = torch.empty(150, 4, dtype=torch.float32, device="cuda")
+    got = H.prompt_attention(q, k, v, scale=scale, lse=lse)
+    check(got, lse, reference(q, k, v, [(0, 150)], scale))
+
+
+@pytest.mark.parametrize("dtype,size", [(F, 2.0 ** -20), (F, 6e4), (B, 2.0 ** -120), (B, 2.0 ** 120)])
+def test_values_of_any_size(H, dtype, size):
+    gen = torch.Generator().manual_seed(1)
+    q, k, _ = inputs(200, 4, 2, 128, dtype, gen)
+    v = ((torch.rand(200, 2, 128, generator=gen) * 2 - 1) * size).to(dtype).cuda()
+    check(H.prompt_attention(q, k, v), None, reference(q, k, v, [(0, 200)], 128 ** -0.5))
+
+
+def test_scores_that_rise_and_fall(H):
+    """The maximum moves all along the sequence, by more than the slack and by less."""
+    gen = torch.Generator().manual_seed(2)
+    for rise in (0.02, 0.3, 2.0, -0.3):
+        q, k, v = inputs(700, 2, 1, 64, F, gen)
+        k = (k + rise * torch.arange(700, device="cuda")[:, None, None] * torch.sign(q[:, :1].float().mean(0))[None] / 30).half()
+        check(H.prompt_attention(q, k, v), None, reference(q, k, v, [(0, 700)], 0.125))
+
+
+@pytest.mark.parametrize("dtype,dim,per", [(F, 128, 1), (B, 64, 4), (F, 256, 2), (B, 128, 8)])
+def test_what_a_row_does_not_see_does_not_change_it(H, dtype, dim, per):
+    """Infinities and NaN in keys and values: rows before them are as without, other sequences too,
+    and in values they reach those that see them in their own dimensions."""
+    gen = torch.Generator().manual_seed(dim)
+    lens = [150, 90]
+    q, k, v = (x.clone() for x in inputs(240, per, 1, dim, dtype, gen))
+    ref = reference(q, k, v, [(0, 150), (150, 240)], dim ** -0.5)
+    at = {"nan": 100, "inf": 70, "-inf": 131}
+    v[100, 0, 5], v[70, 0, 33], v[131, 0, dim - 1] = math.nan, math.inf, -math.inf
+    got = H.prompt_attention(q, k, v, cu_tokens=i32(cumulated(lens))).cpu()
+    clean = torch.ones(240, per, dim, dtype=torch.bool)
+    clean[100:150, :, 5] = clean[70:150, :, 33] = clean[131:150, :, dim - 1] = False
+    x, y, e = got.double()[clean], ref[0][clean], ref[2][clean]
+    assert ((x - y).abs() <= e + R.HALF_STEP[dtype] * (y.abs() + e) + 2.0 ** -25).all()
+    assert not torch.isfinite(got[~clean]).any()
+    k[149, 0, 3], q[30, 0, 1] = math.nan, math.nan
+    got = H.prompt_attention(q, k, v, cu_tokens=i32(cumulated(lens))).cpu()
+    clean[149] = clean[30, 0] = False
+    x, y, e = got.double()[clean], ref[0][clean], ref[2][clean]
+    assert ((x - y).abs() <= e + R.HALF_STEP[dtype] * (y.abs() + e) + 2.0 ** -25).all()
+    assert torch.isnan(got[149]).all() and torch.isnan(got[30, 0]).all()
+
+
+def test_offsets_of_any_contents(H):
+    gen = torch.Generator().manual_seed(4)
+    q, k, v = inputs(200, 4, 2, 128, F, gen)
+    for bad in ([-9, 50, 50, 999, 2000], [0, 0, 0, 0, 0], [7, 20, 130, 130, 145], [200, 200, 300, 400, 500]):
+        out = torch.full_like(q, 5.0)
+        H.hqq_prompt_attention(q, k, v, out, cu_tokens=i32(bad))
+        rows = R.rows_of(bad, 200, 4)
+        ref = reference(q, k, v, rows, 128 ** -0.5)
+        mine = ~torch.isnan(ref[1][:, 0])
+        check(out, None, ref, mine)
+        assert (out.cpu()[~mine] == 5).all()
+    out = torch.full_like(q, 5.0)                   # offsets that fall: nothing is done
+    H.hqq_prompt_attention(q, k, v, out, cu_tokens=i32([0, 90, 60, 100, 200]))
+    assert (out == 5).all()
+
+
+def test_heads_first_and_single_rows(H):
+    gen = torch.Generator().manual_seed(5)
+    q, k, v = inputs(90, 6, 3, 64, B, gen)
+    want = H.prompt_attention(q, k, v)
+    heads_first = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
+    got = H.prompt_attention(*heads_first)
+    assert got.is_contiguous() and torch.equal(got, want)
+    # a single token is its own value
+    one = H.prompt_attention(q[:1], k[:1], v[:1])
+    assert torch.equal(one, v[:1].repeat_interleave(2, 1))
+    assert H.prompt_attention(q[:0], k[:0], v[:0]).shape == (0, 6, 64)
+    assert H.prompt_attention(q[:4], k[:4], v[:4], cu_tokens=i32([0])).shape == (4, 6, 64)
+
+
+def test_the_same_bits_again(H):
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = inputs(600, 8, 2, 128, B, gen)
+    cu = i32([0, 250, 251, 600])
+    want = H.prompt_attention(q, k, v, cu_tokens=cu)
+    for _ in range(3):
+        assert torch.equal(H.prompt_attention(q, k, v, cu_tokens=cu), want)
+
+
+def test_the_binding_refuses(H):
+    q, k, v = inputs(12, 4, 2, 64, F, torch.Generator())
+    cu, out, lse = i32([0, 12]), torch.empty_like(q), torch.empty(12, 4, dtype=torch.float32, device="cuda")
+    for args, kw in (((q, k, v[:6], out), {}), ((q, k[:6], v[:6], out), {}), ((q, k, v[:, :1], out), {}), ((q, k[..., :32], v[..., :32], out), {}),
+                     ((q.float(), k, v, out), {}), ((q, k.bfloat16(), v, out), {}), ((q[0], k, v, out), {}), ((q, k, v, out[:, :2]), {}),
+                     ((q, k, v, out.cpu()), {}), ((q, k, v, out), dict(cu_tokens=cu.long())), ((q, k, v, out), dict(cu_tokens=cu.cpu())),
+                     ((q, k, v, out), dict(cu_tokens=cu[:0])), ((q, k, v, out), dict(n_seqs=5)), ((q, k, v, out), dict(n_seqs=-1)),
+                     ((q, k, v, out), dict(lse=lse[:6])), ((q, k, v, out), dict(lse=lse.half())), ((q, k, v, out), dict(scale=math.nan)),
+                     ((q[:, :3], k, v, out[:, :3]), {}), ((q.transpose(1, 2), k, v, out), {}), ((q[..., :48], k[..., :48], v[..., :48], out[..., :48]), {})):
+        with pytest.raises(H.HQQError):
+            H.hqq_prompt_attention(*args, **kw)
