@@ -9,7 +9,10 @@
 //   O^T = V^T . P^T    B = weights: the scores that the lane has, the order of the contraction being
 //                      free; A = values, transposed on their way out of LDS;
 // so that weights stay in registers, and maxima and sums are per lane, joined over the two lanes of
-// a row.
+// a row. A step makes the next keys' scores while the weights of the present ones are computed, and
+// then meets the values: the vector instructions of a softmax (3 and an exponential for each weight)
+// take about as long as its matrix instructions and run beside them. Keys and values of the steps to
+// come are in registers and in the other half of LDS meanwhile, one barrier to a step.
 #include <cmath>
 
 #include "hqq.h"
@@ -29,8 +32,8 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kRows = 32 * kWaves;
+constexpr int kAhead = 2;         // fragments asked for before they are used
+constexpr int64_t kMaxKeyStride = 1 << 23;
 constexpr float kLog2e = 1.44269504088896341f;
 // How far a score (to base 2) may lie above the maximum that weights are taken from.
 constexpr float kSlack = 8.f;
@@ -63,6 +66,9 @@ __device__ __forceinline__ uint32_t round2(float a, float b)
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2));
 }
 
+// NaN if one is: one instruction for two of these, where fmaxf takes two more that quiet NaN.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // x of both lanes of a row, which are 32 apart.
 template <typename F>
 __device__ __forceinline__ float of_row(float x, F f)
@@ -76,6 +82,20 @@ __device__ __forceinline__ float of_row(float x, F f)
 __device__ __forceinline__ u32x2 read_transposed(const void *p)
 {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p));
+}
+
+// The first n rows from p (uniform), of `dim` numbers each and `ts` apart, no more than `most`, as a
+// buffer: what is read behind them is 0. (most * ts * 2 stays below 2^31.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint16_t *p, int n, int most, int ts, int dim)
+{
+    const uint64_t at = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    const int bytes = ((min(n, most) - 1) * ts + dim) * 2 & -n >> 31;      // 0 without rows, and no branch
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int lane_offset, int offset)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0);
 }
 
 // Whether one of two numbers is an infinity or NaN; the two with such replaced by 0.
@@ -95,164 +115,210 @@ struct Tile {
     int row0, n_rows;
 };
 
-// Tile `back` from the last of all sequences (the longest tiles of each come first), or none.
-// scan: [kWaves + 1] in LDS, found: [2].
-__device__ __forceinline__ bool find_tile(const SeqView &s, int per, int back, int32_t *scan, int32_t *found, Tile &x)
+// Sums of what the lanes of a wave, or with ALL the threads of the block have.
+template <int WAVES, bool ALL>
+__device__ __forceinline__ int sum_of(int x, int32_t (&scan)[2][WAVES], int &turn)
 {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int each = (s.n_seqs + kThreads - 1) / kThreads, b0 = min(t * each, s.n_seqs), b1 = min(b0 + each, s.n_seqs);
-    int sum = 0;
-    bool falls = false;
-    for (int b = b0; b < b1; ++b) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    if constexpr (ALL) {
+        if ((threadIdx.x & 63) == 0) scan[turn][threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) x += scan[turn][w];
+        turn ^= 1;              // who is late still reads the other
+    }
+    return __builtin_amdgcn_readfirstlane(x);
+}
+
+// The u-th of all sequences' tiles, or none. The longest come first, those that lie furthest back in
+// their sequences, for the last ones to begin to be short: behind them nothing fills the GPU. With f(k)
+// tiles at place k or behind, it is at the last place where f(k) > u, which a search finds; there, the
+// (u - f(k + 1))-th of the sequences that reach so far. Up to 64 sequences lie in a wave's lanes, and
+// no wave waits for another.
+template <int WAVES, int ROWS, bool ALL>
+__device__ __forceinline__ bool find_tile(const SeqView &s, int per, int u, int32_t (&scan)[2][WAVES], int32_t (&found)[2], Tile &x)
+{
+    const int t = ALL ? threadIdx.x : threadIdx.x & 63, threads = ALL ? 64 * WAVES : 64;
+    const int each = ALL ? (s.n_seqs + threads - 1) / threads : 1;
+    const int b0 = min(t * each, s.n_seqs), b1 = min(b0 + each, s.n_seqs);
+    int turn = 0;
+    const auto tiles = [&](int b) {
         const Rows r = rows_of(s, b);
-        sum += tiles_of((r.end - r.begin) * per, kRows);
+        return tiles_of((r.end - r.begin) * per, ROWS);
+    };
+    int most = 0;
+    bool falls = false;
+    const int own = b0 < b1 ? tiles(b0) : 0;                // with one sequence to a lane, its tiles
+    for (int b = b0; b < b1; ++b) {
+        most = max(most, ALL ? tiles(b) : own);
         falls = falls || falls_at(s, b);
     }
-    int upto = sum;
+    const auto behind = [&](int k) {                        // f(k)
+        int n = 0;
+        for (int b = b0; b < b1; ++b) n += max(0, (ALL ? tiles(b) : own) - k);
+        return sum_of<WAVES, ALL>(n, scan, turn);
+    };
+    // offsets that fall would count rows twice
+    if (ALL ? __syncthreads_or(falls) : __any(falls)) return false;
+    if (u >= behind(0)) return false;
+    int k = 0;
+    if (ALL) {
+        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+        found[0] = 0;
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) atomicMax(&found[0], most);
+        __syncthreads();
+        most = found[0];
+    } else {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(upto, d);
-        if (lane >= d) upto += y;
+        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
     }
-    if (lane == 63) scan[wave] = upto;
-    if (__syncthreads_or(falls)) return false;      // rows would be counted twice
-    int before = upto - sum, total = 0;
+    most = __builtin_amdgcn_readfirstlane(most);
+    for (int hi = most; hi - k > 1;) {                      // f(k) > u >= f(hi)
+        const int mid = (k + hi) >> 1;
+        if (behind(mid) > u) k = mid; else hi = mid;
+    }
+    int which = u - behind(k + 1), b = 0;
+    if (ALL) {
+        int mine = 0, before = 0;
+        for (int c = b0; c < b1; ++c) mine += tiles(c) > k;
+        int upto = mine;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before += scan[w];
-        total += scan[w];
-    }
-    const int u = total - 1 - back;
-    if (u < 0) return false;
-    if (before <= u && u < before + sum) {
-        for (int b = b0; b < b1; ++b) {
-            const Rows r = rows_of(s, b);
-            const int n = tiles_of((r.end - r.begin) * per, kRows);
-            if (u < before + n) {
-                found[0] = b;
-                found[1] = u - before;
-                break;
-            }
-            before += n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(upto, d);
+            if ((t & 63) >= d) upto += y;
         }
+        if ((t & 63) == 63) scan[turn][t >> 6] = upto;
+        __syncthreads();
+        for (int w = 0; w < t >> 6; ++w) before += scan[turn][w];
+        before += upto - mine;
+        for (int c = b0; c < b1; ++c)
+            if (tiles(c) > k && before++ == which) found[1] = c;
+        __syncthreads();
+        b = found[1];
+    } else {
+        uint64_t reach = __ballot(own > k);
+        for (; which > 0; --which) reach &= reach - 1;
+        b = __builtin_ctzll(reach);
     }
-    __syncthreads();
-    x.seq = rows_of(s, __builtin_amdgcn_readfirstlane(found[0]));
-    x.row0 = __builtin_amdgcn_readfirstlane(found[1]) * kRows;
+    x.seq = rows_of(s, __builtin_amdgcn_readfirstlane(b));
+    x.row0 = k * ROWS;
     x.n_rows = (x.seq.end - x.seq.begin) * per;
     return true;
 }
 
-template <typename T, int D, int BN>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void prompt_kernel(PromptArgs a)
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+
+template <typename T, int D, int WAVES, int KB>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(PromptArgs a)
 {
+    constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES, kKeys = 32 * KB;
     constexpr int kChunks = D / 8;                          // of 16 bytes, in a row of keys or values
-    constexpr int kEach = BN * kChunks / kThreads;          // chunks of keys to a thread
+    constexpr int kEach = kKeys * kChunks / kThreads;       // chunks of keys to a thread
     constexpr int kApart = kThreads / kChunks;              // rows between a thread's chunks
-    __shared__ u32x4 keys[2][BN * kChunks], values[2][BN * kChunks];
-    __shared__ int32_t scan[kWaves], found[2], bad[2];      // bad: the last tile whose values were not finite
+    static_assert(kEach * kThreads == kKeys * kChunks, "whole chunks for each thread");
+    __shared__ u32x4 keys[2][kKeys * kChunks], values[2][kKeys * kChunks];
+    __shared__ int32_t scan[2][WAVES], found[2], bad[2];    // bad: the last step whose values were not finite
     Tile x;
     const int h = (int)(blockIdx.x % (unsigned)a.heads);
     if (threadIdx.x < 2) bad[threadIdx.x] = -1;
-    if (!find_tile(a.s, a.per, (int)(blockIdx.x / (unsigned)a.heads), scan, found, x)) return;
+    const int u = (int)(blockIdx.x / (unsigned)a.heads);
+    const bool has = a.s.n_seqs <= 64 ? find_tile<WAVES, kRows, false>(a.s, a.per, u, scan, found, x)
+                                      : find_tile<WAVES, kRows, true>(a.s, a.per, u, scan, found, x);
+    if (!has) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int n = x.seq.end - x.seq.begin;
-    const int row = x.row0 + 32 * wave + col;
-    const bool have = row < x.n_rows;
-    const int tok = (have ? row : x.n_rows - 1) / a.per, hq = h * a.per + (have ? row - tok * a.per : 0);
+    const int wave_row = x.row0 + 32 * wave, row = wave_row + col;      // a lane's row, and its token
+    const int tok = min(row, x.n_rows - 1) / a.per, hq = h * a.per + (row - tok * a.per);
     // tokens of the block's and the wave's first and last rows
     const int first = x.row0 / a.per, last = min(x.row0 + kRows, x.n_rows) - 1;
-    const int wave_first = min(x.row0 + 32 * wave, x.n_rows - 1) / a.per;
-    const int wave_last = min(x.row0 + 32 * wave + 31, x.n_rows - 1) / a.per;
-    const bool wave_has = x.row0 + 32 * wave < x.n_rows;
-    const int end = last / a.per + 1;                       // keys that some row sees
-    const int tiles = (end + BN - 1) / BN;
+    const int wave_first = min(wave_row, x.n_rows - 1) / a.per;
+    const int wave_last = min(wave_row + 31, x.n_rows - 1) / a.per;
+    const int steps = last / a.per / kKeys + 1;             // of keys that some row sees
 
     // where a thread's chunks come from: rows and places are swapped within LDS so that no two lanes
-    // that read at a time meet in a bank
+    // that read at a time meet in a bank. Rows behind the sequence are beyond the buffer, and 0.
     const int r0 = (int)threadIdx.x / kChunks, place = (int)threadIdx.x % kChunks;
     const auto key_swap = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : r & 15; };
     const auto value_swap = [](int r) { return kChunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
+    const int k_ts = (int)a.k_ts, v_ts = (int)a.v_ts;
+    const uint16_t *next_k = a.k + x.seq.begin * a.k_ts + h * a.k_hs, *next_v = a.v + x.seq.begin * a.v_ts + h * a.v_hs;
+    int left_k = n, left_v = n;                             // rows from there
     u32x4 kr[kEach], vr[kEach];
-    const auto fetch = [&](int j0) {
+    const auto fetch_keys = [&] {
+        const auto k = rows_from(next_k, left_k, kKeys, k_ts, D);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int r = r0 + i * kApart;
-            const int64_t at = x.seq.begin + min(j0 + r, n - 1);
-            kr[i] = *reinterpret_cast<const u32x4 *>(a.k + at * a.k_ts + h * a.k_hs + 8 * (place ^ key_swap(r)));
-            vr[i] = *reinterpret_cast<const u32x4 *>(a.v + at * a.v_ts + h * a.v_hs + 8 * (place ^ value_swap(r)));
-        }
+        for (int i = 0; i < kEach; ++i)
+            kr[i] = load16(k, r0 * k_ts * 2 + 16 * (place ^ key_swap(r0 + i * kApart)), i * kApart * k_ts * 2);
+        next_k += kKeys * k_ts;
+        left_k -= kKeys;
     };
-    const auto put = [&](int tile) {
-        const int j0 = tile * BN, b = tile & 1;
-        if (j0 + BN - 1 > first) {      // some row does not see some key
-            bool ok = true;
+    const auto fetch_values = [&] {
+        const auto v = rows_from(next_v, left_v, kKeys, v_ts, D);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const bool in = j0 + r0 + i * kApart < n;
+        for (int i = 0; i < kEach; ++i)
+            vr[i] = load16(v, r0 * v_ts * 2 + 16 * (place ^ value_swap(r0 + i * kApart)), i * kApart * v_ts * 2);
+        next_v += kKeys * v_ts;
+        left_v -= kKeys;
+    };
+    const auto put_keys = [&](int b) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!in) vr[i][e] = 0;
-                    uint32_t w = vr[i][e];
-                    ok = finite2<T>(w) && ok;
-                    vr[i][e] = w;
-                }
+        for (int i = 0; i < kEach; ++i) keys[b][threadIdx.x + i * kThreads] = kr[i];
+    };
+    const auto put_values = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) values[b][threadIdx.x + i * kThreads] = vr[i];
+    };
+    // Of a step that some rows do not see in full: values that are not finite are left out, and noted.
+    const auto check_values = [&](int step) {
+        if (__builtin_expect((step + 1) * kKeys - 1 <= first, 1)) return;
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w = vr[i][e];
+                ok = finite2<T>(w) && ok;
+                vr[i][e] = w;
             }
-            if (!ok) bad[b] = tile;
-        }
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            keys[b][threadIdx.x + i * kThreads] = kr[i];
-            values[b][threadIdx.x + i * kThreads] = vr[i];
-        }
+        if (!ok) bad[step & 1] = step;
     };
-
-    fetch(0);
     u32x4 qf[D / 16];
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-        qf[s] = u32x4{0, 0, 0, 0};
-        if (have) qf[s] = *reinterpret_cast<const u32x4 *>(a.q + (x.seq.begin + tok) * a.q_ts + hq * a.q_hs + 16 * s + 8 * half);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qf[s][e] = (qf[s][e] & a.keep) ^ a.flip;
-    }
-    put(0);
-    if (tiles > 1) fetch(BN);
+    // Fragment d of 32 keys kb in buffer b; of the values, dimensions 32 j.. of keys 16 g..
+    const auto key_frag = [&](int b, int kb, int d) { return keys[b][(32 * kb + col) * kChunks + ((2 * d + half) ^ key_swap(col))]; };
+    const int vrow = 4 * half + ((lane & 15) >> 2);
+    const auto value_frag = [&](int b, int g, int j) {
+        const int c = (4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swap(vrow);
+        const char *p = reinterpret_cast<const char *>(&values[b][(16 * g + vrow) * kChunks + c]) + 8 * (lane & 1);
+        const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * kChunks * 16);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
     f32x16 o[D / 32];
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
     float m = -INFINITY, l = 0.f;
 
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int j0 = tile * BN, b = tile & 1;
-        __syncthreads();
-        if (tile + 1 < tiles) put(tile + 1);
-        if (tile + 2 < tiles) fetch(j0 + 2 * BN);
-        if (j0 > wave_last || !wave_has) continue;
-        f32x16 s[BN / 32];
+    // The largest of a row's scores so far, and numbers e and e + 1 of them.
+    const auto larger_of = [&](float top, const f32x16 (&s)[KB], int e) {
+        const float p = s[e / 16][e % 16], q = s[e / 16][e % 16 + 1];
+        return e == 0 ? larger(p, q) : larger(larger(top, p), q);
+    };
+    // Moves m where the scores go beyond it by more than the slack; where some row does not see some
+    // key, takes these scores out first.
+    const auto look = [&](f32x16 (&s)[KB], float top, int step) {
+        if (__builtin_expect((step + 1) * kKeys - 1 > wave_first, 0)) {
+            int seen = tok - step * kKeys - 4 * half;
+            asm volatile("" : "+v"(seen));                  // a branch, not a choice in every step
 #pragma unroll
-        for (int kb = 0; kb < BN / 32; ++kb) {
+            for (int e = 0; e < 16 * KB; ++e)
+                if (32 * (e / 16) + 8 * (e % 16 / 4) + e % 4 > seen) s[e / 16][e % 16] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
-            const int r = 32 * kb + col;
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-                s[kb] = mfma<T>(keys[b][r * kChunks + ((2 * d + half) ^ key_swap(r))], qf[d], s[kb]);
+            for (int e = 0; e < 16 * KB; e += 2) top = larger_of(top, s, e);
         }
-        if (j0 + BN - 1 > wave_first)
-#pragma unroll
-            for (int kb = 0; kb < BN / 32; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (j0 + 32 * kb + 8 * (i / 4) + 4 * half + i % 4 > tok) s[kb][i] = -INFINITY;
-        float top = s[0][0];
-#pragma unroll
-        for (int kb = 0; kb < BN / 32; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-        top = of_row(top, [](float p, float q) { return fmaxf(p, q); }) * a.scale;
+        top = of_row(top, larger) * a.scale;
         if (__any(top > m + kSlack)) {
             const float to = fmaxf(m, top), f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
             m = to;
@@ -260,31 +326,70 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void prompt_kernel(Prom
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) o[j] *= f;
         }
+    };
+    // A step: its weights and their products with the values, while the next step's scores are made,
+    // and what comes behind that is on its way. The order is written out, for the matrix instructions
+    // to follow each other while the weights' instructions run beside them: of the pairs of weights
+    // the first kBeside are made beside the scores, the others beside the first half of the products
+    // with the values, and the next scores' maxima beside the second.
+    const auto go = [&](auto parity, int step, f32x16 (&s)[KB], f32x16 (&next)[KB]) {
+        constexpr int b = parity.value, kP = D / 32;
+        constexpr int kQ = KB * (D / 16), kV = 2 * KB * kP;                 // fragments
+        constexpr int kPairs = 8 * KB, kFirst = 2;
+        constexpr int kBeside = (D == 64 ? kPairs / 2 : D == 128 ? kPairs * 5 / 8 : kPairs) - kFirst;
+        u32x4 pf[2 * KB], kf[kAhead + 1], vf[kAhead + 1];
+        const auto weigh = [&](int from, int to) {          // pairs of weights, four for 16 keys
 #pragma unroll
-        for (int kb = 0; kb < BN / 32; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], a.scale, -m));
-                l += s[kb][i];
+            for (int i = from; i < to; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[i / 8][i % 8 * 2], a.scale, -m));
+                const float q = __builtin_amdgcn_exp2f(fmaf(s[i / 8][i % 8 * 2 + 1], a.scale, -m));
+                l += p;
+                l += q;
+                pf[i / 4][i % 4] = round2<T>(p, q);
             }
+        };
+        const auto key = [&](int i) { return key_frag(b ^ 1, i % KB, i / KB); };
+        const auto value = [&](int i) { return value_frag(b, i / kP, i % kP); };
+        __syncthreads();
+        check_values(step + 1);
 #pragma unroll
-        for (int g = 0; g < BN / 16; ++g) {
-            u32x4 pf;
+        for (int i = 0; i < kAhead; ++i) kf[i] = key(i);
+        weigh(0, kFirst);               // while the first fragments are on their way
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pf[e] = round2<T>(s[g / 2][8 * (g % 2) + 2 * e], s[g / 2][8 * (g % 2) + 2 * e + 1]);
-            const int r = 16 * g + 4 * half + ((lane & 15) >> 2);
+        for (int i = 0; i < kQ; ++i) {
+            f32x16 zero;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const int c = (4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swap(r);
-                const char *p = reinterpret_cast<const char *>(&values[b][r * kChunks + c]) + 8 * (lane & 1);
-                const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * kChunks * 16);
-                o[j] = mfma<T>(u32x4{lo[0], lo[1], hi[0], hi[1]}, pf, o[j]);
-            }
+            for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+            next[i % KB] = mfma<T>(kf[i % (kAhead + 1)], qf[i / KB], i < KB ? zero : next[i % KB]);
+            if (i + kAhead < kQ) kf[(i + kAhead) % (kAhead + 1)] = key(i + kAhead);
+            else vf[(i + kAhead - kQ) % (kAhead + 1)] = value(i + kAhead - kQ);
+            weigh(kFirst + i * kBeside / kQ, kFirst + (i + 1) * kBeside / kQ);
+            if (i == kQ / 4) put_keys(b);                   // of step + 2
+            if (i == kQ * 3 / 8) put_values(b ^ 1);         // of step + 1
+            if (i == kQ / 2) fetch_keys();
+            if (i == kQ * 5 / 8) fetch_values();
+            __builtin_amdgcn_sched_barrier(0);
         }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            o[i % kP] = mfma<T>(vf[i % (kAhead + 1)], pf[i / kP], o[i % kP]);
+            if (i + kAhead < kV) vf[(i + kAhead) % (kAhead + 1)] = value(i + kAhead);
+            constexpr int kHalf = kV / 2, kLast = kPairs - kFirst - kBeside;
+            if (i < kHalf) {
+                weigh(kFirst + kBeside + i * kLast / kHalf, kFirst + kBeside + (i + 1) * kLast / kHalf);
+            } else {
+#pragma unroll
+                for (int e = (i - kHalf) * kPairs / kHalf; e < (i - kHalf + 1) * kPairs / kHalf; ++e) top = larger_of(top, next, 2 * e);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("" : "+v"(top), "+v"(l));              // made here
         // values that are not finite, of keys that some rows see and others do not, were left out
-        if (__builtin_expect(bad[b] == tile, 0)) {
+        if (__builtin_expect((step + 1) * kKeys - 1 > first, 0) && bad[b] == step) {
 #pragma unroll 1
-            for (int j = j0; j < min(j0 + BN, wave_last + 1); ++j) {
+            for (int j = step * kKeys; j < min((step + 1) * kKeys, wave_last + 1); ++j) {
                 const uint16_t *v = a.v + (x.seq.begin + j) * a.v_ts + h * a.v_hs;
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d)
@@ -295,9 +400,52 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void prompt_kernel(Prom
                     }
             }
         }
+        if (step + 1 < steps) look(next, top, step + 1);
+    };
+
+    fetch_keys();
+    fetch_values();
+    const uint16_t *q = a.q + (x.seq.begin + tok) * a.q_ts + hq * a.q_hs + 8 * half;
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+        qf[d] = u32x4{0, 0, 0, 0};
+        if (row < x.n_rows) qf[d] = *reinterpret_cast<const u32x4 *>(q + 16 * d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qf[d][e] = (qf[d][e] & a.keep) ^ a.flip;
+    }
+    __syncthreads();                    // `bad` is set
+    check_values(0);
+    put_keys(0);
+    put_values(0);
+    fetch_keys();
+    fetch_values();
+    f32x16 s0[KB], s1[KB];
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s0[kb][e] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) s0[kb] = mfma<T>(key_frag(0, kb, d), qf[d], s0[kb]);
+    }
+#pragma unroll
+    for (int e = 0; e < 16 * KB; e += 2) top = larger_of(top, s0, e);
+    put_keys(1);
+    fetch_keys();
+    look(s0, top, 0);
+    for (int step = 0;;) {
+        go(Index<0>{}, step, s0, s1);
+        if (++step == steps) break;
+        go(Index<1>{}, step, s1, s0);
+        if (++step == steps) break;
     }
     l = of_row(l, [](float p, float q) { return p + q; });
-    if (!have) return;
+    if (row >= x.n_rows) return;
     const float inv = l > 0.f ? 1.f / l : l;
     uint16_t *to = a.out + (x.seq.begin + tok) * a.o_ts + hq * a.o_hs + 4 * half;
 #pragma unroll
@@ -310,14 +458,24 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void prompt_kernel(Prom
         a.lse[(int64_t)(x.seq.begin + tok) * a.heads * a.per + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T>
-hipError_t launch(const PromptArgs &a, int dim, int64_t tiles, hipStream_t stream)
+template <typename T, int D, int WAVES, int KB>
+hipError_t launch_tiles(const PromptArgs &a, hipStream_t stream)
 {
-    const unsigned blocks = (unsigned)(tiles * a.heads);
-    if (dim == 64) prompt_kernel<T, 64, 64><<<blocks, kThreads, 0, stream>>>(a);
-    else if (dim == 128) prompt_kernel<T, 128, 64><<<blocks, kThreads, 0, stream>>>(a);
-    else prompt_kernel<T, 256, 32><<<blocks, kThreads, 0, stream>>>(a);
+    // no more tiles than this, however the sequences are cut
+    constexpr int kRows = 32 * WAVES;
+    const int64_t rows = (int64_t)a.s.n_tokens * a.per, each = rows / a.s.n_seqs;
+    const int64_t tiles = a.s.cu ? rows / kRows + a.s.n_seqs : (each + kRows - 1) / kRows * a.s.n_seqs;
+    prompt_kernel<T, D, WAVES, KB><<<dim3((unsigned)(tiles * a.heads)), 64 * WAVES, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch(const PromptArgs &a, int dim, hipStream_t stream)
+{
+    if (dim == 64) return launch_tiles<T, 64, 4, 1>(a, stream);
+    if (dim == 256) return launch_tiles<T, 256, 4, 1>(a, stream);
+    if ((int64_t)a.s.n_tokens * a.per * a.heads / 256 >= 1024 && a.s.n_tokens / a.s.n_seqs >= 4096) return launch_tiles<T, 128, 8, 2>(a, stream);
+    return launch_tiles<T, 128, 4, 1>(a, stream);
 }
 
 hqq_status refuse(const char *msg, hqq_status st = HQQ_ERR_ARG)
@@ -364,6 +522,9 @@ extern "C" hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride
         if (!aligned(r.p, 16) || r.ts < 0 || r.hs < 0 || r.ts % 8 || r.hs % 8 || r.ts > (int64_t(1) << 36) || r.hs > (int64_t(1) << 36))
             return refuse("q, k, v and out must be 16-byte aligned, with strides that are multiples of 8 in [0, 2^36]");
     }
+    // offsets within a step's keys are 32 bits
+    if (k_token_stride > kMaxKeyStride || v_token_stride > kMaxKeyStride)
+        return refuse("the token strides of k and v must be at most 2^23");
     PromptArgs a{};
     a.q = static_cast<const uint16_t *>(q);
     a.k = static_cast<const uint16_t *>(k);
@@ -388,12 +549,10 @@ extern "C" hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride
     a.scale = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
     a.flip = scale < 0.f ? 0x80008000u : 0u;
     a.keep = scale == 0.f ? 0u : 0xffffffffu;
-    // no more tiles than this, however the sequences are cut
-    const int64_t each = n_tokens / n_seqs * a.per;
-    const int64_t tiles = cu_tokens ? n_tokens * a.per / kRows + n_seqs : (each + kRows - 1) / kRows * n_seqs;
-    if (tiles * a.heads >= (1 << 24)) return refuse("too many rows for one call", HQQ_ERR_UNSUPPORTED);
+    // blocks of the smallest tiles
+    if ((n_tokens * a.per / 128 + n_seqs) * a.heads >= (1 << 24)) return refuse("too many rows for one call", HQQ_ERR_UNSUPPORTED);
     const hipStream_t str = static_cast<hipStream_t>(stream);
-    const hipError_t e = dtype == HQQ_BF16 ? launch<Bf16>(a, head_dim, tiles, str) : launch<F16>(a, head_dim, tiles, str);
+    const hipError_t e = dtype == HQQ_BF16 ? launch<Bf16>(a, head_dim, str) : launch<F16>(a, head_dim, str);
     if (e != hipSuccess) return refuse(hipGetErrorString(e), HQQ_ERR_DEVICE);
     report_error(HQQ_OK, "");
     return HQQ_OK;
