@@ -262,18 +262,6 @@ __device__ __forceinline__ float column_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// Inclusive sum over the lanes of a wave: within rows of 16, then from row to row.
-__device__ __forceinline__ int wave_sum(int x)
-{
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);     // row_shr 1, 2, 4, 8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);     // lane 15 of a row to the next one
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
-    return x;
-}
-
 // A run's next item, or the part of it that the run has.
 struct Item {
     int b;                      // sequence

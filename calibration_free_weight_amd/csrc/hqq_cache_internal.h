@@ -60,6 +60,18 @@ __device__ __forceinline__ void unpack8(const uint4 raw, float (&v)[8])
     }
 }
 
+// Inclusive sum over the lanes of a wave: within rows of 16, then from row to row.
+__device__ __forceinline__ int wave_sum(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);     // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);     // lane 15 of a row to the next one
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
+    return x;
+}
+
 // The sequence of the call's row `i`, which is the wave's first row or close behind it: the
 // wave looks for the first together, 64 entries at a time, and each lane goes on from there.
 // All lanes of the wave must come here.

@@ -119,8 +119,7 @@ struct Tile {
 template <int WAVES, bool ALL>
 __device__ __forceinline__ int sum_of(int x, int32_t (&scan)[2][WAVES], int &turn)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    x = __builtin_amdgcn_readlane(wave_sum(x), 63);
     if constexpr (ALL) {
         if ((threadIdx.x & 63) == 0) scan[turn][threadIdx.x >> 6] = x;
         __syncthreads();
@@ -162,8 +161,9 @@ __device__ __forceinline__ bool find_tile(const SeqView &s, int per, int u, int3
     };
     // offsets that fall would count rows twice
     if (ALL ? __syncthreads_or(falls) : __any(falls)) return false;
-    if (u >= behind(0)) return false;
-    int k = 0;
+    const int total = behind(0);
+    if (u >= total) return false;
+    int k = s.n_seqs == 1 ? total - 1 - u : 0;
     if (ALL) {
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
         found[0] = 0;
@@ -176,20 +176,15 @@ __device__ __forceinline__ bool find_tile(const SeqView &s, int per, int u, int3
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
     }
     most = __builtin_amdgcn_readfirstlane(most);
-    for (int hi = most; hi - k > 1;) {                      // f(k) > u >= f(hi)
+    for (int hi = s.n_seqs == 1 ? 0 : most; hi - k > 1;) {  // f(k) > u >= f(hi)
         const int mid = (k + hi) >> 1;
         if (behind(mid) > u) k = mid; else hi = mid;
     }
-    int which = u - behind(k + 1), b = 0;
+    int which = s.n_seqs == 1 ? 0 : u - behind(k + 1), b = 0;
     if (ALL) {
         int mine = 0, before = 0;
         for (int c = b0; c < b1; ++c) mine += tiles(c) > k;
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(upto, d);
-            if ((t & 63) >= d) upto += y;
-        }
+        const int upto = wave_sum(mine);
         if ((t & 63) == 63) scan[turn][t >> 6] = upto;
         __syncthreads();
         for (int w = 0; w < t >> 6; ++w) before += scan[turn][w];

@@ -6,6 +6,7 @@
 // that is left, whatever the position: nothing is lost at far positions, and no range is reduced.
 // Of it 32 bits are kept: 2^-33 turns, 7e-10 radians.
 #include <cmath>
+#include <type_traits>
 
 #include "hqq.h"
 #include "hqq_cache_internal.h"
@@ -84,54 +85,78 @@ __device__ __forceinline__ void turn8(uint4 &lo, uint4 &hi, const float2 *cs)
     hi = uint4{y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16};
 }
 
+// Where a unit of the block's tokens lies: its first numbers, and the second of pairs that are turned.
+struct Unit {
+    const uint16_t *in;
+    uint16_t *out;
+    int d0, d1, pair;           // pair: of the token's cosines and sines, the first; or -1: copied
+};
+template <bool NEIGHBOURS, bool WIDE>
+__device__ __forceinline__ Unit unit_of(const RotaryArgs &a, int t0, int j)
+{
+    constexpr int kPairs = WIDE ? 8 : 1, kWidth = WIDE ? 8 : 1;
+    const unsigned t = (unsigned)j / (unsigned)a.units, of_token = j - t * a.units;
+    unsigned h = of_token / (unsigned)a.per_head;
+    const int u = of_token - h * a.per_head, turning = a.pairs / kPairs;
+    const bool second = h >= (unsigned)a.x[0].heads;
+    const Tensor &x = a.x[second];
+    if (second) h -= a.x[0].heads;
+    Unit r;
+    r.in = x.in + (t0 + (int64_t)t) * x.in_ts + h * x.in_hs;
+    r.out = x.out + (t0 + (int64_t)t) * x.out_ts + h * x.out_hs;
+    if (u < turning) {
+        r.d0 = NEIGHBOURS ? 2 * kPairs * u : kPairs * u;
+        r.d1 = NEIGHBOURS ? r.d0 + kPairs : r.d0 + a.pairs;
+        r.pair = t * a.pairs + kPairs * u;
+    } else {
+        r.d0 = r.d1 = a.rest0 + kWidth * (u - turning);
+        r.pair = -1;
+    }
+    return r;
+}
+
 // A unit is eight pairs, or with !WIDE one; or as many dimensions that are copied. A block makes
 // the cosines and sines of its tokens once, for all heads, while its first units are on their way.
+// Bound by memory: 16390 tokens of 72 heads of 128, 604 MB: 106 us, 5.7 TB/s (part of it from the
+// last level's cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.3 us, 3.2 TB/s;
+// a token 2.1 us, the launch and two loads that wait for each other.
 template <typename T, bool NEIGHBOURS, bool WIDE>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
 {
+    using Raw = std::conditional_t<WIDE, uint4, uint16_t>;
     extern __shared__ float2 cs[];      // [tokens][pairs]
     const int t0 = (int)(blockIdx.x / (unsigned)a.parts) * a.tokens, part = (int)(blockIdx.x % (unsigned)a.parts);
-    const int tokens = min(a.tokens, a.n_tokens - t0);
-    for (int j = threadIdx.x; j < tokens * a.pairs; j += kThreads) {
-        const unsigned t = (unsigned)j / (unsigned)a.pairs, i = j - t * a.pairs;
-        const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + t] * a.freqs[i];
-        cs[j] = cos_sin((uint32_t)((turns + 0x80000000u) >> 32), a.scale);
+    const int tokens = min(a.tokens, a.n_tokens - t0), all = tokens * a.units;
+    int j = part * kThreads + threadIdx.x;
+    Unit x{};
+    Raw lo{}, hi{};
+    const auto load = [&] {
+        x = unit_of<NEIGHBOURS, WIDE>(a, t0, j);
+        lo = *reinterpret_cast<const Raw *>(x.in + x.d0);
+        hi = *reinterpret_cast<const Raw *>(x.in + x.d1);
+    };
+    if (j < all) load();
+    for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
+        const unsigned t = (unsigned)i / (unsigned)a.pairs, k = i - t * a.pairs;
+        const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + t] * a.freqs[k];
+        cs[i] = cos_sin((uint32_t)((turns + 0x80000000u) >> 32), a.scale);
     }
     __syncthreads();
-    const int turning = WIDE ? a.pairs / 8 : a.pairs;       // units of a head
-    for (int j = part * kThreads + threadIdx.x; j < tokens * a.units; j += a.parts * kThreads) {
-        const unsigned t = (unsigned)j / (unsigned)a.units, of_token = j - t * a.units;
-        unsigned h = of_token / (unsigned)a.per_head;
-        const int u = of_token - h * a.per_head;
-        const bool second = h >= (unsigned)a.x[0].heads;
-        const Tensor &x = a.x[second];
-        if (second) h -= a.x[0].heads;
-        const uint16_t *in = x.in + (t0 + (int64_t)t) * x.in_ts + h * x.in_hs;
-        uint16_t *out = x.out + (t0 + (int64_t)t) * x.out_ts + h * x.out_hs;
-        const float2 *c = cs + t * a.pairs;
-        if constexpr (WIDE) {
-            if (u < turning) {
-                const int d0 = NEIGHBOURS ? 16 * u : 8 * u, d1 = NEIGHBOURS ? d0 + 8 : d0 + a.pairs;
-                uint4 lo = *reinterpret_cast<const uint4 *>(in + d0), hi = *reinterpret_cast<const uint4 *>(in + d1);
-                turn8<T, NEIGHBOURS>(lo, hi, c + 8 * u);
-                *reinterpret_cast<uint4 *>(out + d0) = lo;
-                *reinterpret_cast<uint4 *>(out + d1) = hi;
+    while (j < all) {
+        if (x.pair >= 0) {
+            if constexpr (WIDE) {
+                turn8<T, NEIGHBOURS>(lo, hi, cs + x.pair);
             } else {
-                const int d = a.rest0 + 8 * (u - turning);
-                *reinterpret_cast<uint4 *>(out + d) = *reinterpret_cast<const uint4 *>(in + d);
-            }
-        } else {
-            if (u < turning) {
-                const int d0 = NEIGHBOURS ? 2 * u : u, d1 = NEIGHBOURS ? d0 + 1 : d0 + a.pairs;
                 uint32_t p, q;
-                turn<T>(to_f32<T>(in[d0]), to_f32<T>(in[d1]), c[u], p, q);
-                out[d0] = (uint16_t)p;
-                out[d1] = (uint16_t)q;
-            } else {
-                const int d = a.rest0 + (u - turning);
-                out[d] = in[d];
+                turn<T>(to_f32<T>(lo), to_f32<T>(hi), cs[x.pair], p, q);
+                lo = (uint16_t)p;
+                hi = (uint16_t)q;
             }
+            *reinterpret_cast<Raw *>(x.out + x.d1) = hi;
         }
+        *reinterpret_cast<Raw *>(x.out + x.d0) = lo;
+        j += a.parts * kThreads;
+        if (j < all) load();
     }
 }
 

@@ -547,7 +547,7 @@ def hqq_cache_keep(caches, table, lens, kept, n_tokens, lens_out=None, cu_tokens
     caches = [caches] if isinstance(caches, dict) else list(caches)
     if not caches:
         raise _bad("caches must be one cache or more")
-    structs, devs, types = zip(*(_cache_struct(c) for c in caches))
+    structs, devs, _ = zip(*map(_cache_struct, caches))     # 1.3 us each, most of what the call takes
     dev = devs[0]
     if any(d != dev for d in devs):
         raise _bad("the caches must be on one GPU")
@@ -559,7 +559,7 @@ def hqq_cache_keep(caches, table, lens, kept, n_tokens, lens_out=None, cu_tokens
     if lens_out is not None and (lens_out.shape != (n,) or lens_out.dtype != T.int32 or
                                  lens_out.get_device() != dev or not lens_out.is_contiguous()):
         raise _bad("lens_out must be a contiguous int32 [n_seqs] on the caches' device")
-    st = _on(dev, lib().hqq_cache_keep, b"".join(structs), len(structs), s, kept.data_ptr(), kept.shape[1],
+    st = _on(dev, lib().hqq_cache_keep, b"".join(structs), len(caches), s, kept.data_ptr(), kept.shape[1],
              None if lens_out is None else lens_out.data_ptr(), _stream_of(dev, stream))
     if st:
         _check(st)
@@ -632,55 +632,88 @@ def rotary_frequencies(rotary_dim, theta=10000.0, factor=1.0, original_len=0, lo
     return host.to(device)
 
 
-def _turnable(x, n, dev, dtype, name, dim):
-    if x.dim() != 3 or x.shape[0] != n or x.shape[2] != dim or x.dtype != dtype or x.get_device() != dev:
-        raise _bad(f"{name} must be [n_tokens, heads, head_dim] of q's tokens, dimensions, type and device")
-    return _rows(x, x.shape, dev, dtype, name)
-
-
 _pack_rotary = struct.Struct("@P2qP2qi4x").pack
+
+
+def _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, fresh):
+    """hqq_rotary, or with `fresh` into tensors that it allocates (contiguous) and returns."""
+    T = _torch or _th()
+    shape, dev, dtype = q.shape, q.get_device(), q.dtype
+    if len(shape) != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
+        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
+    n, _, dim = shape
+    if len(freqs.shape) != 1 or freqs.dtype != T.int64 or freqs.get_device() != dev or not freqs.is_contiguous():
+        raise _bad("freqs must be a contiguous int64 vector on q's device")
+    if positions.shape != (n,) or positions.dtype != T.int32 or positions.get_device() != dev or \
+            not positions.is_contiguous():
+        raise _bad("positions must be a contiguous int32 [n_tokens] on q's device")
+    tensors, rows, outs = ((q, q_out, "q"),) if k is None else ((q, q_out, "q"), (k, k_out, "k")), b"", []
+    for x, out, name in tensors:
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != dim:
+            raise _bad(f"{name} must be [n_tokens, heads, head_dim] of q's tokens and dimensions")
+        at = _rows(x, shape, dev, dtype, name)
+        if fresh:
+            out = _on_stream(dev, stream, lambda: T.empty_like(x, memory_format=T.contiguous_format))
+            outs.append(out)
+            to = out.data_ptr(), shape[1] * dim, dim
+        else:
+            to = at if out is None else _rows(out, shape, dev, dtype, name + "_out")
+        rows += _pack_rotary(*at, *to, shape[1])
+    st = _on(dev, (_L or lib()).hqq_rotary, freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, scale,
+             positions.data_ptr(), n, dim, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, rows, len(tensors),
+             _stream_of(dev, stream))
+    if st:
+        _check(st)
+    return outs
 
 
 def hqq_rotary(freqs, positions, q, k=None, q_out=None, k_out=None, interleaved=False, scale=1.0, stream=None) -> None:
     """Turn q and k [n_tokens, heads, head_dim] by positions (int32 [n_tokens]) into q_out and k_out,
     or in place where these are None. freqs (rotary_frequencies) tells by its length how many
     dimensions are turned; interleaved: pairs are neighbours, else of the two halves."""
-    T = _torch or _th()
-    dev, dtype = q.get_device(), q.dtype
-    if q.dim() != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
-        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
-    n, _, dim = q.shape
-    if freqs.dim() != 1 or freqs.dtype != T.int64 or freqs.get_device() != dev or not freqs.is_contiguous():
-        raise _bad("freqs must be a contiguous int64 vector on q's device")
-    if positions.shape != (n,) or positions.dtype != T.int32 or positions.get_device() != dev or \
-            not positions.is_contiguous():
-        raise _bad("positions must be a contiguous int32 [n_tokens] on q's device")
     if k is None and k_out is not None:
         raise _bad("k_out without k")
-    rows = b""
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            continue
-        at = _turnable(x, n, dev, dtype, name, dim)
-        to = at if out is None else _turnable(out, n, dev, dtype, name + "_out", dim)
-        if out is not None and out.shape != x.shape:
-            raise _bad(f"{name}_out must have the heads of {name}")
-        rows += _pack_rotary(*at, *to, x.shape[1])
-    st = _on(dev, (_L or lib()).hqq_rotary, freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)), scale,
-             positions.data_ptr(), n, dim, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, rows, 1 if k is None else 2,
-             _stream_of(dev, stream))
-    if st:
-        _check(st)
+    _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, False)
 
 
 def rotary(freqs, positions, q, k=None, interleaved=False, scale=1.0, stream=None):
     """Allocate the outputs (contiguous) and call hqq_rotary; returns q's, or with k both."""
+    outs = _rotate(freqs, positions, q, k, None, None, interleaved, scale, stream, True)
+    return outs[0] if k is None else (outs[0], outs[1])
+
+
+def _prompt(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream):
     T = _torch or _th()
-    dev = q.get_device()
-    new = lambda x: _on_stream(dev, stream, lambda: T.empty(x.shape, dtype=x.dtype, device=x.device))
-    q_out, k_out = new(q), None if k is None else new(k)
-    hqq_rotary(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream)
-    return q_out if k is None else (q_out, k_out)
+    shape, dev, dtype = q.shape, q.get_device(), q.dtype
+    if len(shape) != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
+        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
+    n, heads, dim = shape
+    kv = k.shape
+    if len(kv) != 3 or kv[0] != n or kv[2] != dim:
+        raise _bad("k must be [n_tokens, n_kv_heads, head_dim] of q's tokens and dimensions")
+    qr, kr, vr = _rows(q, shape, dev, dtype, "q"), _rows(k, kv, dev, dtype, "k"), _rows(v, kv, dev, dtype, "v")
+    cu = None
+    if cu_tokens is not None:
+        cus = cu_tokens.shape
+        if len(cus) != 1 or cus[0] < 1 or cu_tokens.dtype != T.int32 or cu_tokens.get_device() != dev or \
+                not cu_tokens.is_contiguous():
+            raise _bad("cu_tokens must be a contiguous int32 [n_seqs + 1] on q's device")
+        cu, n_seqs = cu_tokens.data_ptr(), cus[0] - 1
+    if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
+                            not lse.is_contiguous()):
+        raise _bad("lse must be a contiguous float32 [n_tokens, n_q_heads] on q's device")
+    if out is None:
+        out = _on_stream(dev, stream, lambda: T.empty_like(q, memory_format=T.contiguous_format))
+        to = out.data_ptr(), heads * dim, dim
+    else:
+        to = _rows(out, shape, dev, dtype, "out")
+    st = _on(dev, (_L or lib()).hqq_prompt_attention, *qr, *kr, *vr, n, heads, kv[1], dim,
+             HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, cu, n_seqs, dim ** -0.5 if scale is None else scale,
+             *to, None if lse is None else lse.data_ptr(), _stream_of(dev, stream))
+    if st:
+        _check(st)
+    return out
 
 
 def hqq_prompt_attention(q, k, v, out, cu_tokens=None, n_seqs=1, lse=None, scale=None, stream=None) -> None:
@@ -688,37 +721,14 @@ def hqq_prompt_attention(q, k, v, out, cu_tokens=None, n_seqs=1, lse=None, scale
     head_dim], k and v [n_tokens, n_kv_heads, head_dim]. cu_tokens (int32 [n_seqs + 1]): where the
     sequences begin and end; without it they are n_seqs of the same length. scale: head_dim ** -0.5
     unless given."""
-    T = _torch or _th()
-    dev, dtype = q.get_device(), q.dtype
-    if q.dim() != 3 or dev < 0 or (dtype != T.float16 and dtype != T.bfloat16):
-        raise _bad("q must be [n_tokens, heads, head_dim] of float16 or bfloat16, on a GPU")
-    n, heads, dim = shape = q.shape
-    kv = k.shape
-    if len(kv) != 3 or kv[0] != n or kv[2] != dim:
-        raise _bad("k must be [n_tokens, n_kv_heads, head_dim] of q's tokens and dimensions")
-    at = (*_rows(q, shape, dev, dtype, "q"), *_rows(k, kv, dev, dtype, "k"), *_rows(v, kv, dev, dtype, "v"))
-    cu = None
-    if cu_tokens is not None:
-        if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 1 or cu_tokens.dtype != T.int32 or \
-                cu_tokens.get_device() != dev or not cu_tokens.is_contiguous():
-            raise _bad("cu_tokens must be a contiguous int32 [n_seqs + 1] on q's device")
-        cu, n_seqs = cu_tokens.data_ptr(), cu_tokens.shape[0] - 1
-    if lse is not None and (lse.shape != (n, heads) or lse.dtype != T.float32 or lse.get_device() != dev or
-                            not lse.is_contiguous()):
-        raise _bad("lse must be a contiguous float32 [n_tokens, n_q_heads] on q's device")
-    st = _on(dev, (_L or lib()).hqq_prompt_attention, *at, n, heads, kv[1], dim,
-             HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, cu, n_seqs, dim ** -0.5 if scale is None else scale,
-             *_rows(out, shape, dev, dtype, "out"), None if lse is None else lse.data_ptr(), _stream_of(dev, stream))
-    if st:
-        _check(st)
+    if out is None:
+        raise _bad("out must be [n_tokens, n_q_heads, head_dim]")
+    _prompt(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream)
 
 
 def prompt_attention(q, k, v, cu_tokens=None, n_seqs=1, scale=None, lse=None, stream=None):
     """Allocate the output (contiguous) and call hqq_prompt_attention."""
-    T = _torch or _th()
-    out = _on_stream(q.get_device(), stream, lambda: T.empty(q.shape, dtype=q.dtype, device=q.device))
-    hqq_prompt_attention(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream)
-    return out
+    return _prompt(q, k, v, None, cu_tokens, n_seqs, lse, scale, stream)
 
 
 # ---- allocation helpers (PyTorch device memory for the outputs) -----------------------------

@@ -328,8 +328,8 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
  * Causal attention of packed sequences over themselves, with keys and values as they are (what
  * hqq_cache_write then stores for the tokens to come). q and out: [n_tokens, n_q_heads, head_dim],
  * k and v: [n_tokens, n_kv_heads, head_dim], of type dtype, with strides in elements between tokens
- * and heads (multiples of 8; dimensions contiguous; pointers 16-byte aligned), e.g. slices of one
- * fused projection's output; head_dim 64, 128 or 256; n_q_heads a multiple of n_kv_heads, query
+ * and heads (multiples of 8, between tokens of k and v at most 2^23; dimensions contiguous;
+ * pointers 16-byte aligned), e.g. slices of one fused projection's output; head_dim 64, 128 or 256; n_q_heads a multiple of n_kv_heads, query
  * head h reads key/value head h / (n_q_heads / n_kv_heads). Sequence b has rows cu_tokens[b] ..
  * cu_tokens[b+1]-1 (device, int32 [n_seqs + 1]), or n_tokens/n_seqs rows each when cu_tokens is
  * NULL. Row i of a sequence sees its rows 0..i:
