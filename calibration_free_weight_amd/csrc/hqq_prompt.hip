@@ -464,13 +464,27 @@ hipError_t launch_tiles(const PromptArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Heads of 128 in blocks of 128 rows that go 32 keys a step, two to a CU, or of 256 rows and 64 keys,
+// one to a CU, which fetch a key for twice the rows and meet half as often, but begin and end alone.
+// Measured in us, of 128 and of 256 rows (sequences x tokens, query heads / key heads):
+//   1 x 8190, 64/8    1062   991      1 x 2048, 32/32   56    62      2 x 4096, 32/32   296   285
+//   1 x 4096, 32/8     155   137      1 x 8190, 8/8    183   198      3 x 3000, 40/40   339   348
+//   1 x 2048, 64/8      94    88      16 x 1024, 32/8  201   225      2 x 2048, 40/40   113   116
+//   4 x 2048, 16/4      87    79      64 x 512, 32/8   324   343      8 x 2048, 32/8    319   325
+// so the wide ones have long sequences (the rows of one head cover fewer tokens the more heads share
+// it, and a tile's end wastes less) and two blocks at least to a CU.
+bool wide_blocks(const PromptArgs &a)
+{
+    const int64_t blocks = (int64_t)a.s.n_tokens * a.per * a.heads / 256;
+    return blocks >= 512 && a.s.n_tokens / a.s.n_seqs >= (a.per >= 4 ? 2048 : 4096);
+}
+
 template <typename T>
 hipError_t launch(const PromptArgs &a, int dim, hipStream_t stream)
 {
     if (dim == 64) return launch_tiles<T, 64, 4, 1>(a, stream);
     if (dim == 256) return launch_tiles<T, 256, 4, 1>(a, stream);
-    if ((int64_t)a.s.n_tokens * a.per * a.heads / 256 >= 1024 && a.s.n_tokens / a.s.n_seqs >= 4096) return launch_tiles<T, 128, 8, 2>(a, stream);
-    return launch_tiles<T, 128, 4, 1>(a, stream);
+    return wide_blocks(a) ? launch_tiles<T, 128, 8, 2>(a, stream) : launch_tiles<T, 128, 4, 1>(a, stream);
 }
 
 hqq_status refuse(const char *msg, hqq_status st = HQQ_ERR_ARG)
