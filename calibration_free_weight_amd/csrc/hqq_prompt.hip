@@ -163,40 +163,40 @@ __device__ __forceinline__ bool find_tile(const SeqView &s, int per, int u, int3
     if (ALL ? __syncthreads_or(falls) : __any(falls)) return false;
     const int total = behind(0);
     if (u >= total) return false;
-    int k = s.n_seqs == 1 ? total - 1 - u : 0;
-    if (ALL) {
-        for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-        found[0] = 0;
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) atomicMax(&found[0], most);
-        __syncthreads();
-        most = found[0];
-    } else {
+    int k = total - 1 - u, b = 0;                           // of a single sequence, from its end
+    if (s.n_seqs > 1) {
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
-    }
-    most = __builtin_amdgcn_readfirstlane(most);
-    for (int hi = s.n_seqs == 1 ? 0 : most; hi - k > 1;) {  // f(k) > u >= f(hi)
-        const int mid = (k + hi) >> 1;
-        if (behind(mid) > u) k = mid; else hi = mid;
-    }
-    int which = s.n_seqs == 1 ? 0 : u - behind(k + 1), b = 0;
-    if (ALL) {
-        int mine = 0, before = 0;
-        for (int c = b0; c < b1; ++c) mine += tiles(c) > k;
-        const int upto = wave_sum(mine);
-        if ((t & 63) == 63) scan[turn][t >> 6] = upto;
-        __syncthreads();
-        for (int w = 0; w < t >> 6; ++w) before += scan[turn][w];
-        before += upto - mine;
-        for (int c = b0; c < b1; ++c)
-            if (tiles(c) > k && before++ == which) found[1] = c;
-        __syncthreads();
-        b = found[1];
-    } else {
-        uint64_t reach = __ballot(own > k);
-        for (; which > 0; --which) reach &= reach - 1;
-        b = __builtin_ctzll(reach);
+        if constexpr (ALL) {
+            found[0] = 0;
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) atomicMax(&found[0], most);
+            __syncthreads();
+            most = found[0];
+        }
+        k = 0;
+        for (int hi = __builtin_amdgcn_readfirstlane(most); hi - k > 1;) {      // f(k) > u >= f(hi)
+            const int mid = (k + hi) >> 1;
+            if (behind(mid) > u) k = mid; else hi = mid;
+        }
+        int which = u - behind(k + 1);
+        if constexpr (ALL) {
+            int mine = 0, before = 0;
+            for (int c = b0; c < b1; ++c) mine += tiles(c) > k;
+            const int upto = wave_sum(mine);
+            if ((t & 63) == 63) scan[turn][t >> 6] = upto;
+            __syncthreads();
+            for (int w = 0; w < t >> 6; ++w) before += scan[turn][w];
+            before += upto - mine;
+            for (int c = b0; c < b1; ++c)
+                if (tiles(c) > k && before++ == which) found[1] = c;
+            __syncthreads();
+            b = found[1];
+        } else {
+            uint64_t reach = __ballot(own > k);
+            for (; which > 0; --which) reach &= reach - 1;
+            b = __builtin_ctzll(reach);
+        }
     }
     x.seq = rows_of(s, __builtin_amdgcn_readfirstlane(b));
     x.row0 = k * ROWS;
@@ -209,20 +209,22 @@ struct Index {
     static constexpr int value = I;
 };
 
-template <typename T, int D, int WAVES, int KB>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(PromptArgs a)
+template <typename T, int D, int DV, int WAVES, int KB>
+__global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
 {
     constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES, kKeys = 32 * KB;
     constexpr int kChunks = D / 8;                          // of 16 bytes, in a row of keys or values
     constexpr int kEach = kKeys * kChunks / kThreads;       // chunks of keys to a thread
     constexpr int kApart = kThreads / kChunks;              // rows between a thread's chunks
+    constexpr int kVChunks = DV / 8, kVEach = kKeys * kVChunks / kThreads, kVApart = kThreads / kVChunks;
     static_assert(kEach * kThreads == kKeys * kChunks, "whole chunks for each thread");
-    __shared__ u32x4 keys[2][kKeys * kChunks], values[2][kKeys * kChunks];
+    __shared__ u32x4 keys[2][kKeys * kChunks], values[2][kKeys * kVChunks];
     __shared__ int32_t scan[2][WAVES], found[2], bad[2];    // bad: the last step whose values were not finite
     Tile x;
-    const int h = (int)(blockIdx.x % (unsigned)a.heads);
+    const unsigned parts = a.heads * (D / DV), part = blockIdx.x % parts;
+    const int h = (int)(part % (unsigned)a.heads), dv0 = (int)(part / (unsigned)a.heads) * DV;     // of the outputs
     if (threadIdx.x < 2) bad[threadIdx.x] = -1;
-    const int u = (int)(blockIdx.x / (unsigned)a.heads);
+    const int u = (int)(blockIdx.x / parts);
     const bool has = a.s.n_seqs <= 64 ? find_tile<WAVES, kRows, false>(a.s, a.per, u, scan, found, x)
                                       : find_tile<WAVES, kRows, true>(a.s, a.per, u, scan, found, x);
     if (!has) return;
@@ -240,11 +242,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     // that read at a time meet in a bank. Rows behind the sequence are beyond the buffer, and 0.
     const int r0 = (int)threadIdx.x / kChunks, place = (int)threadIdx.x % kChunks;
     const auto key_swap = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : r & 15; };
-    const auto value_swap = [](int r) { return kChunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
+    const auto value_swap = [](int r) { return kVChunks == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2; };
+    const int vr0 = (int)threadIdx.x / kVChunks, vplace = (int)threadIdx.x % kVChunks;
     const int k_ts = (int)a.k_ts, v_ts = (int)a.v_ts;
-    const uint16_t *next_k = a.k + x.seq.begin * a.k_ts + h * a.k_hs, *next_v = a.v + x.seq.begin * a.v_ts + h * a.v_hs;
+    const uint16_t *next_k = a.k + x.seq.begin * a.k_ts + h * a.k_hs, *next_v = a.v + x.seq.begin * a.v_ts + h * a.v_hs + dv0;
     int left_k = n, left_v = n;                             // rows from there
-    u32x4 kr[kEach], vr[kEach];
+    u32x4 kr[kEach], vr[kVEach];
     const auto fetch_keys = [&] {
         const auto k = rows_from(next_k, left_k, kKeys, k_ts, D);
 #pragma unroll
@@ -254,10 +257,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
         left_k -= kKeys;
     };
     const auto fetch_values = [&] {
-        const auto v = rows_from(next_v, left_v, kKeys, v_ts, D);
+        const auto v = rows_from(next_v, left_v, kKeys, v_ts, DV);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            vr[i] = load16(v, r0 * v_ts * 2 + 16 * (place ^ value_swap(r0 + i * kApart)), i * kApart * v_ts * 2);
+        for (int i = 0; i < kVEach; ++i)
+            vr[i] = load16(v, vr0 * v_ts * 2 + 16 * (vplace ^ value_swap(vr0 + i * kVApart)), i * kVApart * v_ts * 2);
         next_v += kKeys * v_ts;
         left_v -= kKeys;
     };
@@ -267,14 +270,14 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     };
     const auto put_values = [&](int b) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) values[b][threadIdx.x + i * kThreads] = vr[i];
+        for (int i = 0; i < kVEach; ++i) values[b][threadIdx.x + i * kThreads] = vr[i];
     };
     // Of a step that some rows do not see in full: values that are not finite are left out, and noted.
     const auto check_values = [&](int step) {
         if (__builtin_expect((step + 1) * kKeys - 1 <= first, 1)) return;
         bool ok = true;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < kVEach; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 uint32_t w = vr[i][e];
@@ -289,11 +292,11 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     const int vrow = 4 * half + ((lane & 15) >> 2);
     const auto value_frag = [&](int b, int g, int j) {
         const int c = (4 * j + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swap(vrow);
-        const char *p = reinterpret_cast<const char *>(&values[b][(16 * g + vrow) * kChunks + c]) + 8 * (lane & 1);
-        const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * kChunks * 16);
+        const char *p = reinterpret_cast<const char *>(&values[b][(16 * g + vrow) * kVChunks + c]) + 8 * (lane & 1);
+        const u32x2 lo = read_transposed(p), hi = read_transposed(p + 8 * kVChunks * 16);
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
-    f32x16 o[D / 32];
+    f32x16 o[DV / 32];
     float m = -INFINITY, l = 0.f;
 
     // The largest of a row's scores so far, and numbers e and e + 1 of them.
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
             m = to;
             l *= f;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) o[j] *= f;
+            for (int j = 0; j < DV / 32; ++j) o[j] *= f;
         }
     };
     // A step: its weights and their products with the values, while the next step's scores are made,
@@ -328,7 +331,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     // the first kBeside are made beside the scores, the others beside the first half of the products
     // with the values, and the next scores' maxima beside the second.
     const auto go = [&](auto parity, int step, f32x16 (&s)[KB], f32x16 (&next)[KB]) {
-        constexpr int b = parity.value, kP = D / 32;
+        constexpr int b = parity.value, kP = DV / 32;
         constexpr int kQ = KB * (D / 16), kV = 2 * KB * kP;                 // fragments
         constexpr int kPairs = 8 * KB, kFirst = 2;
         constexpr int kBeside = (D == 64 ? kPairs / 2 : D == 128 ? kPairs * 5 / 8 : kPairs) - kFirst;
@@ -385,9 +388,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
         if (__builtin_expect((step + 1) * kKeys - 1 > first, 0) && bad[b] == step) {
 #pragma unroll 1
             for (int j = step * kKeys; j < min((step + 1) * kKeys, wave_last + 1); ++j) {
-                const uint16_t *v = a.v + (x.seq.begin + j) * a.v_ts + h * a.v_hs;
+                const uint16_t *v = a.v + (x.seq.begin + j) * a.v_ts + h * a.v_hs + dv0;
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d)
+                for (int d = 0; d < DV / 32; ++d)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float y = to_f32<T>(v[32 * d + 8 * (i / 4) + 4 * half + i % 4]);
@@ -417,7 +420,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     f32x16 s0[KB], s1[KB];
     float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j)
+    for (int j = 0; j < DV / 32; ++j)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
     __syncthreads();
@@ -442,25 +445,25 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void prompt_kernel(Pr
     l = of_row(l, [](float p, float q) { return p + q; });
     if (row >= x.n_rows) return;
     const float inv = l > 0.f ? 1.f / l : l;
-    uint16_t *to = a.out + (x.seq.begin + tok) * a.o_ts + hq * a.o_hs + 4 * half;
+    uint16_t *to = a.out + (x.seq.begin + tok) * a.o_ts + hq * a.o_hs + dv0 + 4 * half;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j)
+    for (int j = 0; j < DV / 32; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<u32x2 *>(to + 32 * j + 8 * i) = u32x2{round2<T>(o[j][4 * i] * inv, o[j][4 * i + 1] * inv),
                                                                     round2<T>(o[j][4 * i + 2] * inv, o[j][4 * i + 3] * inv)};
-    if (a.lse && half == 0)
+    if (a.lse && half == 0 && dv0 == 0)
         a.lse[(int64_t)(x.seq.begin + tok) * a.heads * a.per + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T, int D, int WAVES, int KB>
+template <typename T, int D, int DV, int WAVES, int KB>
 hipError_t launch_tiles(const PromptArgs &a, hipStream_t stream)
 {
     // no more tiles than this, however the sequences are cut
     constexpr int kRows = 32 * WAVES;
     const int64_t rows = (int64_t)a.s.n_tokens * a.per, each = rows / a.s.n_seqs;
     const int64_t tiles = a.s.cu ? rows / kRows + a.s.n_seqs : (each + kRows - 1) / kRows * a.s.n_seqs;
-    prompt_kernel<T, D, WAVES, KB><<<dim3((unsigned)(tiles * a.heads)), 64 * WAVES, 0, stream>>>(a);
+    prompt_kernel<T, D, DV, WAVES, KB><<<dim3((unsigned)(tiles * a.heads * (D / DV))), 64 * WAVES, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -479,12 +482,23 @@ bool wide_blocks(const PromptArgs &a)
     return blocks >= 512 && a.s.n_tokens / a.s.n_seqs >= (a.per >= 4 ? 2048 : 4096);
 }
 
+// Heads of 256 have their outputs' dimensions in two blocks, each of which makes all scores: half as
+// many products more, but two waves to a SIMD where the sums of one took the registers of both (4 x
+// 1500..2047, 16/4: 177 us and 201; 1 x 1000: 33 and 53; 1 x 8190: 774 and 769). Heads of 128 too while
+// that leaves a CU to each block (1 x 300, 32/32: 11.6 and 13.4; 1 x 1000, 8/8: 23.9 and 27.2; 1 x 2048,
+// 8/1: 40 and 45; with more, 4 x 1..1000, 32/8: 37 and 32).
+bool halved(const PromptArgs &a)
+{
+    return ((int64_t)a.s.n_tokens * a.per / 128 + a.s.n_seqs) * a.heads <= 128;
+}
+
 template <typename T>
 hipError_t launch(const PromptArgs &a, int dim, hipStream_t stream)
 {
-    if (dim == 64) return launch_tiles<T, 64, 4, 1>(a, stream);
-    if (dim == 256) return launch_tiles<T, 256, 4, 1>(a, stream);
-    return wide_blocks(a) ? launch_tiles<T, 128, 8, 2>(a, stream) : launch_tiles<T, 128, 4, 1>(a, stream);
+    if (dim == 64) return launch_tiles<T, 64, 64, 4, 1>(a, stream);
+    if (dim == 256) return launch_tiles<T, 256, 128, 4, 1>(a, stream);
+    if (halved(a)) return launch_tiles<T, 128, 64, 4, 1>(a, stream);
+    return wide_blocks(a) ? launch_tiles<T, 128, 128, 8, 2>(a, stream) : launch_tiles<T, 128, 128, 4, 1>(a, stream);
 }
 
 hqq_status refuse(const char *msg, hqq_status st = HQQ_ERR_ARG)
@@ -558,8 +572,8 @@ extern "C" hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride
     a.scale = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
     a.flip = scale < 0.f ? 0x80008000u : 0u;
     a.keep = scale == 0.f ? 0u : 0xffffffffu;
-    // blocks of the smallest tiles
-    if ((n_tokens * a.per / 128 + n_seqs) * a.heads >= (1 << 24)) return refuse("too many rows for one call", HQQ_ERR_UNSUPPORTED);
+    // blocks of the smallest tiles (a dimension of a grid has less than 2^32 threads)
+    if ((n_tokens * a.per / 128 + n_seqs) * a.heads * (head_dim == 256 ? 2 : 1) >= (1 << 24)) return refuse("too many rows for one call", HQQ_ERR_UNSUPPORTED);
     const hipStream_t str = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == HQQ_BF16 ? launch<Bf16>(a, head_dim, str) : launch<F16>(a, head_dim, str);
     if (e != hipSuccess) return refuse(hipGetErrorString(e), HQQ_ERR_DEVICE);
