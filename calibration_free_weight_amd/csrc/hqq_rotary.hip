@@ -6,7 +6,6 @@
 // that is left, whatever the position: nothing is lost at far positions, and no range is reduced.
 // Of it 32 bits are kept: 2^-33 turns, 7e-10 radians.
 #include <cmath>
-#include <type_traits>
 
 #include "hqq.h"
 #include "hqq_cache_internal.h"
@@ -33,7 +32,7 @@ struct RotaryArgs {
     int32_t n_tokens, pairs;    // rotary_dim / 2
     int32_t per_head, units;    // units of a head, of a token
     int32_t tokens, parts;      // tokens to a block; blocks to a token
-    int32_t rest0, dim;         // dimensions from rest0 to dim are copied
+    int32_t copied;             // dimensions behind those of the pairs
 };
 
 // Cosine and sine of a part of a turn, 2^-32 turns a step: the nearest quarter turn is taken off,
@@ -84,55 +83,83 @@ __device__ __forceinline__ void turn8(uint4 &lo, uint4 &hi, const float2 *cs)
     hi = uint4{y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16};
 }
 
-// Where a unit of the block's tokens lies: its first numbers, and the second of pairs that are turned.
+// Sixteen bytes at any even address, which global memory reads and writes as it does aligned ones.
+typedef uint32_t Sixteen __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ uint4 load16(const uint16_t *p)
+{
+    const Sixteen x = *reinterpret_cast<const Sixteen *>(p);
+    return uint4{x[0], x[1], x[2], x[3]};
+}
+__device__ __forceinline__ void store16(uint16_t *p, uint4 x)
+{
+    *reinterpret_cast<Sixteen *>(p) = Sixteen{x.x, x.y, x.z, x.w};
+}
+
+// A unit is eight pairs, or eight dimensions that are copied; a head ends with units of one, where
+// these do not go into eights. Where it lies: its first numbers, and the second of pairs.
 struct Unit {
     const uint16_t *in;
     uint16_t *out;
     int d0, d1, pair;           // pair: of the token's cosines and sines, the first; or -1: copied
+    bool wide;
 };
-template <bool NEIGHBOURS, bool WIDE>
+template <bool NEIGHBOURS>
 __device__ __forceinline__ Unit unit_of(const RotaryArgs &a, int t0, int j)
 {
-    constexpr int kPairs = WIDE ? 8 : 1, kWidth = WIDE ? 8 : 1;
     const unsigned t = (unsigned)j / (unsigned)a.units, of_token = j - t * a.units;
     unsigned h = of_token / (unsigned)a.per_head;
-    const int u = of_token - h * a.per_head, turning = a.pairs / kPairs;
+    int u = of_token - h * a.per_head;
     const bool second = h >= (unsigned)a.x[0].heads;
     const Tensor &x = a.x[second];
     if (second) h -= a.x[0].heads;
     Unit r;
     r.in = x.in + (t0 + (int64_t)t) * x.in_ts + h * x.in_hs;
     r.out = x.out + (t0 + (int64_t)t) * x.out_ts + h * x.out_hs;
-    if (u < turning) {
-        r.d0 = NEIGHBOURS ? 2 * kPairs * u : kPairs * u;
-        r.d1 = NEIGHBOURS ? r.d0 + kPairs : r.d0 + a.pairs;
-        r.pair = t * a.pairs + kPairs * u;
+    // eights that are turned and copied, then ones
+    const int turned8 = a.pairs >> 3, copied8 = a.copied >> 3, turned1 = a.pairs & 7;
+    r.wide = u < turned8 + copied8;
+    bool turn = u < turned8;
+    int first = 8 * u;                                      // pair, or dimension copied
+    if (!r.wide) {
+        u -= turned8 + copied8;
+        turn = u < turned1;
+        first = turn ? 8 * turned8 + u : 8 * copied8 + u - turned1;
+    } else if (!turn) {
+        first -= 8 * turned8;
+    }
+    if (turn) {
+        r.d0 = NEIGHBOURS ? 2 * first : first;
+        r.d1 = NEIGHBOURS ? r.d0 + (r.wide ? 8 : 1) : first + a.pairs;
+        r.pair = t * a.pairs + first;
     } else {
-        r.d0 = r.d1 = a.rest0 + kWidth * (u - turning);
+        r.d0 = r.d1 = 2 * a.pairs + first;
         r.pair = -1;
     }
     return r;
 }
 
-// A unit is eight pairs, or with !WIDE one; or as many dimensions that are copied. A block makes
-// the cosines and sines of its tokens once, for all heads, while its first units are on their way.
-// Bound by memory: 16390 tokens of 72 heads of 128, 604 MB: 106 us, 5.7 TB/s (part of it from the
-// last level's cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.3 us, 3.2 TB/s;
+// A block makes the cosines and sines of its tokens once, for all heads, while its first units are on
+// their way. Bound by memory: 16390 tokens of 72 heads of 128, 604 MB: 102 us, 5.9 TB/s (part of it from
+// the last level's cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.3 us, 3.2 TB/s;
 // a token 2.1 us, the launch and two loads that wait for each other.
-template <typename T, bool NEIGHBOURS, bool WIDE>
+template <typename T, bool NEIGHBOURS>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
 {
-    using Raw = std::conditional_t<WIDE, uint4, uint16_t>;
     extern __shared__ float2 cs[];      // [tokens][pairs]
     const int t0 = (int)(blockIdx.x / (unsigned)a.parts) * a.tokens, part = (int)(blockIdx.x % (unsigned)a.parts);
     const int tokens = min(a.tokens, a.n_tokens - t0), all = tokens * a.units;
     int j = part * kThreads + threadIdx.x;
     Unit x{};
-    Raw lo{}, hi{};
+    uint4 lo{}, hi{};
     const auto load = [&] {
-        x = unit_of<NEIGHBOURS, WIDE>(a, t0, j);
-        lo = *reinterpret_cast<const Raw *>(x.in + x.d0);
-        hi = *reinterpret_cast<const Raw *>(x.in + x.d1);
+        x = unit_of<NEIGHBOURS>(a, t0, j);
+        if (__builtin_expect(x.wide, 1)) {
+            lo = load16(x.in + x.d0);
+            hi = load16(x.in + x.d1);
+        } else {
+            lo.x = x.in[x.d0];
+            hi.x = x.in[x.d1];
+        }
     };
     if (j < all) load();
     for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
@@ -142,29 +169,28 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
     }
     __syncthreads();
     while (j < all) {
-        if (x.pair >= 0) {
-            if constexpr (WIDE) {
+        if (__builtin_expect(x.wide, 1)) {
+            if (x.pair >= 0) {
                 turn8<T, NEIGHBOURS>(lo, hi, cs + x.pair);
-            } else {
-                uint32_t p, q;
-                turn<T>(to_f32<T>(lo), to_f32<T>(hi), cs[x.pair], p, q);
-                lo = (uint16_t)p;
-                hi = (uint16_t)q;
+                store16(x.out + x.d1, hi);
             }
-            *reinterpret_cast<Raw *>(x.out + x.d1) = hi;
+            store16(x.out + x.d0, lo);
+        } else {
+            if (x.pair >= 0) {
+                turn<T>(to_f32<T>(lo.x), to_f32<T>(hi.x), cs[x.pair], lo.x, hi.x);
+                x.out[x.d1] = (uint16_t)hi.x;
+            }
+            x.out[x.d0] = (uint16_t)lo.x;
         }
-        *reinterpret_cast<Raw *>(x.out + x.d0) = lo;
         j += a.parts * kThreads;
         if (j < all) load();
     }
 }
 
 template <typename T, bool NEIGHBOURS>
-void launch(const RotaryArgs &a, bool wide, unsigned blocks, hipStream_t stream)
+void launch(const RotaryArgs &a, unsigned blocks, hipStream_t stream)
 {
-    const size_t lds = (size_t)a.tokens * a.pairs * sizeof(float2);
-    if (wide) rotary_kernel<T, NEIGHBOURS, true><<<blocks, kThreads, lds, stream>>>(a);
-    else rotary_kernel<T, NEIGHBOURS, false><<<blocks, kThreads, lds, stream>>>(a);
+    rotary_kernel<T, NEIGHBOURS><<<blocks, kThreads, (size_t)a.tokens * a.pairs * sizeof(float2), stream>>>(a);
 }
 
 hqq_status refuse(const char *msg)
@@ -216,7 +242,7 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     if (n_tokens < 0 || n_tokens > (1 << 24)) return refuse("n_tokens must be in [0, 2^24]");
     if (n_rows < 0 || n_rows > 2 || (n_rows > 0 && !rows)) return refuse("rows must be one or two tensors");
     RotaryArgs a{};
-    bool wide = rotary_dim % 16 == 0 && head_dim % 8 == 0, rest = false;
+    bool rest = false;
     int heads = 0;
     for (int i = 0; i < n_rows; ++i) {
         const hqq_rotary_rows &r = rows[i];
@@ -227,9 +253,7 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
         const int64_t strides[] = {r.in_token_stride, r.in_head_stride, r.out_token_stride, r.out_head_stride};
         for (int64_t s : strides) {
             if (s < 0 || s > (int64_t(1) << 36)) return refuse("rows: strides must be in [0, 2^36]");
-            wide = wide && s % 8 == 0;
         }
-        wide = wide && aligned(r.in, 16) && aligned(r.out, 16);
         if (r.in == r.out) {
             if (strides[0] != strides[2] || strides[1] != strides[3])
                 return refuse("rows: in place, the strides of in and out must be the same");
@@ -246,16 +270,14 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     }
     if (!freqs || !positions || !aligned(freqs, 8) || !aligned(positions, 4))
         return refuse("freqs and positions must be non-null, 8- and 4-byte aligned");
-    const int turning = rotary_dim / (wide ? 16 : 2);
     a.freqs = freqs;
     a.positions = positions;
     a.scale = scale;
     a.n_tokens = (int32_t)n_tokens;
     a.pairs = rotary_dim / 2;
-    a.per_head = turning + (rest ? (head_dim - rotary_dim) / (wide ? 8 : 1) : 0);
+    a.copied = rest ? head_dim - rotary_dim : 0;
+    a.per_head = a.pairs / 8 + a.pairs % 8 + a.copied / 8 + a.copied % 8;
     a.units = a.per_head * heads;
-    a.rest0 = rotary_dim;
-    a.dim = head_dim;
     // A unit to a thread; with fewer than a block's in a token, several tokens. (Four to a thread: 16390
     // tokens of 72 heads of 128 107 us and 102 with one; 5000 of 16 heads of 256, a quarter turned, 15.9
     // and 17.3, for the angles are made more often; no difference for 4000 and fewer of the former.)
@@ -270,11 +292,11 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     }
     const hipStream_t str = static_cast<hipStream_t>(stream);
     if (dtype == HQQ_BF16) {
-        if (interleaved) launch<Bf16, true>(a, wide, (unsigned)blocks, str);
-        else launch<Bf16, false>(a, wide, (unsigned)blocks, str);
+        if (interleaved) launch<Bf16, true>(a, (unsigned)blocks, str);
+        else launch<Bf16, false>(a, (unsigned)blocks, str);
     } else {
-        if (interleaved) launch<F16, true>(a, wide, (unsigned)blocks, str);
-        else launch<F16, false>(a, wide, (unsigned)blocks, str);
+        if (interleaved) launch<F16, true>(a, (unsigned)blocks, str);
+        else launch<F16, false>(a, (unsigned)blocks, str);
     }
     const hipError_t e = hipGetLastError();
     const hqq_status st = e == hipSuccess ? HQQ_OK : HQQ_ERR_DEVICE;

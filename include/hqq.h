@@ -318,8 +318,7 @@ typedef struct hqq_rotary_rows {
 /* Turn one or two tensors (queries and keys) in one launch. freqs: device, uint64
  * [rotary_dim/2]; positions: device, int32 [n_tokens], any values. rotary_dim is even, at most
  * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24. Any strides and
- * 2-byte alignment will do; 16-byte pointers, strides that are multiples of 8 and rotary_dim a
- * multiple of 16 (head_dim of 8) take the fast path. Nothing is allocated. */
+ * 2-byte alignment will do; rotary_dim a multiple of 16 is fastest. Nothing is allocated. */
 hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, float scale,
                       const int32_t *positions, int64_t n_tokens, int head_dim, int dtype,
                       const hqq_rotary_rows *rows, int n_rows, void *stream);

@@ -62,6 +62,9 @@ CASES = [
     (F, 1024, 1024, False, 2, 1, [123456]),
     (B, 65, 64, False, 2, 1, [4, 5]),
     (F, 128, 64, False, 300, 7, [11, 12, 13]),
+    (B, 128, 74, False, 5, 3, [1, 70000, 3]),
+    (F, 256, 254, True, 3, 1, [5, 6]),
+    (B, 31, 30, False, 3, 2, [17]),
 ]
 
 
