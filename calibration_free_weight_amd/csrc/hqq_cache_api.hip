@@ -369,7 +369,8 @@ hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs 
     if (max_kept > 0 && (!kept || !aligned(kept, 4))) return refuse("kept must be non-null and 4-byte aligned");
     if (!seqs->lens || !aligned(seqs->lens, 4) || !aligned(seqs->cu_tokens, 4) || !aligned(lens_out, 4))
         return refuse("lens must be non-null, and lens, cu_tokens and lens_out 4-byte aligned");
-    if (lens_out == seqs->lens) return refuse("lens_out must not be lens");
+    if (lens_out && lens_out < seqs->lens + seqs->n_seqs && seqs->lens < lens_out + seqs->n_seqs)
+        return refuse("lens_out must not overlap lens");
     hqq::KeepArgs a{view_of(caches, seqs), kept, lens_out, max_kept, caches->n_heads, caches->head_dim / caches->group_size, {}};
     hipError_t e = hipSuccess;
     for (int first = 0; first < n_caches && e == hipSuccess; first += hqq::kKeepLayers) {

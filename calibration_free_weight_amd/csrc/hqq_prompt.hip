@@ -33,7 +33,7 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 
 constexpr int kAhead = 2;         // fragments asked for before they are used
-constexpr int64_t kMaxKeyStride = 1 << 23;
+constexpr int64_t kMaxKeyStride = 1 << 22;
 constexpr float kLog2e = 1.44269504088896341f;
 // How far a score (to base 2) may lie above the maximum that weights are taken from.
 constexpr float kSlack = 8.f;
@@ -85,7 +85,7 @@ __device__ __forceinline__ u32x2 read_transposed(const void *p)
 }
 
 // The first n rows from p (uniform), of `dim` numbers each and `ts` apart, no more than `most`, as a
-// buffer: what is read behind them is 0. (most * ts * 2 stays below 2^31.)
+// buffer: what is read behind them is 0. (Up to 256 rows' offsets stay below 2^31.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint16_t *p, int n, int most, int ts, int dim)
 {
     const uint64_t at = (uint64_t)p;
@@ -93,9 +93,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint16_t *p, i
     const int bytes = ((min(n, most) - 1) * ts + dim) * 2 & -n >> 31;      // 0 without rows, and no branch
     return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int lane_offset, int offset)
+// The whole offset is the lanes', which is the one that the buffer's end is held against.
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int offset)
 {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0);
+    return __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
 }
 
 // Whether one of two numbers is an infinity or NaN; the two with such replaced by 0.
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
         const auto k = rows_from(next_k, left_k, kKeys, k_ts, D);
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            kr[i] = load16(k, r0 * k_ts * 2 + 16 * (place ^ key_swap(r0 + i * kApart)), i * kApart * k_ts * 2);
+            kr[i] = load16(k, (r0 + i * kApart) * k_ts * 2 + 16 * (place ^ key_swap(r0 + i * kApart)));
         next_k += kKeys * k_ts;
         left_k -= kKeys;
     };
@@ -260,7 +261,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
         const auto v = rows_from(next_v, left_v, kKeys, v_ts, DV);
 #pragma unroll
         for (int i = 0; i < kVEach; ++i)
-            vr[i] = load16(v, vr0 * v_ts * 2 + 16 * (vplace ^ value_swap(vr0 + i * kVApart)), i * kVApart * v_ts * 2);
+            vr[i] = load16(v, (vr0 + i * kVApart) * v_ts * 2 + 16 * (vplace ^ value_swap(vr0 + i * kVApart)));
         next_v += kKeys * v_ts;
         left_v -= kKeys;
     };
@@ -547,7 +548,7 @@ extern "C" hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride
     }
     // offsets within a step's keys are 32 bits
     if (k_token_stride > kMaxKeyStride || v_token_stride > kMaxKeyStride)
-        return refuse("the token strides of k and v must be at most 2^23");
+        return refuse("the token strides of k and v must be at most 2^22");
     PromptArgs a{};
     a.q = static_cast<const uint16_t *>(q);
     a.k = static_cast<const uint16_t *>(k);

@@ -542,7 +542,7 @@ def hqq_cache_keep(caches, table, lens, kept, n_tokens, lens_out=None, cu_tokens
     """Move the accepted tokens of the last call (its n_tokens rows are the last tokens of their
     sequences) behind what was there before it, in `caches`, one cache or the list of all layers'.
     kept: int32 [n_seqs, max_kept], for each sequence the accepted rows by their number, ascending,
-    with -1 behind the last. lens_out (int32 [n_seqs], not lens) gets the new lengths."""
+    with -1 behind the last. lens_out (int32 [n_seqs], apart from lens) gets the new lengths."""
     T = _torch or _th()
     caches = [caches] if isinstance(caches, dict) else list(caches)
     if not caches:

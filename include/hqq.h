@@ -290,7 +290,7 @@ typedef enum hqq_dtype {
  * with `interleaved` (2i, 2i + 1), and becomes
  *   (a, b) -> scale * (a cos x - b sin x, b cos x + a sin x),  x = 2 pi * position * freqs[i] / 2^64;
  * the other dimensions stay. freqs are turns per position in 64 bits behind the point, so far
- * positions lose nothing: x is off by 10^-9 whatever the position, cosine and sine by 2^-23; products
+ * positions lose nothing: x is off by about 10^-9 whatever the position, cosine and sine by 2^-23; products
  * are in binary32, rounded once to the type. Negated positions turn back (with scale 1, that is
  * also the gradient's way). */
 
@@ -327,7 +327,7 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
  * Causal attention of packed sequences over themselves, with keys and values as they are (what
  * hqq_cache_write then stores for the tokens to come). q and out: [n_tokens, n_q_heads, head_dim],
  * k and v: [n_tokens, n_kv_heads, head_dim], of type dtype, with strides in elements between tokens
- * and heads (multiples of 8, between tokens of k and v at most 2^23; dimensions contiguous;
+ * and heads (multiples of 8, between tokens of k and v at most 2^22; dimensions contiguous;
  * pointers 16-byte aligned), e.g. slices of one fused projection's output; head_dim 64, 128 or 256; n_q_heads a multiple of n_kv_heads, query
  * head h reads key/value head h / (n_q_heads / n_kv_heads). Sequence b has rows cu_tokens[b] ..
  * cu_tokens[b+1]-1 (device, int32 [n_seqs + 1]), or n_tokens/n_seqs rows each when cu_tokens is
@@ -486,7 +486,7 @@ size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seq
  * rows, ascending; a list ends with its row of kept, or before the first entry that is negative,
  * n_b or more, or not above the one before it. With m_b entries, token kept[b][i] moves to position
  * lens[b] - n_b + i: codes and grids are copied as they are. lens_out (device, int32 [n_seqs],
- * nullable, not lens) gets lens[b] - n_b + m_b, 0 at least. Positions from there on hold nothing of
+ * nullable, apart from lens) gets lens[b] - n_b + m_b, 0 at least. Positions from there on hold nothing of
  * meaning afterwards. Where either place is not in the cache, that token does not move. Pages that
  * hold the moved places must belong to one sequence alone. One launch for up to 64 caches. */
 hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs *seqs,

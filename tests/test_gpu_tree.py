@@ -36,6 +36,11 @@ TREES = [
     (B, 4, 64, 64, 16, 1, 4, [40] * 70, [3] * 70, 1),           # more sequences than a wave has lanes
     (F, 8, 256, 32, 64, 1, 16, [130, 400], [33, 64], 1),
     (B, 4, 128, 64, 64, 8, 8, [800, 750], [100, 128], 2),
+    # tiles of 128 rows, and of 64 and 32 with heads of 256
+    (B, 4, 128, 64, 64, 40, 1, [4000, 3900, 4000, 100], [100, 100, 97, 100], 2),
+    (F, 8, 64, 32, 32, 64, 1, [3000, 2900, 3000], [100, 101, 99], 2),
+    (F, 8, 256, 128, 64, 16, 1, [4600, 4600, 4500, 4600], [100, 99, 100, 100], 2),
+    (B, 4, 256, 64, 32, 16, 1, [2000] * 8, [25] * 8, 1),
 ]
 
 
@@ -73,6 +78,26 @@ def test_masks_of_chains_are_attention(H, dtype, nbits, kv, per, lens, new):
     q = torch.randn(cu[-1], kv * per, 128, generator=gen).to(dtype).cuda()
     args = (cache, i32(table), i32(lens))
     assert torch.equal(H.cache_attention_tree(*args, masks, q, cu_tokens=i32(cu)), H.cache_attention(*args, q, cu_tokens=i32(cu)))
+
+
+@pytest.mark.parametrize("dtype,nbits,dim,kv,per,lens,new", [(B, 4, 128, 2, 8, [700, 90], [7, 9]), (F, 8, 64, 1, 4, [500], [80]),
+                                                             (B, 8, 128, 40, 1, [3000, 3100, 3000, 3000], [120] * 4)])
+def test_chains_over_values_of_very_different_size(H, dtype, nbits, dim, kv, per, lens, new):
+    """Tokens whose values lie far apart in size come behind the others in an item: with masks too."""
+    gen = torch.Generator().manual_seed(9)
+    table, n_pages, _ = layout(lens, 64, gen)
+    cache = H.alloc_cache(n_pages, 64, kv, dim, nbits, 32, dtype)
+    n = sum(lens)
+    k = values(n, kv, dim, dtype, gen)
+    size = 2.0 ** torch.randint(-18, 8, (n, 1, 1), generator=gen)
+    v = (torch.randn(n, kv, dim, generator=gen) * size).to(dtype).cuda()
+    H.hqq_cache_write(cache, i32(table), i32(lens), k, v, cu_tokens=i32(cumulated(lens)))
+    cu, words = cumulated(new), (max(new) + 63) // 64
+    masks = T.to_words([(1 << (j + 1)) - 1 for m in new for j in range(m)], words).cuda()
+    q = torch.randn(cu[-1], kv * per, dim, generator=gen).to(dtype).cuda()
+    args = (cache, i32(table), i32(lens))
+    got = H.cache_attention_tree(*args, masks, q, cu_tokens=i32(cu))
+    assert torch.isfinite(got).all() and torch.equal(got, H.cache_attention(*args, q, cu_tokens=i32(cu)))
 
 
 def test_masks_of_any_bits(H):

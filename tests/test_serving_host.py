@@ -108,7 +108,7 @@ def prompt(H, **kw):
     dict(hq=3), dict(hq=0), dict(hq=-2), dict(hk=0), dict(hk=1025, hq=1025), dict(hq=(1 << 20) + 2), dict(dim=96), dict(dim=0), dict(dim=512),
     dict(dtype=2), dict(dtype=-1), dict(seqs=-1), dict(seqs=4097), dict(n=-1), dict(n=(1 << 24) + 2), dict(n=7),
     dict(cu=P + 2), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(lse=P + 2),
-    dict(n=1 << 24, hq=128, hk=2), dict(k=(P, (1 << 23) + 8, 128)), dict(v=(P, (1 << 23) + 8, 128)),
+    dict(n=1 << 24, hq=128, hk=2), dict(k=(P, (1 << 22) + 8, 128)), dict(v=(P, (1 << 22) + 8, 128)),
     *[{x: y} for x in ("q", "k", "v", "out") for y in ((None, 512, 128), (P + 8, 512, 128), (P, 511, 128), (P, 512, 4), (P, -512, 128),
                                                        (P, 512, 1 << 37))]], ids=str)
 def test_prompt_refuses(H, kw):
@@ -167,7 +167,7 @@ def keep(H, caches, s, kept=P, most=3, out=2 * P, n=None):
 
 def test_keep_refuses(H):
     one = [cache(H)]
-    for kw in (dict(kept=None), dict(kept=P + 2), dict(most=-1), dict(most=(1 << 24) + 1), dict(out=P + 2), dict(out=0x6000),
+    for kw in (dict(kept=None), dict(kept=P + 2), dict(most=-1), dict(most=(1 << 24) + 1), dict(out=P + 2), dict(out=0x6000), dict(out=0x6004), dict(out=0x5ffc),
                dict(n=0), dict(n=-1), dict(n=1025)):
         assert keep(H, one, seqs(H), **kw) == H.HQQ_ERR_ARG and H.hqq_last_error(), kw
     other = dict(k_codes=0x8000)

@@ -42,11 +42,11 @@ def attention(held, table, lens, cu, q, scale, tree):
         t, ln = hi - lo, min(max(lens[b], 0), len(table[b]) * c["page_size"])
         k, ka, ok = held.tokens("k", table[b], ln)
         v, va, _ = held.tokens("v", table[b], ln)
-        seen = torch.zeros(t, ln, dtype=torch.bool)
+        seen = torch.ones(t, ln, dtype=torch.bool)
         for i in range(t):
-            for p in range(ln):
+            for p in range(max(ln - t, 0), ln):
                 j = p - (ln - t)
-                seen[i, p] = j < 0 or (j // 64 < tree.shape[1] and words[lo + i][j // 64] >> j % 64 & 1)
+                seen[i, p] = j // 64 < tree.shape[1] and words[lo + i][j // 64] >> j % 64 & 1
         seen = (seen & ok[None])[None, None]
         x = q[lo:hi].cpu().double().reshape(t, heads, per, dim).permute(1, 2, 0, 3)
         s = torch.matmul(x, k.transpose(1, 2)[:, None]) * scale
