@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
     constexpr int kEach = kKeys * kChunks / kThreads;       // chunks of keys to a thread
     constexpr int kApart = kThreads / kChunks;              // rows between a thread's chunks
     constexpr int kVChunks = DV / 8, kVEach = kKeys * kVChunks / kThreads, kVApart = kThreads / kVChunks;
-    static_assert(kEach * kThreads == kKeys * kChunks, "whole chunks for each thread");
+    static_assert(kEach * kThreads == kKeys * kChunks && kVEach * kThreads == kKeys * kVChunks, "whole chunks for each thread");
     __shared__ u32x4 keys[2][kKeys * kChunks], values[2][kKeys * kVChunks];
     __shared__ int32_t scan[2][WAVES], found[2], bad[2];    // bad: the last step whose values were not finite
     Tile x;
@@ -468,19 +468,23 @@ hipError_t launch_tiles(const PromptArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Heads of 128 in blocks of 128 rows that go 32 keys a step, two to a CU, or of 256 rows and 64 keys,
+// Blocks of 128 rows that go 32 keys a step, two to a CU, or of 256 rows and with heads of 128 64 keys,
 // one to a CU, which fetch a key for twice the rows and meet half as often, but begin and end alone.
-// Measured in us, of 128 and of 256 rows (sequences x tokens, query heads / key heads):
+// Measured in us, of 128 and of 256 rows (sequences x tokens, query heads / key heads), heads of 128:
 //   1 x 8190, 64/8    1062   991      1 x 2048, 32/32   56    62      2 x 4096, 32/32   296   285
 //   1 x 4096, 32/8     155   137      1 x 8190, 8/8    183   198      3 x 3000, 40/40   339   348
 //   1 x 2048, 64/8      94    88      16 x 1024, 32/8  201   225      2 x 2048, 40/40   113   116
 //   4 x 2048, 16/4      87    79      64 x 512, 32/8   324   343      8 x 2048, 32/8    319   325
+// and of 256:
+//   1 x 8190, 16/4     757   718      1 x 4096, 16/4   215   195      8 x 2048, 16/4    441   443
+//   1 x 16384, 8/2    1480  1391      1 x 1000, 16/4    33    41      4 x 1500..2047, 16/4   173   181
 // so the wide ones have long sequences (the rows of one head cover fewer tokens the more heads share
-// it, and a tile's end wastes less) and two blocks at least to a CU.
-bool wide_blocks(const PromptArgs &a)
+// it, and a tile's end wastes less) and two blocks at least to a CU. (Heads of 64: 599 and 616 at 1 x
+// 8190, 64/8.)
+bool wide_blocks(const PromptArgs &a, int dim)
 {
-    const int64_t blocks = (int64_t)a.s.n_tokens * a.per * a.heads / 256;
-    return blocks >= 512 && a.s.n_tokens / a.s.n_seqs >= (a.per >= 4 ? 2048 : 4096);
+    const int64_t blocks = (int64_t)a.s.n_tokens * a.per * a.heads / 256 * (dim / 128);
+    return blocks >= 512 && a.s.n_tokens / a.s.n_seqs >= (dim == 128 && a.per >= 4 ? 2048 : 4096);
 }
 
 // Heads of 256 have their outputs' dimensions in two blocks, each of which makes all scores: half as
@@ -497,9 +501,10 @@ template <typename T>
 hipError_t launch(const PromptArgs &a, int dim, hipStream_t stream)
 {
     if (dim == 64) return launch_tiles<T, 64, 64, 4, 1>(a, stream);
-    if (dim == 256) return launch_tiles<T, 256, 128, 4, 1>(a, stream);
+    const bool wide = wide_blocks(a, dim);
+    if (dim == 256) return wide ? launch_tiles<T, 256, 128, 8, 1>(a, stream) : launch_tiles<T, 256, 128, 4, 1>(a, stream);
     if (halved(a)) return launch_tiles<T, 128, 64, 4, 1>(a, stream);
-    return wide_blocks(a) ? launch_tiles<T, 128, 128, 8, 2>(a, stream) : launch_tiles<T, 128, 128, 4, 1>(a, stream);
+    return wide ? launch_tiles<T, 128, 128, 8, 2>(a, stream) : launch_tiles<T, 128, 128, 4, 1>(a, stream);
 }
 
 hqq_status refuse(const char *msg, hqq_status st = HQQ_ERR_ARG)

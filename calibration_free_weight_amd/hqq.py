@@ -8,6 +8,7 @@ function raises.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import os
 import struct
 
@@ -365,19 +366,20 @@ def _bad(msg):
     return HQQError(HQQ_ERR_ARG, msg)
 
 
+_cache_fields = operator.itemgetter("k_codes", "v_codes", "k_meta", "v_meta", "page_size", "n_heads", "head_dim",
+                                    "nbits", "group_size")
+
+
 def _cache_struct(cache):
     """The C struct of a cache dict, its GPU's index and its type."""
     T = _torch or _th()
-    kc, vc, km, vm = cache["k_codes"], cache["v_codes"], cache["k_meta"], cache["v_meta"]
-    page, heads, dim = cache["page_size"], cache["n_heads"], cache["head_dim"]
-    nbits, group = cache["nbits"], cache["group_size"]
+    kc, vc, km, vm, page, heads, dim, nbits, group = _cache_fields(cache)
     codes, meta, dtype, dev = kc.shape, km.shape, km.dtype, kc.get_device()
-    n = codes[0]
-    if codes != (n, heads, page * dim * nbits // 8) or vc.shape != codes or \
-            not kc.dtype == vc.dtype == T.uint8:
+    n, u8 = codes[0], T.uint8
+    if codes != (n, heads, page * dim * nbits // 8) or vc.shape != codes or kc.dtype is not u8 or vc.dtype is not u8:
         raise _bad("k_codes and v_codes must be uint8 [n_pages, n_heads, page_size*head_dim*nbits/8]")
-    if meta != (n, heads, page, dim // max(group, 1), 2) or vm.shape != meta or vm.dtype != dtype or \
-            (dtype != T.float16 and dtype != T.bfloat16):
+    if meta != (n, heads, page, dim // max(group, 1), 2) or vm.shape != meta or vm.dtype is not dtype or \
+            (dtype is not T.float16 and dtype is not T.bfloat16):
         raise _bad("k_meta and v_meta must be [n_pages, n_heads, page_size, head_dim/group_size, 2] "
                    "of float16 or bfloat16")
     if not (kc.is_contiguous() and vc.is_contiguous() and km.is_contiguous() and vm.is_contiguous()):
@@ -385,7 +387,7 @@ def _cache_struct(cache):
     if dev < 0 or not dev == vc.get_device() == km.get_device() == vm.get_device():
         raise _bad("the cache's tensors must be on one GPU")
     return _pack_cache(kc.data_ptr(), vc.data_ptr(), km.data_ptr(), vm.data_ptr(), n, page, heads,
-                       dim, nbits, group, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16), dev, dtype
+                       dim, nbits, group, HQQ_BF16 if dtype is T.bfloat16 else HQQ_F16), dev, dtype
 
 
 def _seqs_struct(table, lens, cu_tokens, n_tokens, dev):
@@ -635,6 +637,14 @@ def rotary_frequencies(rotary_dim, theta=10000.0, factor=1.0, original_len=0, lo
 _pack_rotary = struct.Struct("@P2qP2qi4x").pack
 
 
+def _alike(x, dev, stream):
+    """A contiguous tensor of x's shape, type and device, of the call's stream."""
+    T = _torch
+    if stream is None:
+        return T.empty_like(x, memory_format=T.contiguous_format)
+    return _on_stream(dev, stream, lambda: T.empty_like(x, memory_format=T.contiguous_format))
+
+
 def _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, fresh):
     """hqq_rotary, or with `fresh` into tensors that it allocates (contiguous) and returns."""
     T = _torch or _th()
@@ -654,12 +664,11 @@ def _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, fr
             raise _bad(f"{name} must be [n_tokens, heads, head_dim] of q's tokens and dimensions")
         at = _rows(x, shape, dev, dtype, name)
         if fresh:
-            out = _on_stream(dev, stream, lambda: T.empty_like(x, memory_format=T.contiguous_format))
+            out = _alike(x, dev, stream)
             outs.append(out)
-            to = out.data_ptr(), shape[1] * dim, dim
+            rows += _pack_rotary(*at, out.data_ptr(), shape[1] * dim, dim, shape[1])
         else:
-            to = at if out is None else _rows(out, shape, dev, dtype, name + "_out")
-        rows += _pack_rotary(*at, *to, shape[1])
+            rows += _pack_rotary(*at, *(at if out is None else _rows(out, shape, dev, dtype, name + "_out")), shape[1])
     st = _on(dev, (_L or lib()).hqq_rotary, freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, scale,
              positions.data_ptr(), n, dim, HQQ_BF16 if dtype == T.bfloat16 else HQQ_F16, rows, len(tensors),
              _stream_of(dev, stream))
@@ -704,7 +713,7 @@ def _prompt(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream):
                             not lse.is_contiguous()):
         raise _bad("lse must be a contiguous float32 [n_tokens, n_q_heads] on q's device")
     if out is None:
-        out = _on_stream(dev, stream, lambda: T.empty_like(q, memory_format=T.contiguous_format))
+        out = _alike(q, dev, stream)
         to = out.data_ptr(), heads * dim, dim
     else:
         to = _rows(out, shape, dev, dtype, "out")

@@ -128,25 +128,26 @@ def test_prompt_attention(H, dtype, dim, hk, per, lens):
         assert got.is_contiguous() and torch.equal(got, obuf[:n, 1:-1])
 
 
-@pytest.mark.parametrize("dtype,lens", [(F, [2100, 2049]), (B, [4130])])
-def test_long_prompts_of_many_heads(H, dtype, lens):
-    """Blocks of 256 rows, with values that are not finite and a scale below zero; three key heads are
-    looked at in full."""
+@pytest.mark.parametrize("dtype,dim,hk,lens", [(F, 128, 5, [2100, 2049]), (B, 128, 5, [4130]), (F, 256, 2, [4130])])
+def test_long_prompts_of_many_heads(H, dtype, dim, hk, lens):
+    """Blocks of 256 rows, with values that are not finite and a scale below zero; every other key head
+    is looked at in full."""
     gen = torch.Generator().manual_seed(lens[0])
-    hk, per, cu = 5, 8, cumulated(lens)
-    q, k, v = (x.clone() for x in inputs(cu[-1], hk * per, hk, 128, dtype, gen))
-    ref = {h: reference(q[:, per * h:per * h + per], k[:, h:h + 1], v[:, h:h + 1], list(zip(cu, cu[1:])), -0.08) for h in (0, 2, 4)}
-    v[1234, 2, 77], v[2047, 4, 0] = math.nan, math.inf
+    per, cu, last = 8, cumulated(lens), hk - 1 - (hk - 1) % 2
+    q, k, v = (x.clone() for x in inputs(cu[-1], hk * per, hk, dim, dtype, gen))
+    scale = -0.9 * dim ** -0.5
+    ref = {h: reference(q[:, per * h:per * h + per], k[:, h:h + 1], v[:, h:h + 1], list(zip(cu, cu[1:])), scale) for h in range(0, hk, 2)}
+    v[1234, 0, 77], v[2047, last, dim - 1] = math.nan, math.inf
     lse = torch.empty(cu[-1], hk * per, dtype=torch.float32, device="cuda")
-    got = H.prompt_attention(q, k, v, cu_tokens=i32(cu), scale=-0.08, lse=lse)
+    got = H.prompt_attention(q, k, v, cu_tokens=i32(cu), scale=scale, lse=lse)
     end = lens[0]
     for h, r in ref.items():
         x = got[:, per * h:per * h + per].cpu()
         seen = torch.zeros(x.shape, dtype=torch.bool)
-        if h == 2:
+        if h == 0:
             seen[1234:end, :, 77] = True
-        if h == 4:
-            seen[2047:end, :, 0] = True
+        if h == last:
+            seen[2047:end, :, dim - 1] = True
         assert not torch.isfinite(x[seen]).any()
         x[seen] = r[0][seen].to(dtype)
         check(x, lse[:, per * h:per * h + per], r)
