@@ -446,13 +446,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
     l = of_row(l, [](float p, float q) { return p + q; });
     if (row >= x.n_rows) return;
     const float inv = l > 0.f ? 1.f / l : l;
-    uint16_t *to = a.out + (x.seq.begin + tok) * a.o_ts + hq * a.o_hs + dv0 + 4 * half;
+    uint16_t *to = a.out + (x.seq.begin + tok) * a.o_ts + hq * a.o_hs + dv0 + 8 * half;
 #pragma unroll
     for (int j = 0; j < DV / 32; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<u32x2 *>(to + 32 * j + 8 * i) = u32x2{round2<T>(o[j][4 * i] * inv, o[j][4 * i + 1] * inv),
-                                                                    round2<T>(o[j][4 * i + 2] * inv, o[j][4 * i + 3] * inv)};
+        for (int i = 0; i < 16; i += 8) {
+            // of each sixteen dimensions the first lane of a row gets the first eight, the other the others
+            const auto p = __builtin_amdgcn_permlane32_swap(round2<T>(o[j][i] * inv, o[j][i + 1] * inv),
+                                                            round2<T>(o[j][i + 4] * inv, o[j][i + 5] * inv), false, false);
+            const auto q = __builtin_amdgcn_permlane32_swap(round2<T>(o[j][i + 2] * inv, o[j][i + 3] * inv),
+                                                            round2<T>(o[j][i + 6] * inv, o[j][i + 7] * inv), false, false);
+            *reinterpret_cast<u32x4 *>(to + 32 * j + 2 * i) = u32x4{p[0], q[0], p[1], q[1]};
+        }
     if (a.lse && half == 0 && dv0 == 0)
         a.lse[(int64_t)(x.seq.begin + tok) * a.heads * a.per + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
