@@ -45,9 +45,18 @@ struct PromptArgs {
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
     SeqView s;                  // cu, n_seqs, n_tokens
     int32_t heads, per;         // key/value heads, query heads to one
+    uint64_t inv;               // 2^64 / per, rounded up; 0 with one
     float scale;                // |scale| times log2(e), or 1 where scale is 0
     uint32_t flip, keep;        // of two queries: bits that change, bits that stay
 };
+
+// row / per, of rows below 2^30 and up to 2^20 heads: what inv is too large by adds less than 2^-34.
+__device__ __forceinline__ int token_of(const PromptArgs &a, int row)
+{
+    if (a.inv == 0) return row;
+    const uint64_t high = (uint64_t)(uint32_t)row * (uint32_t)(a.inv >> 32);
+    return (int)((high + __umulhi((uint32_t)row, (uint32_t)a.inv)) >> 32);
+}
 
 template <typename T>
 __device__ __forceinline__ f32x16 mfma(const u32x4 a, const u32x4 b, const f32x16 c)
@@ -232,12 +241,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int n = x.seq.end - x.seq.begin;
     const int wave_row = x.row0 + 32 * wave, row = wave_row + col;      // a lane's row, and its token
-    const int tok = min(row, x.n_rows - 1) / a.per, hq = h * a.per + (row - tok * a.per);
+    const int tok = token_of(a, min(row, x.n_rows - 1)), hq = h * a.per + (row - tok * a.per);
     // tokens of the block's and the wave's first and last rows
-    const int first = x.row0 / a.per, last = min(x.row0 + kRows, x.n_rows) - 1;
-    const int wave_first = min(wave_row, x.n_rows - 1) / a.per;
-    const int wave_last = min(wave_row + 31, x.n_rows - 1) / a.per;
-    const int steps = last / a.per / kKeys + 1;             // of keys that some row sees
+    const int first = token_of(a, x.row0), last = min(x.row0 + kRows, x.n_rows) - 1;
+    const int wave_first = token_of(a, min(wave_row, x.n_rows - 1));
+    const int wave_last = token_of(a, min(wave_row + 31, x.n_rows - 1));
+    const int steps = token_of(a, last) / kKeys + 1;            // of keys that some row sees
 
     // where a thread's chunks come from: rows and places are swapped within LDS so that no two lanes
     // that read at a time meet in a bank. Rows behind the sequence are beyond the buffer, and 0.
@@ -409,9 +418,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
     for (int d = 0; d < D / 16; ++d) {
         qf[d] = u32x4{0, 0, 0, 0};
         if (row < x.n_rows) qf[d] = *reinterpret_cast<const u32x4 *>(q + 16 * d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qf[d][e] = (qf[d][e] & a.keep) ^ a.flip;
     }
+    if (__builtin_expect(a.flip != 0 || a.keep == 0, 0))
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qf[d][e] = (qf[d][e] & a.keep) ^ a.flip;
     __syncthreads();                    // `bad` is set
     check_values(0);
     put_keys(0);
@@ -578,6 +590,7 @@ extern "C" hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride
     a.s.n_tokens = (int32_t)n_tokens;
     a.heads = n_kv_heads;
     a.per = n_q_heads / n_kv_heads;
+    a.inv = a.per == 1 ? 0 : UINT64_MAX / a.per + 1;
     // the sign of scale goes to the queries, and a scale of 0 makes them 0: the largest score is then
     // the largest product, and what a row does not see stays at -infinity
     a.scale = scale == 0.f ? 1.f : std::fabs(scale) * kLog2e;
