@@ -328,7 +328,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
         }
         top = of_row(top, larger) * a.scale;
         if (__any(top > m + kSlack)) {
-            const float to = fmaxf(m, top), f = m == to ? 1.f : __builtin_amdgcn_exp2f(m - to);
+            const bool up = top > m + kSlack;               // of this row: no other row's scores change it
+            const float to = up ? top : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.f;
             m = to;
             l *= f;
 #pragma unroll

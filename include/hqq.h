@@ -328,19 +328,21 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
  * hqq_cache_write then stores for the tokens to come). q and out: [n_tokens, n_q_heads, head_dim],
  * k and v: [n_tokens, n_kv_heads, head_dim], of type dtype, with strides in elements between tokens
  * and heads (multiples of 8, between tokens of k and v at most 2^22; dimensions contiguous;
- * pointers 16-byte aligned), e.g. slices of one fused projection's output; head_dim 64, 128 or 256; n_q_heads a multiple of n_kv_heads, query
- * head h reads key/value head h / (n_q_heads / n_kv_heads). Sequence b has rows cu_tokens[b] ..
- * cu_tokens[b+1]-1 (device, int32 [n_seqs + 1]), or n_tokens/n_seqs rows each when cu_tokens is
- * NULL. Row i of a sequence sees its rows 0..i:
+ * pointers 16-byte aligned), e.g. slices of one fused projection's output; head_dim 64, 128 or
+ * 256; n_q_heads a multiple of n_kv_heads, query head h reads key/value head
+ * h / (n_q_heads / n_kv_heads). Sequence b has rows cu_tokens[b] .. cu_tokens[b+1]-1 (device, int32
+ * [n_seqs + 1]), or n_tokens/n_seqs rows each when cu_tokens is NULL. Row i of a sequence sees its
+ * rows 0..i:
  *   out_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale * <q_i, k_j>),
- * with scores, sums and the softmax's statistics in binary32, weights rounded to the type where they
- * meet the values, and out rounded from binary32; lse (binary32 [n_tokens, n_q_heads], nullable)
- * gets log(sum_j w_ij). What a row does not see does not change it, infinities and NaN included; a
- * row that sees them in k or q, or whose scores leave binary32's range, is unspecified, one that
- * sees them in v in that dimension. Offsets outside 0..n_tokens count as the nearest of these, and
- * where they fall all rows stay as they were; rows of no sequence always do. n_seqs: 0..4096;
- * n_tokens: 0..2^24; n_kv_heads: 1..1024; n_tokens * n_q_heads at most 2^30. out must not overlap
- * q, k, v or itself. No workspace is needed, nothing is allocated. */
+ * with scores, sums and the softmax's statistics in binary32 (the sums of 2^8 |v_j| must stay in its
+ * range), weights rounded to the type where they meet the values, and out rounded from binary32; lse
+ * (binary32 [n_tokens, n_q_heads], nullable) gets log(sum_j w_ij). What a row does not see does not
+ * change it, infinities and NaN included; a row that sees them in k or q, or whose scores leave
+ * binary32's range, is unspecified, one that sees them in v in that dimension. Offsets outside
+ * 0..n_tokens count as the nearest of these, and where they fall all rows stay as they were; rows of
+ * no sequence always do. n_seqs: 0..4096; n_tokens: 0..2^24; n_kv_heads: 1..1024; n_tokens * n_q_heads
+ * at most 2^30 (and some less with very many sequences and heads: HQQ_ERR_UNSUPPORTED). out must not
+ * overlap q, k, v or itself. No workspace is needed, nothing is allocated. */
 hqq_status hqq_prompt_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride,
                                 const void *k, int64_t k_token_stride, int64_t k_head_stride,
                                 const void *v, int64_t v_token_stride, int64_t v_head_stride,

@@ -243,6 +243,18 @@ def test_the_same_bits_again(H):
         assert torch.equal(H.prompt_attention(q, k, v, cu_tokens=cu), want)
 
 
+def test_rows_do_not_change_each_other(H):
+    """A row has the same bits whatever the other rows' queries are, with others beside it or not."""
+    gen = torch.Generator().manual_seed(7)
+    for dim, hk, per in ((128, 2, 4), (64, 1, 3), (256, 1, 2)):
+        q, k, v = (x.clone() for x in inputs(300, hk * per, hk, dim, F, gen))
+        want = H.prompt_attention(q, k, v)
+        other = q.clone()
+        other[::2] = torch.randn(150, hk * per, dim, generator=gen).half().cuda() * 30
+        assert torch.equal(H.prompt_attention(other, k, v)[1::2], want[1::2])
+        assert torch.equal(H.prompt_attention(q[:131], k[:131], v[:131]), want[:131])
+
+
 def test_the_binding_refuses(H):
     q, k, v = inputs(12, 4, 2, 64, F, torch.Generator())
     cu, out, lse = i32([0, 12]), torch.empty_like(q), torch.empty(12, 4, dtype=torch.float32, device="cuda")
