@@ -10,6 +10,7 @@
 #include "hqq.h"
 #include "hqq_cache_internal.h"
 #include "hqq_internal.h"
+#include "hqq_rotary.h"
 
 namespace hqq {
 namespace {
@@ -21,18 +22,17 @@ struct Tensor {
     const uint16_t *in;
     uint16_t *out;
     int64_t in_ts, in_hs, out_ts, out_hs;
-    int32_t heads;
 };
 
 struct RotaryArgs {
     Tensor x[2];
+    RotaryHeads heads[2];
     const uint64_t *freqs;
     const int32_t *positions;
     float scale;
     int32_t n_tokens, pairs;    // rotary_dim / 2
-    int32_t per_head, units;    // units of a head, of a token
+    int32_t before, units;      // units of a token: the first tensor's, all
     int32_t tokens, parts;      // tokens to a block; blocks to a token
-    int32_t copied;             // dimensions behind those of the pairs
 };
 
 // Cosine and sine of a part of a turn, 2^-32 turns a step: the nearest quarter turn is taken off,
@@ -95,47 +95,20 @@ __device__ __forceinline__ void store16(uint16_t *p, uint4 x)
     *reinterpret_cast<Sixteen *>(p) = Sixteen{x.x, x.y, x.z, x.w};
 }
 
-// A unit is eight pairs, or eight dimensions that are copied; a head ends with units of one, where
-// these do not go into eights. Where it lies: its first numbers, and the second of pairs.
 struct Unit {
     const uint16_t *in;
     uint16_t *out;
-    int d0, d1, pair;           // pair: of the token's cosines and sines, the first; or -1: copied
+    int d0, d1, pair;           // as in RotaryUnit; pair: of the token's cosines and sines
     bool wide;
 };
 template <bool NEIGHBOURS>
 __device__ __forceinline__ Unit unit_of(const RotaryArgs &a, int t0, int j)
 {
-    const unsigned t = (unsigned)j / (unsigned)a.units, of_token = j - t * a.units;
-    unsigned h = of_token / (unsigned)a.per_head;
-    int u = of_token - h * a.per_head;
-    const bool second = h >= (unsigned)a.x[0].heads;
-    const Tensor &x = a.x[second];
-    if (second) h -= a.x[0].heads;
-    Unit r;
-    r.in = x.in + (t0 + (int64_t)t) * x.in_ts + h * x.in_hs;
-    r.out = x.out + (t0 + (int64_t)t) * x.out_ts + h * x.out_hs;
-    // eights that are turned and copied, then ones
-    const int turned8 = a.pairs >> 3, copied8 = a.copied >> 3, turned1 = a.pairs & 7;
-    r.wide = u < turned8 + copied8;
-    bool turn = u < turned8;
-    int first = 8 * u;                                      // pair, or dimension copied
-    if (!r.wide) {
-        u -= turned8 + copied8;
-        turn = u < turned1;
-        first = turn ? 8 * turned8 + u : 8 * copied8 + u - turned1;
-    } else if (!turn) {
-        first -= 8 * turned8;
-    }
-    if (turn) {
-        r.d0 = NEIGHBOURS ? 2 * first : first;
-        r.d1 = NEIGHBOURS ? r.d0 + (r.wide ? 8 : 1) : first + a.pairs;
-        r.pair = t * a.pairs + first;
-    } else {
-        r.d0 = r.d1 = 2 * a.pairs + first;
-        r.pair = -1;
-    }
-    return r;
+    const unsigned t = (unsigned)j / (unsigned)a.units;
+    const RotaryUnit u = rotary_unit<NEIGHBOURS>(a.heads, a.pairs, a.before, j - t * a.units);
+    const Tensor &x = a.x[u.tensor];
+    return Unit{x.in + (t0 + (int64_t)t) * x.in_ts + u.head * x.in_hs, x.out + (t0 + (int64_t)t) * x.out_ts + u.head * x.out_hs,
+                u.d0, u.d1, u.pair < 0 ? -1 : (int)(t * a.pairs) + u.pair, u.wide};
 }
 
 // A block makes the cosines and sines of its tokens once, for all heads, while its first units are on
@@ -242,8 +215,7 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     if (n_tokens < 0 || n_tokens > (1 << 24)) return refuse("n_tokens must be in [0, 2^24]");
     if (n_rows < 0 || n_rows > 2 || (n_rows > 0 && !rows)) return refuse("rows must be one or two tensors");
     RotaryArgs a{};
-    bool rest = false;
-    int heads = 0;
+    int n = 0;                  // tensors with something to turn
     for (int i = 0; i < n_rows; ++i) {
         const hqq_rotary_rows &r = rows[i];
         if (r.n_heads < 0 || r.n_heads > 4096) return refuse("rows: n_heads must be in [0, 4096]");
@@ -257,14 +229,15 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
         if (r.in == r.out) {
             if (strides[0] != strides[2] || strides[1] != strides[3])
                 return refuse("rows: in place, the strides of in and out must be the same");
-        } else {
-            rest = true;
         }
-        a.x[heads > 0] = Tensor{static_cast<const uint16_t *>(r.in), static_cast<uint16_t *>(r.out),
-                                strides[0], strides[1], strides[2], strides[3], r.n_heads};
-        heads += r.n_heads;
+        a.x[n] = Tensor{static_cast<const uint16_t *>(r.in), static_cast<uint16_t *>(r.out),
+                        strides[0], strides[1], strides[2], strides[3]};
+        // in place, the dimensions behind those of the pairs are neither read nor written
+        a.heads[n] = rotary_heads(r.n_heads, rotary_dim / 2, r.in == r.out ? 0 : head_dim - rotary_dim);
+        a.units += r.n_heads * a.heads[n].per_head;
+        if (n++ == 0) a.before = a.units;
     }
-    if (heads == 0 || n_tokens == 0) {
+    if (n == 0) {
         report_error(HQQ_OK, "");
         return HQQ_OK;
     }
@@ -275,9 +248,6 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     a.scale = scale;
     a.n_tokens = (int32_t)n_tokens;
     a.pairs = rotary_dim / 2;
-    a.copied = rest ? head_dim - rotary_dim : 0;
-    a.per_head = a.pairs / 8 + a.pairs % 8 + a.copied / 8 + a.copied % 8;
-    a.units = a.per_head * heads;
     // A unit to a thread; with fewer than a block's in a token, several tokens. (Four to a thread: 16390
     // tokens of 72 heads of 128 107 us and 102 with one; 5000 of 16 heads of 256, a quarter turned, 15.9
     // and 17.3, for the angles are made more often; no difference for 4000 and fewer of the former.)
