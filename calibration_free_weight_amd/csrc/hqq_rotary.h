@@ -61,4 +61,23 @@ HQQ_HD RotaryUnit rotary_unit(const RotaryHeads (&x)[2], int32_t pairs, int32_t 
     return r;
 }
 
+// Whether rows of `width` numbers of n tokens and `heads` heads, these strides apart, share any.
+inline bool rows_meet(int64_t n, int64_t heads, int64_t token_stride, int64_t head_stride, int64_t width)
+{
+    if ((n > 1 && token_stride < width) || (heads > 1 && head_stride < width)) return true;
+    // in order of their tokens, or of their heads: what layouts are as a rule
+    if (n <= 1 || heads <= 1 || token_stride >= (heads - 1) * head_stride + width || head_stride >= (n - 1) * token_stride + width)
+        return false;
+    // else a row of one token and one of another, some heads before it, the nearest two for each number of them
+    const bool by_head = heads <= n;
+    const int64_t few = by_head ? heads : n, many = by_head ? n : heads;
+    const int64_t step = by_head ? head_stride : token_stride, other = by_head ? token_stride : head_stride;
+    for (int64_t i = 1; i < few; ++i) {
+        const int64_t k = i * step / other, rest = i * step - k * other;
+        if ((k < many && rest < width) || (k + 1 < many && other - rest < width)) return true;
+        if (k >= many) break;
+    }
+    return false;
+}
+
 }  // namespace hqq

@@ -230,6 +230,10 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
             if (strides[0] != strides[2] || strides[1] != strides[3])
                 return refuse("rows: in place, the strides of in and out must be the same");
         }
+        // in place, what is not turned may be shared
+        if (rows_meet(n_tokens, r.n_heads, strides[2], strides[3], r.in == r.out ? rotary_dim : head_dim))
+            return refuse("rows: heads and tokens of out must not overlap each other");
+        if (n > 0 && r.out == a.x[0].out) return refuse("rows: the outputs must not overlap");
         a.x[n] = Tensor{static_cast<const uint16_t *>(r.in), static_cast<uint16_t *>(r.out),
                         strides[0], strides[1], strides[2], strides[3]};
         // in place, the dimensions behind those of the pairs are neither read nor written

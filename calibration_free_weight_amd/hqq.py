@@ -679,8 +679,9 @@ def _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, fr
 
 def hqq_rotary(freqs, positions, q, k=None, q_out=None, k_out=None, interleaved=False, scale=1.0, stream=None) -> None:
     """Turn q and k [n_tokens, heads, head_dim] by positions (int32 [n_tokens]) into q_out and k_out,
-    or in place where these are None. freqs (rotary_frequencies) tells by its length how many
-    dimensions are turned; interleaved: pairs are neighbours, else of the two halves."""
+    or in place where these are None; what is written must not overlap (no expanded tensors). freqs
+    (rotary_frequencies) tells by its length how many dimensions are turned; interleaved: pairs are
+    neighbours, else of the two halves."""
     if k is None and k_out is not None:
         raise _bad("k_out without k")
     _rotate(freqs, positions, q, k, q_out, k_out, interleaved, scale, stream, False)

@@ -305,8 +305,9 @@ hqq_status hqq_rotary_frequencies(int rotary_dim, double theta, double factor, i
                                   double low, double high, uint64_t *freqs);
 
 /* One tensor of hqq_rotary: [n_tokens, n_heads, head_dim], strides in elements, dimensions
- * contiguous. out may be in, with the same strides (the other dimensions are then not touched);
- * else it must overlap no input or output of the call. */
+ * contiguous. out may be in, with the same strides (the other dimensions are then not touched, and
+ * may be those of other rows); else it must overlap no input or output of the call. Heads and tokens
+ * of out must not overlap each other (an expanded tensor is refused), nor the two tensors' outputs. */
 typedef struct hqq_rotary_rows {
     const void *in;
     int64_t in_token_stride, in_head_stride;
@@ -317,7 +318,7 @@ typedef struct hqq_rotary_rows {
 
 /* Turn one or two tensors (queries and keys) in one launch. freqs: device, uint64
  * [rotary_dim/2]; positions: device, int32 [n_tokens], any values. rotary_dim is even, at most
- * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24. Any strides and
+ * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24. Any other strides and
  * 2-byte alignment will do; rotary_dim a multiple of 16 is fastest. Nothing is allocated. */
 hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, float scale,
                       const int32_t *positions, int64_t n_tokens, int head_dim, int dtype,

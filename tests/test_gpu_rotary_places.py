@@ -55,3 +55,22 @@ def test_rows_whose_other_dimensions_are_the_next_rows(H, interleaved):
     check(alone, ref)
     check(k_out, reference(freqs.tolist(), p.tolist(), k, interleaved, 1.0))
     assert torch.equal(flat[n * heads * rot:], before[n * heads * rot:])
+
+
+def test_expanded_outputs_are_refused(H):
+    """Rows that lie on each other would be turned once or several times."""
+    freqs, p = H.rotary_frequencies(64), i32([1, 2, 3])
+    q, k = torch.ones(3, 4, 64, dtype=F, device="cuda"), torch.ones(3, 2, 64, dtype=F, device="cuda")
+    one = k[:, :1].expand(3, 2, 64)
+    for args, kw in (((q, one), {}), ((one,), {}), ((k[:1].expand(3, 2, 64),), {}), ((k,), dict(q_out=one)), ((q, k), dict(k_out=one)),
+                     ((q, q), {})):
+        with pytest.raises(H.HQQError, match="overlap"):
+            H.hqq_rotary(freqs, p, *args, **kw)
+    assert (q == 1).all() and (k == 1).all()
+    # inputs may be, and what has one token or head may have any strides
+    want = H.rotary(freqs, p, k)
+    assert torch.equal(H.rotary(freqs, p, one), want)
+    assert torch.equal(H.rotary(freqs, p[:1], one[:1, :1]), want[:1, :1])
+    x = k[:, :1].clone()
+    H.hqq_rotary(freqs, p, torch.as_strided(x, (3, 1, 64), (64, 0, 1)))
+    assert torch.equal(x, want[:, :1])

@@ -2,9 +2,14 @@
 import os
 import subprocess
 
+import pytest
+
+from test_serving_host import H, P, rotary      # noqa: F401 (H is a fixture)
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 DRIVER = r"""
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <vector>
@@ -62,6 +67,17 @@ int main()
         count<false>(s[0], s[1], h, p);
         count<true>(s[0], s[1], h, p);
     }
+    // rows that share a number, against all pairs of them
+    for (int n = 1; n <= 7; ++n) for (int h = 1; h <= 6; ++h) for (int w : {1, 2, 3, 5})
+        for (int ts = 0; ts < 24; ++ts) for (int hs = 0; hs < 24; ++hs) {
+            bool meet = false;
+            for (int i = 0; i < n * h; ++i) for (int j = 0; j < i; ++j)
+                meet = meet || std::abs((i / h - j / h) * ts + (i % h - j % h) * hs) < w;
+            need(rows_meet(n, h, ts, hs, w) == meet, "rows that meet");
+        }
+    const int64_t far = int64_t(1) << 36;
+    need(!rows_meet(1 << 24, 4096, far, 1024, 1024) && !rows_meet(1 << 24, 4096, 1024, far, 1024), "long strides");
+    need(rows_meet(1 << 24, 4096, far, far, 1024) && rows_meet(1 << 24, 4096, 1024, 1024 << 10, 1024), "long strides that meet");
     std::puts("ok");
 }
 """
@@ -77,3 +93,16 @@ def test_what_a_call_turns_and_copies(tmp_path):
                            "-fno-sanitize-recover=all", "-I", inc, "-o", str(exe), str(src)])
     out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert out.returncode == 0 and out.stdout.strip() == "ok", out.stdout + out.stderr[-2000:]
+
+
+OVER = dict(out=P)          # in place, of 5 tokens and 4 heads of 128, 64 of them turned
+
+
+@pytest.mark.parametrize("rows", [
+    [dict(OVER, in_token_stride=0, out_token_stride=0)], [dict(OVER, in_head_stride=0, out_head_stride=0)],
+    [dict(OVER, in_head_stride=63, out_head_stride=63)], [dict(OVER, in_token_stride=63, out_token_stride=63)],
+    [dict(OVER, in_token_stride=192, out_token_stride=192)],                # a token's second head and the next one's first
+    [dict(out_token_stride=0)], [dict(out_head_stride=0)], [dict(out_head_stride=127)], [dict(out_token_stride=511)],
+    [{}, dict(in_=5 * P, out=4 * P, out_head_stride=0)], [dict(OVER), dict(OVER)], [{}, {}]], ids=str)
+def test_outputs_that_overlap_are_refused(H, rows):     # noqa: F811
+    assert rotary(H, rows=rows) == H.HQQ_ERR_ARG and "overlap" in H.hqq_last_error()
