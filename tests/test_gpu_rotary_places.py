@@ -61,8 +61,8 @@ def test_expanded_outputs_are_refused(H):
     """Rows that lie on each other would be turned once or several times."""
     freqs, p = H.rotary_frequencies(64), i32([1, 2, 3])
     q, k = torch.ones(3, 4, 64, dtype=F, device="cuda"), torch.ones(3, 2, 64, dtype=F, device="cuda")
-    one = k[:, :1].expand(3, 2, 64)
-    for args, kw in (((q, one), {}), ((one,), {}), ((k[:1].expand(3, 2, 64),), {}), ((k,), dict(q_out=one)), ((q, k), dict(k_out=one)),
+    one, other = k[:, :1].expand(3, 2, 64), torch.ones(3, 1, 64, dtype=F, device="cuda").expand(3, 2, 64)
+    for args, kw in (((q, one), {}), ((one,), {}), ((k[:1].expand(3, 2, 64),), {}), ((k,), dict(q_out=other)), ((q, k), dict(k_out=other)),
                      ((q, q), {})):
         with pytest.raises(H.HQQError, match="overlap"):
             H.hqq_rotary(freqs, p, *args, **kw)
