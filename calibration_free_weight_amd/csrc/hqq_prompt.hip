@@ -35,8 +35,14 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 constexpr int kAhead = 2;         // fragments asked for before they are used
 constexpr int64_t kMaxKeyStride = 1 << 22;
 constexpr float kLog2e = 1.44269504088896341f;
-// How far a score (to base 2) may lie above the maximum that weights are taken from.
+// How far a score (to base 2) may lie above a row's maximum before what is taken off all scores moves,
+// and how far below the maximum that then lies. A binary16 weight has 24 powers of two below 1 and 15
+// above: from 2^7 for the largest weight, 2^15 with the slack, to 2^-25, where one is lost from the
+// products that the sum counts, there are 32; from 1 there would be 25, and a long prompt's many small
+// weights beside a large one went short by up to 2^-25 each. A bfloat16 weight has binary32's exponents.
 constexpr float kSlack = 8.f;
+template <typename T>
+constexpr float kBelow = Types<T>::kBf16 ? 0.f : 7.f;
 
 struct PromptArgs {
     const uint16_t *q, *k, *v;
@@ -314,8 +320,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
         const float p = s[e / 16][e % 16], q = s[e / 16][e % 16 + 1];
         return e == 0 ? larger(p, q) : larger(larger(top, p), q);
     };
-    // Moves m where the scores go beyond it by more than the slack; where some row does not see some
-    // key, takes these scores out first.
+    // Moves m, kBelow below the largest score, where the scores go beyond that by more than the slack;
+    // where some row does not see some key, takes these scores out first.
     const auto look = [&](f32x16 (&s)[KB], float top, int step) {
         if (__builtin_expect((step + 1) * kKeys - 1 > wave_first, 0)) {
             int seen = tok - step * kKeys - 4 * half;
@@ -327,9 +333,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
             for (int e = 0; e < 16 * KB; e += 2) top = larger_of(top, s, e);
         }
         top = of_row(top, larger) * a.scale;
-        if (__any(top > m + kSlack)) {
-            const bool up = top > m + kSlack;               // of this row: no other row's scores change it
-            const float to = up ? top : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.f;
+        if (__any(top > m + (kSlack + kBelow<T>))) {
+            const bool up = top > m + (kSlack + kBelow<T>); // of this row: no other row's scores change it
+            const float to = up ? top - kBelow<T> : m, f = up ? __builtin_amdgcn_exp2f(m - to) : 1.f;
             m = to;
             l *= f;
 #pragma unroll

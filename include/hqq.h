@@ -336,8 +336,9 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
  * rows 0..i:
  *   out_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = exp(scale * <q_i, k_j>),
  * with scores, sums and the softmax's statistics in binary32 (the sums of 2^8 |v_j| must stay in its
- * range), weights rounded to the type where they meet the values, and out rounded from binary32; lse
- * (binary32 [n_tokens, n_q_heads], nullable) gets log(sum_j w_ij). What a row does not see does not
+ * range), weights rounded to the type where they meet the values (with binary16 by up to 2^-32 of the
+ * row's largest weight, where that is more), and out rounded from binary32; lse (binary32
+ * [n_tokens, n_q_heads], nullable) gets log(sum_j w_ij). What a row does not see does not
  * change it, infinities and NaN included; a row that sees them in k or q, or whose scores leave
  * binary32's range, is unspecified, one that sees them in v in that dimension. Offsets outside
  * 0..n_tokens count as the nearest of these, and where they fall all rows stay as they were; rows of
