@@ -121,6 +121,25 @@ bool alike(const hqq_cache &a, const hqq_cache &b)
            a.nbits == b.nbits && a.group_size == b.group_size && a.dtype == b.dtype;
 }
 
+// Whether any of the caches' buffers overlap: moved twice, a token would go on to where the first move
+// found another. In order of their addresses, whose lowest bit tells grids from codes, each has to end
+// where the next one begins or before. (128 buffers: 1 us.)
+bool overlap(const hqq_cache *caches, int n)
+{
+    const uint64_t tokens = (uint64_t)caches->n_pages * caches->n_heads * caches->page_size;
+    const uint64_t bytes[2] = {tokens * caches->head_dim * caches->nbits / 8, tokens * (caches->head_dim / caches->group_size) * 4};
+    uint64_t at[4 * kMaxCaches];
+    for (int i = 0; i < n; ++i) {
+        const hqq_cache &c = caches[i];
+        const void *const part[4] = {c.k_codes, c.v_codes, c.k_meta, c.v_meta};
+        for (int k = 0; k < 4; ++k) at[4 * i + k] = reinterpret_cast<uintptr_t>(part[k]) | (unsigned)k >> 1;
+    }
+    std::sort(at, at + 4 * n);
+    for (int i = 1; i < 4 * n; ++i)
+        if ((at[i] & ~uint64_t(1)) - (at[i - 1] & ~uint64_t(1)) < bytes[at[i - 1] & 1]) return true;
+    return false;
+}
+
 // ---- attention --------------------------------------------------------------------------------
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -352,16 +371,11 @@ hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs 
                           int max_kept, int32_t *lens_out, void *stream)
 {
     if (n_caches < 1 || n_caches > kMaxCaches || !caches) return refuse("caches must be 1 to 1024 caches");
-    const void *codes[kMaxCaches];
     for (int i = 0; i < n_caches; ++i) {
         const hqq_status st = check_cache(caches + i);
         if (st != HQQ_OK) return st;
         if (!alike(caches[0], caches[i])) return refuse("the caches of a call must have the same sizes and type");
-        codes[i] = caches[i].k_codes;
     }
-    // moved twice, a token would go on to where the first move found another
-    std::sort(codes, codes + n_caches);
-    if (std::adjacent_find(codes, codes + n_caches) != codes + n_caches) return refuse("the caches of a call must differ");
     const hqq_status st = check_seqs(caches, seqs);
     if (st != HQQ_OK) return st;
     if (max_kept < 0 || max_kept > (1 << 24)) return refuse("max_kept must be in [0, 2^24]");
@@ -371,6 +385,7 @@ hqq_status hqq_cache_keep(const hqq_cache *caches, int n_caches, const hqq_seqs 
         return refuse("lens must be non-null, and lens, cu_tokens and lens_out 4-byte aligned");
     if (lens_out && lens_out < seqs->lens + seqs->n_seqs && seqs->lens < lens_out + seqs->n_seqs)
         return refuse("lens_out must not overlap lens");
+    if (overlap(caches, n_caches)) return refuse("the caches of a call must differ: their buffers must not overlap");
     hqq::KeepArgs a{view_of(caches, seqs), kept, lens_out, max_kept, caches->n_heads, caches->head_dim / caches->group_size, {}};
     hipError_t e = hipSuccess;
     for (int first = 0; first < n_caches && e == hipSuccess; first += hqq::kKeepLayers) {

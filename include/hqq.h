@@ -485,7 +485,7 @@ size_t hqq_cache_attention_workspace(const hqq_cache *cache, const hqq_seqs *seq
                                      int n_q_heads, int64_t prefix_len);
 
 /* Keep the accepted ones of the call's tokens, in the caches of all layers (host array of
- * n_caches, 1..1024, all different, with the same sizes, type and table). kept (device, int32
+ * n_caches, 1..1024, whose buffers do not overlap, with the same sizes, type and table). kept (device, int32
  * [n_seqs, max_kept]) lists for each sequence the accepted rows by their number among its n_b
  * rows, ascending; a list ends with its row of kept, or before the first entry that is negative,
  * n_b or more, or not above the one before it. With m_b entries, token kept[b][i] moves to position
