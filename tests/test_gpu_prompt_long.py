@@ -75,3 +75,31 @@ def test_long_prompts(H, dtype, dim, hk, per, n):
     for i in (n - 1, n // 2, 8191, 4097, 1000, 31, 0):
         check_row(out, lse, q, k, v, i, 0, dim ** -0.5)
     assert math.isfinite(float(out.float().sum()))
+
+
+@pytest.mark.parametrize("dtype,dim,per,mean", [(F, 128, 4, 2100), (B, 128, 5, 2300), (B, 256, 1, 4200)])
+def test_blocks_of_256_rows_and_many_sequences(H, dtype, dim, per, mean):
+    """More sequences than a wave has lanes, some empty and one six times the mean: in blocks of 256
+    rows, like the two halves of the batch by themselves, whose sequences fit a wave."""
+    gen = torch.Generator().manual_seed(dim + per)
+    lens = [0, 1, 6 * mean, 255, 256, 257] + [mean + 7 * (i % 9 - 4) for i in range(64)] + [2 * mean, 0]
+    assert len(lens) == 72
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    n = cu[-1]
+    x = torch.randn(n + 3, per + 2, dim, generator=gen, dtype=torch.float32).to(dtype).cuda()
+    q, k, v = x[:, :per], x[:, per:per + 1], x[:, per + 1:]
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")
+    out = torch.full((n + 3, per, dim), 11.0, dtype=dtype, device="cuda")
+    lse = torch.full((n + 3, per), 13.0, dtype=torch.float32, device="cuda")
+    H.hqq_prompt_attention(q, k, v, out, cu_tokens=i32(cu), lse=lse)
+    assert (out[n:] == 11).all() and (lse[n:] == 13).all()
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        for row in {hi - 1, (lo + hi) // 2, lo} if i % 5 < 2 and hi > lo else ():
+            check_row(out, lse, q, k, v, row, lo, dim ** -0.5)
+    for lo, hi in ((0, 36), (36, 72)):          # the same bits: a step has as many keys
+        part = slice(cu[lo], cu[hi])
+        assert sum(lens[lo:hi]) // 36 >= (2048 if dim == 128 else 4096)
+        got = H.prompt_attention(q[part], k[part], v[part], cu_tokens=i32([c - cu[lo] for c in cu[lo:hi + 1]]))
+        assert torch.equal(got, out[part])
