@@ -16,7 +16,6 @@ namespace hqq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 2048;         // of a block's tokens: 16 KB of cosines and sines
 
 struct Tensor {
     const uint16_t *in;
@@ -111,52 +110,46 @@ __device__ __forceinline__ Unit unit_of(const RotaryArgs &a, int t0, int j)
                 u.d0, u.d1, u.pair < 0 ? -1 : (int)(t * a.pairs) + u.pair, u.wide};
 }
 
-// A block makes the cosines and sines of its tokens once, for all heads, while its first units are on
-// their way. Bound by memory: 16390 tokens of 72 heads of 128, 604 MB: 102 us, 5.9 TB/s (part of it from
-// the last level's cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.3 us, 3.2 TB/s;
-// a token 2.1 us, the launch and two loads that wait for each other.
+// A thread has one unit, whose numbers are on their way while the block makes the cosines and sines of its
+// tokens (of a token with more units than a block has threads each of its blocks makes them). Bound by
+// memory: 16390 tokens of 72 heads of 128, 604 MB: 102 us, 5.9 TB/s (part of it from the last level's
+// cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.8 us, 3.0 TB/s; a token 2.5 us,
+// the launch and two loads that wait for each other.
 template <typename T, bool NEIGHBOURS>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
 {
-    extern __shared__ float2 cs[];      // [tokens][pairs]
+    extern __shared__ float2 cs[];      // [tokens][pairs]; a unit has eight pairs at most, so 2048 of a block's
     const int t0 = (int)(blockIdx.x / (unsigned)a.parts) * a.tokens, part = (int)(blockIdx.x % (unsigned)a.parts);
-    const int tokens = min(a.tokens, a.n_tokens - t0), all = tokens * a.units;
-    int j = part * kThreads + threadIdx.x;
-    Unit x{};
-    uint4 lo{}, hi{};
-    const auto load = [&] {
-        x = unit_of<NEIGHBOURS>(a, t0, j);
-        if (__builtin_expect(x.wide, 1)) {
-            lo = load16(x.in + x.d0);
-            hi = load16(x.in + x.d1);
-        } else {
-            lo.x = x.in[x.d0];
-            hi.x = x.in[x.d1];
-        }
-    };
-    if (j < all) load();
+    const int tokens = min(a.tokens, a.n_tokens - t0);
+    const int j = part * kThreads + threadIdx.x, last = tokens * a.units - 1;
+    const Unit x = unit_of<NEIGHBOURS>(a, t0, min(j, last));    // a thread without one reads the last and leaves
+    uint4 lo, hi;
+    if (__builtin_expect(x.wide, 1)) {
+        lo = load16(x.in + x.d0);
+        hi = load16(x.in + x.d1);
+    } else {
+        lo.x = x.in[x.d0];
+        hi.x = x.in[x.d1];
+    }
     for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
         const unsigned t = (unsigned)i / (unsigned)a.pairs, k = i - t * a.pairs;
         const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + t] * a.freqs[k];
         cs[i] = cos_sin((uint32_t)((turns + 0x80000000u) >> 32), a.scale);
     }
     __syncthreads();
-    while (j < all) {
-        if (__builtin_expect(x.wide, 1)) {
-            if (x.pair >= 0) {
-                turn8<T, NEIGHBOURS>(lo, hi, cs + x.pair);
-                store16(x.out + x.d1, hi);
-            }
-            store16(x.out + x.d0, lo);
-        } else {
-            if (x.pair >= 0) {
-                turn<T>(to_f32<T>(lo.x), to_f32<T>(hi.x), cs[x.pair], lo.x, hi.x);
-                x.out[x.d1] = (uint16_t)hi.x;
-            }
-            x.out[x.d0] = (uint16_t)lo.x;
+    if (j > last) return;
+    if (__builtin_expect(x.wide, 1)) {
+        if (x.pair >= 0) {
+            turn8<T, NEIGHBOURS>(lo, hi, cs + x.pair);
+            store16(x.out + x.d1, hi);
         }
-        j += a.parts * kThreads;
-        if (j < all) load();
+        store16(x.out + x.d0, lo);
+    } else {
+        if (x.pair >= 0) {
+            turn<T>(to_f32<T>(lo.x), to_f32<T>(hi.x), cs[x.pair], lo.x, hi.x);
+            x.out[x.d1] = (uint16_t)hi.x;
+        }
+        x.out[x.d0] = (uint16_t)lo.x;
     }
 }
 
@@ -255,8 +248,7 @@ hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, fl
     // A unit to a thread; with fewer than a block's in a token, several tokens. (Four to a thread: 16390
     // tokens of 72 heads of 128 107 us and 102 with one; 5000 of 16 heads of 256, a quarter turned, 15.9
     // and 17.3, for the angles are made more often; no difference for 4000 and fewer of the former.)
-    a.tokens = kThreads / a.units < kMaxPairs / a.pairs ? kThreads / a.units : kMaxPairs / a.pairs;
-    if (a.tokens < 1) a.tokens = 1;
+    a.tokens = kThreads / a.units > 1 ? kThreads / a.units : 1;
     if (a.tokens > a.n_tokens) a.tokens = a.n_tokens;
     a.parts = a.tokens > 1 ? 1 : (a.units + kThreads - 1) / kThreads;
     const int64_t blocks = (n_tokens + a.tokens - 1) / a.tokens * a.parts;
