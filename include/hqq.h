@@ -318,8 +318,10 @@ typedef struct hqq_rotary_rows {
 
 /* Turn one or two tensors (queries and keys) in one launch. freqs: device, uint64
  * [rotary_dim/2]; positions: device, int32 [n_tokens], any values. rotary_dim is even, at most
- * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24. Any other strides and
- * 2-byte alignment will do; rotary_dim a multiple of 16 is fastest. Nothing is allocated. */
+ * head_dim, and that at most 1024; dtype is an hqq_dtype; n_tokens at most 2^24, and where a token
+ * has t > 128 units of eight pairs, or of eight others that are copied, at most (2^24 - 1) / ceil(t / 256)
+ * (else HQQ_ERR_UNSUPPORTED). Any other strides and 2-byte alignment will do; rotary_dim a multiple of
+ * 16 is fastest. Nothing is allocated. */
 hqq_status hqq_rotary(const uint64_t *freqs, int rotary_dim, int interleaved, float scale,
                       const int32_t *positions, int64_t n_tokens, int head_dim, int dtype,
                       const hqq_rotary_rows *rows, int n_rows, void *stream);

@@ -106,3 +106,10 @@ OVER = dict(out=P)          # in place, of 5 tokens and 4 heads of 128, 64 of th
     [{}, dict(in_=5 * P, out=4 * P, out_head_stride=0)], [dict(OVER), dict(OVER)], [{}, {}]], ids=str)
 def test_outputs_that_overlap_are_refused(H, rows):     # noqa: F811
     assert rotary(H, rows=rows) == H.HQQ_ERR_ARG and "overlap" in H.hqq_last_error()
+
+
+def test_more_rows_than_a_launch_takes(H):      # noqa: F811
+    """Heads of 64 that are turned in place have four units: 64 of them 256, 33 of them 132."""
+    rows = lambda heads: [dict(out=P, in_token_stride=1 << 20, out_token_stride=1 << 20, n_heads=heads)]
+    for heads, n in ((64, 1 << 24), (33, 1 << 24), (65, 1 << 23), (128, 1 << 23), (4096, 1 << 18)):
+        assert rotary(H, rows=rows(heads), n_tokens=n) == H.HQQ_ERR_UNSUPPORTED, heads
