@@ -495,20 +495,29 @@ hipError_t launch_tiles(const PromptArgs &a, hipStream_t stream)
 // Blocks of 128 rows that go 32 keys a step, two to a CU, or of 256 rows and with heads of 128 64 keys,
 // one to a CU, which fetch a key for twice the rows and meet half as often, but begin and end alone.
 // Measured in us, of 128 and of 256 rows (sequences x tokens, query heads / key heads), heads of 128:
-//   1 x 8190, 64/8    1062   991      1 x 2048, 32/32   56    62      2 x 4096, 32/32   296   285
-//   1 x 4096, 32/8     155   137      1 x 8190, 8/8    183   198      3 x 3000, 40/40   339   348
-//   1 x 2048, 64/8      94    88      16 x 1024, 32/8  201   225      2 x 2048, 40/40   113   116
-//   4 x 2048, 16/4      87    79      64 x 512, 32/8   324   343      8 x 2048, 32/8    319   325
+//   1 x 8190, 64/8    1072   995      2 x 4096, 32/32   298   299      8 x 2048, 32/8    322   321
+//   1 x 4096, 32/8     155   136      2 x 2048, 40/40   115   117      4 x 2048, 64/8    309   316
+//   2 x 2048, 32/8      87    79      4 x 1536, 32/8     96    99      16 x 1536, 32/8   388   401
+//   4 x 3000, 32/8     311   304      4 x 2048, 32/32   171   176      1 x 8190, 32/32   551   521
 // and of 256:
-//   1 x 8190, 16/4     757   718      1 x 4096, 16/4   215   195      8 x 2048, 16/4    441   443
-//   1 x 16384, 8/2    1480  1391      1 x 1000, 16/4    33    41      4 x 1500..2047, 16/4   173   181
+//   1 x 8190, 16/4     739   696      1 x 4096, 16/4    209   187      2 x 3000, 16/4    221   220
+//   8 x 2048, 16/4     431   434      8 x 2048, 8/8     225   238      8 x 3000, 8/8     472   484
 // so the wide ones have long sequences (the rows of one head cover fewer tokens the more heads share
-// it, and a tile's end wastes less) and two blocks at least to a CU. (Heads of 64: 599 and 616 at 1 x
-// 8190, 64/8.)
+// it, and a tile's end wastes less) and two blocks at least to a CU. And where keys and values are more
+// than the last level's cache holds, 256 MB, each block fetches them from memory, and sequences need not
+// be long:
+//   16 x 2048, 32/32  1048   815      64 x 512, 32/32   460   410      64 x 1024, 64/8  1857  1747
+//   16 x 3000, 40/40  2724  2031      32 x 1024, 32/32  654   537      128 x 1536, 32/8 5087  3774
+//   400 x 128, 32/32   534   679      200 x 300, 40/40 1058  1182      8 x 1536, 40/40   298   303 (251 MB)
+//   of 256: 16 x 2048, 16/16   1165  1038      64 x 512, 16/16   498   494
+// Lengths are known by their mean alone: one of 8190 among 31 of 100, 32/8, has small blocks (550 us,
+// wide ones 519). (Heads of 64: 599 and 616 at 1 x 8190, 64/8.)
 bool wide_blocks(const PromptArgs &a, int dim)
 {
     const int64_t blocks = (int64_t)a.s.n_tokens * a.per * a.heads / 256 * (dim / 128);
-    return blocks >= 512 && a.s.n_tokens / a.s.n_seqs >= (dim == 128 && a.per >= 4 ? 2048 : 4096);
+    const int64_t bytes = (int64_t)a.s.n_tokens * a.heads * dim * 4;
+    const int mean = a.s.n_tokens / a.s.n_seqs;
+    return blocks >= 512 && (mean >= (dim == 128 && a.per >= 4 ? 2048 : 4096) || (bytes >= 1 << 28 && mean >= 512));
 }
 
 // Heads of 256 have their outputs' dimensions in two blocks, each of which makes all scores: half as

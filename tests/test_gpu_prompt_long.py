@@ -103,3 +103,25 @@ def test_blocks_of_256_rows_and_many_sequences(H, dtype, dim, per, mean):
         assert sum(lens[lo:hi]) // 36 >= (2048 if dim == 128 else 4096)
         got = H.prompt_attention(q[part], k[part], v[part], cu_tokens=i32([c - cu[lo] for c in cu[lo:hi + 1]]))
         assert torch.equal(got, out[part])
+
+
+@pytest.mark.parametrize("dtype,dim,hk,per,lens", [(F, 128, 32, 1, [520] * 24 + [900, 1, 0, 1300] * 8), (B, 256, 16, 2, [640, 515] * 16),
+                                                   (B, 128, 16, 4, [600] * 80)])
+def test_keys_and_values_beyond_the_caches(H, dtype, dim, hk, per, lens):
+    """Medium sequences whose keys and values are more than 256 MB: some rows of some heads."""
+    gen = torch.Generator().manual_seed(dim + hk)
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    n = cu[-1]
+    assert n * hk * dim * 4 >= 1 << 28 and n // len(lens) >= 512
+    x = torch.randn(n, hk * (per + 2), dim, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(dtype)
+    q, k, v = x[:, :hk * per], x[:, hk * per:hk * (per + 1)], x[:, hk * (per + 1):]
+    lse = torch.empty(n, hk * per, dtype=torch.float32, device="cuda")
+    out = H.prompt_attention(q, k, v, cu_tokens=torch.tensor(cu, dtype=torch.int32, device="cuda"), lse=lse)
+    for i, (lo, hi) in enumerate(zip(cu, cu[1:])):
+        for row in {hi - 1, (lo + hi) // 2, lo} if hi > lo else ():
+            h = int(torch.randint(0, hk, (1,), generator=gen))
+            mine = slice(h * per, h * per + per)
+            check_row(out[:, mine], lse[:, mine], q[:, mine], k[:, h:h + 1], v[:, h:h + 1], row, lo, dim ** -0.5)
+    assert torch.isfinite(out).all()
