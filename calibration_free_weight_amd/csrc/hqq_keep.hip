@@ -7,13 +7,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A sixteenth of a token's codes. Vectors, which stay in registers: of an array of four words the
+// compiler keeps two in LDS on their way.
 template <int BYTES>
 struct Piece {
-    uint32_t w[BYTES / 4];
-} __attribute__((aligned(BYTES)));
+    typedef uint32_t Type __attribute__((ext_vector_type(BYTES / 4)));
+};
 template <>
 struct Piece<2> {
-    uint16_t w[1];
+    using Type = uint16_t;
+};
+template <>
+struct Piece<4> {
+    using Type = uint32_t;
 };
 
 // A wave has one head of one sequence in one layer. A row of 16 lanes moves a token: lane u has the
@@ -26,6 +32,7 @@ struct Piece<2> {
 template <int S>                // bytes of a sixteenth of a token's codes
 __global__ __launch_bounds__(kThreads) void keep_kernel(KeepArgs a)
 {
+    using Code = typename Piece<S>::Type;
     const int lane = threadIdx.x & 63, u = lane & 15;
     const unsigned wave = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + threadIdx.x / 64);
     const unsigned b = wave / (unsigned)a.heads, h = wave - b * a.heads;
@@ -54,17 +61,17 @@ __global__ __launch_bounds__(kThreads) void keep_kernel(KeepArgs a)
         const int k = k0 + lane / 16, j = k < m ? kept[k] : k;
         const int64_t from = j != k ? slot(first + j) : -1, to = j != k ? slot(first + k) : -1;
         const bool move = from >= 0 && to >= 0;
-        Piece<S> key, value;
+        Code key{}, value{};
         uint32_t word = 0;
         if (move) {
-            key = *reinterpret_cast<const Piece<S> *>(layer[0] + (from * 16 + u) * S);
-            value = *reinterpret_cast<const Piece<S> *>(layer[1] + value_at(from));
+            key = *reinterpret_cast<const Code *>(layer[0] + (from * 16 + u) * S);
+            value = *reinterpret_cast<const Code *>(layer[1] + value_at(from));
             if (grid) word = meta[from * a.groups + (u & 7)];
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // a place that is written may have been another lane's to read
         if (move) {
-            *reinterpret_cast<Piece<S> *>(layer[0] + (to * 16 + u) * S) = key;
-            *reinterpret_cast<Piece<S> *>(layer[1] + value_at(to)) = value;
+            *reinterpret_cast<Code *>(layer[0] + (to * 16 + u) * S) = key;
+            *reinterpret_cast<Code *>(layer[1] + value_at(to)) = value;
             if (grid) meta[to * a.groups + (u & 7)] = word;
         }
     }

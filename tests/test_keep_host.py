@@ -1,4 +1,8 @@
 """Caches that share memory, as hqq_cache_keep refuses them (no GPU needed)."""
+import os
+import re
+import subprocess
+
 import pytest
 
 from test_cache_host import cache, seqs
@@ -32,3 +36,16 @@ def test_caches_that_share_a_buffer_are_refused(H, part):       # noqa: F811
     many = [cache(H, **apart((i + 1) << 20)) for i in range(900)]
     bad = dict(apart(1000 << 20), **{part: (500 << 20) + 32})
     assert keep(H, many + [cache(H, **bad)], seqs(H)) == H.HQQ_ERR_ARG and "overlap" in H.hqq_last_error()
+
+
+def test_moved_codes_stay_in_registers(tmp_path):
+    """No instance of the kernel takes LDS or scratch memory."""
+    from calibration_free_weight_amd import build as hb
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not found")
+    out = tmp_path / "keep.s"
+    subprocess.check_call([hipcc, *hb.HIPCC_FLAGS, "-w", "--offload-device-only", "-S", "-I", os.path.join(hb.ROOT, "include"),
+                           "-I", os.path.join(hb.PKG, "csrc"), "-o", str(out), os.path.join(hb.PKG, "csrc", "hqq_keep.hip")])
+    sizes = re.findall(r"\.(?:group|private)_segment_fixed_size:\s+(\d+)", out.read_text())
+    assert len(sizes) == 8 and set(sizes) == {"0"}
