@@ -27,8 +27,8 @@ struct Piece<4> {
 // of values. A list ascends, so number k comes from place k or behind: four tokens at a time are
 // read, then written, and no token that is still to be read lies where one has been written.
 // Bound by latency: loads that wait for each other (lengths and list, pages, codes), then stores. 5 of
-// 26 tokens in 32 layers of 8 heads of 128, 4 bits: 4.4 us; of 64 sequences 1 to 7 of 32, 16 layers, 8
-// bits, 14 MB: 8.6 us, 1.6 TB/s (eight or sixteen tokens at a time take as long).
+// 26 tokens in 32 layers of 8 heads of 128, 4 bits: 4.6 us; of 64 sequences 1 to 7 of 32, 16 layers, 8
+// bits, 14 MB: 9.1 us, 1.5 TB/s (eight or sixteen tokens at a time take as long).
 template <int S>                // bytes of a sixteenth of a token's codes
 __global__ __launch_bounds__(kThreads) void keep_kernel(KeepArgs a)
 {

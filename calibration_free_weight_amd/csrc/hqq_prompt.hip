@@ -353,7 +353,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void prompt_kernel(PromptArgs a)
         constexpr int kPairs = 8 * KB, kFirst = 2;
         constexpr int kBeside = (D == 64 ? kPairs / 2 : D == 128 ? kPairs * 5 / 8 : kPairs) - kFirst;
         u32x4 pf[2 * KB], kf[kAhead + 1], vf[kAhead + 1];
-        const auto weigh = [&](int from, int to) {          // pairs of weights, four for 16 keys
+        // Pairs of weights, four for 16 keys. Where it meets the values a weight has the type's bits, for a
+        // matrix instruction takes one type on both sides: the rest of each in a second product would
+        // be half as many matrix instructions more, of which long prompts are bound. The sum counts it
+        // as it was, for lse is made of it. Errors against 64 bits, of the outputs' size: 2.3e-4 at 16 x
+        // 1..1021, binary16, and 1.8e-3 at 4 x 1500..2047, bfloat16; 2.0e-4 and 1.6e-3 are the outputs' own
+        // rounding.
+        const auto weigh = [&](int from, int to) {
 #pragma unroll
             for (int i = from; i < to; ++i) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[i / 8][i % 8 * 2], a.scale, -m));

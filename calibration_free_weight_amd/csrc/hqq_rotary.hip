@@ -112,8 +112,8 @@ __device__ __forceinline__ Unit unit_of(const RotaryArgs &a, int t0, int j)
 
 // A thread has one unit, whose numbers are on their way while the block makes the cosines and sines of its
 // tokens (of a token with more units than a block has threads each of its blocks makes them). Bound by
-// memory: 16390 tokens of 72 heads of 128, 604 MB: 102 us, 5.9 TB/s (part of it from the last level's
-// cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.8 us, 3.0 TB/s; a token 2.5 us,
+// memory: 16390 tokens of 72 heads of 128, 604 MB: 101 us, 6.0 TB/s (part of it from the last level's
+// cache; a copy of 4 GB reaches 5.0). 1000 tokens of 80 heads of 64: 6.8 us, 3.0 TB/s; a token 2.7 us,
 // the launch and two loads that wait for each other.
 template <typename T, bool NEIGHBOURS>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)

@@ -542,7 +542,8 @@ def hqq_cache_attention_tree(cache, table, lens, tree, q, out, lse=None, scale=N
 
 def hqq_cache_keep(caches, table, lens, kept, n_tokens, lens_out=None, cu_tokens=None, stream=None) -> None:
     """Move the accepted tokens of the last call (its n_tokens rows are the last tokens of their
-    sequences) behind what was there before it, in `caches`, one cache or the list of all layers'.
+    sequences) behind what was there before it, in `caches`, one cache or the list of all layers', which
+    share no memory.
     kept: int32 [n_seqs, max_kept], for each sequence the accepted rows by their number, ascending,
     with -1 behind the last. lens_out (int32 [n_seqs], apart from lens) gets the new lengths."""
     T = _torch or _th()
