@@ -731,7 +731,7 @@ def hqq_prompt_attention(q, k, v, out, cu_tokens=None, n_seqs=1, lse=None, scale
     """out = causal attention of packed sequences over themselves: q and out [n_tokens, n_q_heads,
     head_dim], k and v [n_tokens, n_kv_heads, head_dim]. cu_tokens (int32 [n_seqs + 1]): where the
     sequences begin and end; without it they are n_seqs of the same length. scale: head_dim ** -0.5
-    unless given."""
+    unless given. out must not overlap q, k, v or itself."""
     if out is None:
         raise _bad("out must be [n_tokens, n_q_heads, head_dim]")
     _prompt(q, k, v, out, cu_tokens, n_seqs, lse, scale, stream)
